@@ -32,7 +32,9 @@ __all__ = ["coo_from_lookups", "csr_from_coo", "csr_from_lookups", "csr_to_coo",
            "set_step_events",
            "CooGradient",
            "CsrGradient", "SparseAdam", "SparseSgd", "SparseOptError", "TRUSTED", "VALIDATE",
-           "read_rows", "HostArray"]
+           "read_rows", "HostArray",
+           "layer_norm_forward", "layer_norm_backward", "layer_norm_backward_workspace_size",
+           "LayerNorm", "newton_schulz", "newton_schulz_workspace_size", "muon_step", "Muon"]
 
 
 def _stream(stream) -> int:
@@ -576,3 +578,9 @@ class SparseSgd:
     def step_lookups(self, ids: torch.Tensor, vals: torch.Tensor, **kw):
         """One step from raw lookups of full rows; as SparseAdam.step_lookups."""
         return sparse_step_from_lookups(self.handle, ids, vals, **kw)
+
+
+# The dense operators, which use the helpers above.
+from .dense import (LayerNorm, Muon, layer_norm_backward,  # noqa: E402
+                    layer_norm_backward_workspace_size, layer_norm_forward, muon_step,
+                    newton_schulz, newton_schulz_workspace_size)

@@ -24,6 +24,7 @@ KIND_ADAM, KIND_SGD = 0, 1
 MODE_LAZY, MODE_DORMANCY = 0, 1
 WD_L2, WD_DECOUPLED = 0, 1
 FORMAT_COO, FORMAT_CSR = 0, 1
+DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
 
 
 class AdamConfig(C.Structure):
@@ -50,6 +51,15 @@ class Csr(C.Structure):
 
 class Grad(C.Structure):
     _fields_ = [("format", C.c_int32), ("coo", Coo), ("csr", Csr)]
+
+
+class NsConfig(C.Structure):
+    _fields_ = [("coef", C.c_double * 3), ("eps", C.c_double), ("steps", C.c_int32)]
+
+
+class MuonConfig(C.Structure):
+    _fields_ = [("lr", C.c_double), ("momentum", C.c_double), ("weight_decay", C.c_double),
+                ("scale", C.c_double), ("nesterov", C.c_int32), ("ns", NsConfig)]
 
 
 class SparseOptError(RuntimeError):
@@ -111,6 +121,20 @@ def lib() -> C.CDLL:
         L.sparse_step_from_lookups_noalloc.restype = C.c_int
         L.sparse_opt_set_step_events.argtypes = [P, P]
         L.sparse_opt_set_step_events.restype = C.c_int
+        F64, SZ = C.c_double, C.c_size_t
+        L.layer_norm_forward.argtypes = [P, I64, I64, I64, I32, P, P, I32, F64, P, I64, P, P, P,
+                                         U32]
+        L.layer_norm_backward_workspace_size.argtypes = [I64, I64, C.POINTER(SZ)]
+        L.layer_norm_backward.argtypes = [P, I64, P, I64, I64, I64, I32, P, P, P, I32, P, I64, P,
+                                          P, P, SZ, P, U32]
+        L.newton_schulz_workspace_size.argtypes = [I64, I64, I64, C.POINTER(SZ)]
+        L.newton_schulz.argtypes = [P, I32, I64, I64, I64, C.POINTER(NsConfig), P, P, SZ, P, U32]
+        L.muon_step.argtypes = [P, I32, P, P, I32, I64, I64, I64, C.POINTER(MuonConfig), P, SZ, P,
+                                U32]
+        for f in (L.layer_norm_forward, L.layer_norm_backward_workspace_size,
+                  L.layer_norm_backward, L.newton_schulz_workspace_size, L.newton_schulz,
+                  L.muon_step):
+            f.restype = C.c_int
         _lib = L
     return _lib
 
@@ -125,4 +149,6 @@ EXPORTED = ("sparse_opt_create", "sparse_opt_destroy", "sparse_opt_get_step", "s
             "csr_from_coo", "csr_from_lookups", "csr_to_coo", "sparse_adam_step",
             "sparse_sgd_step", "sparse_step_from_lookups", "sparse_step_from_lookups_noalloc",
             "sparse_opt_set_step_events", "read_rows",
-            "sparse_opt_host_alloc", "sparse_opt_host_free", "sparse_opt_host_device_pointer")
+            "sparse_opt_host_alloc", "sparse_opt_host_free", "sparse_opt_host_device_pointer",
+            "layer_norm_forward", "layer_norm_backward_workspace_size", "layer_norm_backward",
+            "newton_schulz_workspace_size", "newton_schulz", "muon_step")
