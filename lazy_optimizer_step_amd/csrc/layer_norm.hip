@@ -4,23 +4,154 @@
 // operations on it: HBM bounds them.
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.hpp"
 #include "dense_ops.h"
 #include "dense.hpp"
 
 namespace spopt {
 
-// Sum over the 256 threads of a block; every thread gets it.  `lds` holds one
-// float per wave; a barrier before the next use is inside.
-__device__ __forceinline__ float block_sum(float v, float* lds) {
-#pragma unroll
-    for (int off = kWave / 2; off; off >>= 1) v += __shfl_xor(v, off, kWave);
+// Sum over the G lanes of a group that share a row (G = 16, 32 or 64): every
+// lane gets it.  The first four exchanges stay in the vector unit: quads, then
+// mirrors of 8 and 16 lanes, which join sums that are already alike within
+// each half.
+template <int G>
+__device__ __forceinline__ float lane_sum(float v) {
+    auto dpp = [](float x, auto ctrl) {
+        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+            0, __builtin_bit_cast(int, x), decltype(ctrl)::value, 0xf, 0xf, true));
+    };
+    v += dpp(v, std::integral_constant<int, 0xB1>{});   // quad_perm 1,0,3,2
+    v += dpp(v, std::integral_constant<int, 0x4E>{});   // quad_perm 2,3,0,1
+    v += dpp(v, std::integral_constant<int, 0x141>{});  // row_half_mirror
+    v += dpp(v, std::integral_constant<int, 0x140>{});  // row_mirror
+    if (G >= 32) v += __shfl_xor(v, 16, kWave);
+    if (G >= 64) v += __shfl_xor(v, 32, kWave);
+    return v;
+}
+
+// Sum over a block of `waves` waves; every thread gets it.  A barrier is
+// passed before `lds` is written, so it can be used again at once.
+__device__ __forceinline__ float block_sum(float v, float* lds, int waves = 4) {
+    v = lane_sum<64>(v);
     __syncthreads();
     if (lane_id() == 0) lds[threadIdx.x >> 6] = v;
     __syncthreads();
     float s = 0.f;
-    for (int i = 0; i < (int)(blockDim.x >> 6); ++i) s += lds[i];
+    for (int i = 0; i < waves; ++i) s += lds[i];
     return s;
+}
+
+// V values at p, which need only be aligned to one of them: gfx950 takes
+// 16-byte global accesses at any address, and rows of odd widths or strides
+// start anywhere.
+template <class T, int V>
+struct Pack {
+    typedef T type __attribute__((ext_vector_type(V), aligned(sizeof(T))));
+};
+template <class T>
+struct Pack<T, 1> {
+    typedef T type;
+};
+
+template <class T, int V>
+__device__ __forceinline__ void load_v(const T* p, float (&x)[V]) {
+    const auto q = *reinterpret_cast<const typename Pack<T, V>::type*>(p);
+    if constexpr (V == 1)
+        x[0] = (float)q;
+    else
+#pragma unroll
+        for (int e = 0; e < V; ++e) x[e] = (float)q[e];
+}
+
+template <class T, int V>
+__device__ __forceinline__ void store_v(T* p, const float (&x)[V]) {
+    typename Pack<T, V>::type q;
+    if constexpr (V == 1)
+        q = (T)x[0];
+    else
+#pragma unroll
+        for (int e = 0; e < V; ++e) q[e] = (T)x[e];
+    *reinterpret_cast<typename Pack<T, V>::type*>(p) = q;
+}
+
+// Where chunk `ch` of V columns lies in a row of `cols` >= V: the last one is
+// moved back to end with the row, its first `skip` columns being the chunk
+// before's (they count in no sum; stores write them twice, the same value).  A
+// chunk past the row counts nothing (skip = V) and reads column 0.
+template <int V>
+struct Chunk {
+    int at, skip;
+    bool in;
+    __device__ __forceinline__ Chunk(int ch, int cols) {
+        const int c = ch * V;
+        in = c < cols;
+        at = in ? (c < cols - V ? c : cols - V) : 0;
+        skip = in ? c - at : V;
+    }
+};
+
+// A row in the registers of G lanes, NV chunks of V values each: read once,
+// the mean and then the centred squares summed from registers, written once.
+// G <= 64: 256 / G rows a block; above: a block of G threads per row.
+template <class T, class W, int V, int NV, int G>
+__global__ __launch_bounds__(G < 256 ? 256 : G) void k_ln_fwd(const T* x, int64_t xs,
+                                                             int64_t rows, int cols, const W* w,
+                                                             const W* b, float eps, T* y,
+                                                             int64_t ys, float* mean,
+                                                             float* rstd) {
+    constexpr int RPB = G < 256 ? 256 / G : 1;
+    __shared__ float lds[G < 256 ? 1 : G / 64];
+    const int gl = G < 256 ? threadIdx.x % G : threadIdx.x;
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    const float n = (float)cols;  // divided by: a constant row has exactly its value as mean
+    for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < rows; r0 += step) {
+        const int64_t rr = r0 + (G < 256 ? threadIdx.x / G : 0);
+        const int64_t r = rr < rows ? rr : rows - 1;  // spare groups redo the last row, unwritten
+        float v[NV][V];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) load_v<T, V>(x + r * xs + Chunk<V>(k * G + gl, cols).at, v[k]);
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const Chunk<V> c(k * G + gl, cols);
+#pragma unroll
+            for (int e = 0; e < V; ++e) s += e >= c.skip ? v[k][e] : 0.f;
+        }
+        const float mu = (G < 256 ? lane_sum<G>(s) : block_sum(s, lds, G / 64)) / n;
+        float q = 0.f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const Chunk<V> c(k * G + gl, cols);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                v[k][e] -= mu;
+                q += e >= c.skip ? v[k][e] * v[k][e] : 0.f;
+            }
+        }
+        const float rs =
+            1.0f / sqrtf((G < 256 ? lane_sum<G>(q) : block_sum(q, lds, G / 64)) / n + eps);
+        if (gl == 0 && rr < rows) {
+            if (mean) mean[r] = mu;
+            if (rstd) rstd[r] = rs;
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const Chunk<V> c(k * G + gl, cols);
+            float wv[V], bv[V];
+            if (w) load_v<W, V>(w + c.at, wv);
+            if (b) load_v<W, V>(b + c.at, bv);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                float o = v[k][e] * rs;
+                if (w) o *= wv[e];
+                if (b) o += bv[e];
+                v[k][e] = o;
+            }
+            if (c.in && rr < rows) store_v<T, V>(y + r * ys + c.at, v[k]);
+        }
+    }
 }
 
 // One block per row, any width: the row is read once for the mean, again for
@@ -81,6 +212,166 @@ __global__ __launch_bounds__(256) void k_ln_dx_any(const T* dy, int64_t ds, cons
     }
 }
 
+// The whole backward pass of the rows of one slice (blockIdx.x): each group of
+// G lanes takes every (groups)th row of it, with the row's dy and x read once
+// into registers, the next row's asked for before this one is worked on, and
+// the lane's columns' sums of dy * xhat and dy kept in registers over all its
+// rows.  At the end the block's groups are joined in LDS and written to
+// part[slice][2][cols].
+template <class T, class W, int V, int NV, int G>
+__global__ __launch_bounds__(G < 256 ? 256 : G) void k_ln_bwd(
+    const T* dy, int64_t ds, const T* x, int64_t xs, int64_t rows, int cols, const float* mean,
+    const float* rstd, const W* w, T* dx, int64_t os, int64_t per, float* part) {
+    constexpr int RPB = G < 256 ? 256 / G : 1;
+    // 1024 threads have 128 registers each: no room for a row ahead.
+    constexpr bool kAhead = G < 1024;
+    __shared__ float lds[G < 256 ? 1 : 4 * (G / 64)];
+    typedef typename Pack<T, V>::type P;
+    const int gl = G < 256 ? threadIdx.x % G : threadIdx.x;
+    const int grp = G < 256 ? threadIdx.x / G : 0;
+    const float inv = 1.0f / (float)cols;
+    const int64_t r0 = (int64_t)blockIdx.x * per, r1 = r0 + per < rows ? r0 + per : rows;
+    float dw[NV][V] = {}, db[NV][V] = {};
+    float wv[NV][V];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        if (w)
+            load_v<W, V>(w + Chunk<V>(k * G + gl, cols).at, wv[k]);
+        else
+            for (int e = 0; e < V; ++e) wv[k][e] = 1.f;
+    }
+    P nd[NV], nx[NV];
+    float nmu = 0.f, nrs = 0.f;
+    auto fetch = [&](int64_t q) {
+        const int64_t r = q < rows ? q : rows - 1;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int at = Chunk<V>(k * G + gl, cols).at;
+            nd[k] = *reinterpret_cast<const P*>(dy + r * ds + at);
+            nx[k] = *reinterpret_cast<const P*>(x + r * xs + at);
+        }
+        nmu = mean[r];
+        nrs = rstd[r];
+    };
+    if (kAhead) fetch(r0 + grp);
+    int parity = 0;
+    for (int64_t rb = r0; rb < r1; rb += RPB) {
+        const int64_t r = rb + grp;
+        const bool live = r < r1;
+        P d[NV], h[NV];
+        if (!kAhead) fetch(r);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            d[k] = nd[k];
+            h[k] = nx[k];
+        }
+        const float mu = nmu, rs = live ? nrs : 0.f;
+        if (kAhead && rb + RPB < r1) fetch(r + RPB);
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const Chunk<V> c(k * G + gl, cols);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const bool on = live && e >= c.skip;
+                float g, xv;
+                if constexpr (V == 1) {
+                    g = (float)d[k];
+                    xv = (float)h[k];
+                } else {
+                    g = (float)d[k][e];
+                    xv = (float)h[k][e];
+                }
+                const float hat = (xv - mu) * rs;
+                const float z = g * wv[k][e];
+                s1 += on ? z : 0.f;
+                s2 += on ? z * hat : 0.f;
+                dw[k][e] += on ? g * hat : 0.f;
+                db[k][e] += on ? g : 0.f;
+            }
+        }
+        if constexpr (G < 256) {
+            s1 = lane_sum<G>(s1);
+            s2 = lane_sum<G>(s2);
+        } else {
+            // One barrier a row: the two halves of lds take turns.
+            s1 = lane_sum<64>(s1);
+            s2 = lane_sum<64>(s2);
+            float* l = lds + parity * 2 * (G / 64);
+            parity ^= 1;
+            if (lane_id() == 0) {
+                l[2 * (threadIdx.x >> 6)] = s1;
+                l[2 * (threadIdx.x >> 6) + 1] = s2;
+            }
+            __syncthreads();
+            s1 = s2 = 0.f;
+#pragma unroll
+            for (int i = 0; i < G / 64; ++i) {
+                s1 += l[2 * i];
+                s2 += l[2 * i + 1];
+            }
+        }
+        if (dx != nullptr) {
+            const float m1 = s1 * inv, m2 = s2 * inv;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const Chunk<V> c(k * G + gl, cols);
+                float o[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    float g, xv;
+                    if constexpr (V == 1) {
+                        g = (float)d[k];
+                        xv = (float)h[k];
+                    } else {
+                        g = (float)d[k][e];
+                        xv = (float)h[k][e];
+                    }
+                    o[e] = rs * (g * wv[k][e] - m1 - (xv - mu) * rs * m2);
+                }
+                if (live && c.in) store_v<T, V>(dx + r * os + c.at, o);
+            }
+        }
+    }
+    if (part == nullptr) return;
+    float* p = part + (int64_t)blockIdx.x * 2 * cols;
+    if constexpr (G < 256) {
+        // Lane gl of every group holds the same columns: join the groups.
+        __shared__ float jw[RPB][G * NV * V], jb[RPB][G * NV * V];
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                jw[grp][(k * G + gl) * V + e] = dw[k][e];
+                jb[grp][(k * G + gl) * V + e] = db[k][e];
+            }
+        __syncthreads();
+        for (int i = threadIdx.x; i < G * NV * V; i += 256) {
+            const Chunk<V> c(i / V, cols);
+            if (i % V < c.skip) continue;
+            float sw = 0.f, sb = 0.f;
+#pragma unroll
+            for (int q = 0; q < RPB; ++q) {
+                sw += jw[q][i];
+                sb += jb[q][i];
+            }
+            p[c.at + i % V] = sw;
+            p[cols + c.at + i % V] = sb;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const Chunk<V> c(k * G + gl, cols);
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (e >= c.skip) {
+                    p[c.at + e] = dw[k][e];
+                    p[cols + c.at + e] = db[k][e];
+                }
+        }
+    }
+}
+
 // Sums of dy * xhat and dy over one slice of rows (blockIdx.y) for 64 columns:
 // four rows at a time, joined in LDS.  part: [slices][2][cols].
 template <class T>
@@ -109,34 +400,61 @@ __global__ __launch_bounds__(256) void k_ln_cols_any(const T* dy, int64_t ds, co
     }
 }
 
-// dweight and dbias from the slices' sums: a block takes 64 columns, its four
-// waves a quarter of the slices each; joined in double.
+// dweight and dbias from the slices' sums: a block takes 16 columns of one of
+// the two, 64 threads on each column's slices, joined in double in a fixed
+// order.
 template <class W>
-__global__ __launch_bounds__(256) void k_ln_join(const float* part, int64_t slices, int64_t cols,
-                                                 W* dw, W* db) {
-    __shared__ double lw[4][64], lb[4][64];
-    const int lane = lane_id(), k = threadIdx.x >> 6;
-    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
-    double sw = 0., sb = 0.;
+__global__ __launch_bounds__(1024) void k_ln_join(const float* part, int64_t slices, int64_t cols,
+                                                  W* dw, W* db) {
+    __shared__ double l[64][17];
+    const int q = threadIdx.x & 15, k = threadIdx.x >> 4;
+    const int64_t c = (int64_t)blockIdx.x * 16 + q;
+    W* out = blockIdx.y ? db : dw;
+    if (out == nullptr) return;
+    double s = 0.;
     if (c < cols)
-        for (int64_t i = k; i < slices; i += 4) {
-            sw += (double)part[i * 2 * cols + c];
-            sb += (double)part[(i * 2 + 1) * cols + c];
-        }
-    lw[k][lane] = sw;
-    lb[k][lane] = sb;
+        for (int64_t i = k; i < slices; i += 64) s += (double)part[(i * 2 + blockIdx.y) * cols + c];
+    l[k][q] = s;
     __syncthreads();
-    if (k == 0 && c < cols) {
-        if (dw) dw[c] = (W)(float)((lw[0][lane] + lw[1][lane]) + (lw[2][lane] + lw[3][lane]));
-        if (db) db[c] = (W)(float)((lb[0][lane] + lb[1][lane]) + (lb[2][lane] + lb[3][lane]));
+    for (int n = 32; n; n >>= 1) {
+        if (k < n) l[k][q] += l[k + n][q];
+        __syncthreads();
     }
+    if (k == 0 && c < cols) out[c] = (W)(float)l[0][q];
 }
 
-// Row slices of the column sums: enough blocks to fill the card, and partial
-// sums of no more than about 1/32 of the inputs.
-static int64_t ln_slices(int64_t rows) {
-    const int64_t s = ceil_div(rows, 64);
-    return s < 1 ? 1 : s > 256 ? 256 : s;
+// How a row is shared out: G lanes of NV chunks of V values hold it.
+struct RowPlan {
+    int g, nv;     // 0: no kernel holds a row this wide
+    bool one;      // fewer columns than a vector: single values, 16 lanes
+};
+
+// 16-byte chunks.  Few lanes on narrow rows, so that every lane loads; a wave
+// up to 32 values a lane forward (16 backward, which keeps dy, x and two sums
+// of each), a block beyond, as then several rows' loads still fit a CU.
+static RowPlan ln_plan(int64_t cols, int v, bool backward) {
+    static const RowPlan fwd[] = {{16, 1}, {32, 1}, {64, 1}, {64, 2}, {64, 4}, {256, 2}, {256, 4},
+                                  {256, 8}, {1024, 4}};
+    static const RowPlan bwd[] = {{16, 1}, {32, 1}, {64, 1}, {64, 2}, {256, 1}, {256, 2}, {512, 2},
+                                  {1024, 2}, {1024, 4}};
+    if (cols < v) return {16, 1, true};
+    if (backward) {
+        for (const RowPlan& p : bwd)
+            if (cols <= (int64_t)p.g * p.nv * v && p.nv * v <= 16) return p;
+    } else {
+        for (const RowPlan& p : fwd)
+            if (cols <= (int64_t)p.g * p.nv * v) return p;
+    }
+    return {0, 0, false};
+}
+
+// Row slices of the column sums, one block each: enough to fill the card with
+// rows for every group to loop over, and few enough that the slices' sums stay
+// a small part of the traffic.
+static int64_t ln_slices(int64_t rows, int64_t cols) {
+    const int64_t most = cols <= 1024 ? 1024 : 512;
+    const int64_t s = ceil_div(rows, cols <= 1024 ? 16 : 4);
+    return s < 1 ? 1 : s > most ? most : s;
 }
 
 static int ln_check(const char* what, int64_t rows, int64_t cols, int32_t dtype, int32_t wdtype) {
@@ -166,6 +484,9 @@ static void ln_types(int32_t dtype, int32_t wdtype, F&& f) {
         wdtype == SPOPT_DTYPE_F32 ? f(_Float16{}, float{}) : f(_Float16{}, _Float16{});
 }
 
+template <int N>
+using Int = std::integral_constant<int, N>;
+
 static unsigned row_grid(int64_t rows) { return (unsigned)(rows < 65536 ? rows : 65536); }
 
 }  // namespace spopt
@@ -194,9 +515,31 @@ extern "C" int layer_norm_forward(const void* x, int64_t x_stride, int64_t rows,
     ln_types(dtype, wdtype, [&](auto t, auto wt) {
         using T = decltype(t);
         using W = decltype(wt);
-        k_ln_fwd_any<T, W><<<row_grid(rows), 256, 0, s>>>(
-            (const T*)x, x_stride, rows, cols, (const W*)weight, (const W*)bias, (float)eps,
-            (T*)y, y_stride, mean, rstd);
+        constexpr int V = 16 / sizeof(T);
+        const RowPlan p = ln_plan(cols, V, false);
+        auto go = [&](auto v, auto nv, auto g) {
+            constexpr int G = decltype(g)::value;
+            const unsigned grid = row_grid(ceil_div(rows, G < 256 ? 256 / G : 1));
+            k_ln_fwd<T, W, decltype(v)::value, decltype(nv)::value, G>
+                <<<grid, G < 256 ? 256 : G, 0, s>>>((const T*)x, x_stride, rows, (int)cols,
+                                                    (const W*)weight, (const W*)bias, (float)eps,
+                                                    (T*)y, y_stride, mean, rstd);
+        };
+        auto at = [&](auto nv, auto g) { go(Int<V>{}, nv, g); };
+        if (p.one) go(Int<1>{}, Int<1>{}, Int<16>{});
+        else if (p.g == 16) at(Int<1>{}, Int<16>{});
+        else if (p.g == 32) at(Int<1>{}, Int<32>{});
+        else if (p.g == 64 && p.nv == 1) at(Int<1>{}, Int<64>{});
+        else if (p.g == 64 && p.nv == 2) at(Int<2>{}, Int<64>{});
+        else if (p.g == 64) at(Int<4>{}, Int<64>{});
+        else if (p.g == 256 && p.nv == 2) at(Int<2>{}, Int<256>{});
+        else if (p.g == 256 && p.nv == 4) at(Int<4>{}, Int<256>{});
+        else if (p.g == 256) at(Int<8>{}, Int<256>{});
+        else if (p.g == 1024) at(Int<4>{}, Int<1024>{});
+        else
+            k_ln_fwd_any<T, W><<<row_grid(rows), 256, 0, s>>>(
+                (const T*)x, x_stride, rows, cols, (const W*)weight, (const W*)bias, (float)eps,
+                (T*)y, y_stride, mean, rstd);
     });
     SPOPT_LAUNCHED();
     return SPOPT_OK;
@@ -207,7 +550,7 @@ extern "C" int layer_norm_backward_workspace_size(int64_t rows, int64_t cols, si
         cols > INT64_MAX / 8192)
         return fail(SPOPT_EINVAL, "layer_norm_backward_workspace_size: bad size %lld x %lld",
                     (long long)rows, (long long)cols);
-    *bytes = (size_t)ln_slices(rows) * 2 * (size_t)cols * sizeof(float);
+    *bytes = (size_t)ln_slices(rows, cols) * 2 * (size_t)cols * sizeof(float);
     return SPOPT_OK;
 }
 
@@ -239,23 +582,49 @@ extern "C" int layer_norm_backward(const void* dy, int64_t dy_stride, const void
         });
         if (rc) return rc;
     }
-    const int64_t slices = rows == 0 ? 0 : ln_slices(rows);
+    int64_t slices = rows == 0 ? 0 : ln_slices(rows, cols);
     ln_types(dtype, wdtype, [&](auto t, auto wt) {
         using T = decltype(t);
         using W = decltype(wt);
-        float* part = (float*)workspace;
-        const unsigned cb = (unsigned)ceil_div(cols, 64);
-        // The column sums first: dx may lie over dy or x.
-        if (sums && rows > 0)
-            k_ln_cols_any<T><<<dim3(cb, (unsigned)slices), 256, 0, s>>>(
-                (const T*)dy, dy_stride, (const T*)x, x_stride, rows, cols, mean, rstd,
-                ceil_div(rows, slices), part);
-        if (dx != nullptr && rows > 0)
-            k_ln_dx_any<T, W><<<row_grid(rows), 256, 0, s>>>(
-                (const T*)dy, dy_stride, (const T*)x, x_stride, rows, cols, mean, rstd,
-                (const W*)weight, (T*)dx, dx_stride);
+        constexpr int V = 16 / sizeof(T);
+        float* part = sums ? (float*)workspace : nullptr;
+        const RowPlan p = ln_plan(cols, V, true);
+        const int64_t per = slices ? ceil_div(rows, slices) : 0;
+        if (slices) slices = ceil_div(rows, per);  // no empty slice
+        auto go = [&](auto v, auto nv, auto g) {
+            constexpr int G = decltype(g)::value;
+            k_ln_bwd<T, W, decltype(v)::value, decltype(nv)::value, G>
+                <<<(unsigned)slices, G < 256 ? 256 : G, 0, s>>>(
+                    (const T*)dy, dy_stride, (const T*)x, x_stride, rows, (int)cols, mean, rstd,
+                    (const W*)weight, (T*)dx, dx_stride, per, part);
+        };
+        auto at = [&](auto nv, auto g) { go(Int<V>{}, nv, g); };
+        if (rows == 0 || (!sums && dx == nullptr)) {
+        } else if (p.one) go(Int<1>{}, Int<1>{}, Int<16>{});
+        else if (p.g == 16) at(Int<1>{}, Int<16>{});
+        else if (p.g == 32) at(Int<1>{}, Int<32>{});
+        else if (p.g == 64 && p.nv == 1) at(Int<1>{}, Int<64>{});
+        else if (p.g == 64) at(Int<2>{}, Int<64>{});
+        else if (p.g == 256 && p.nv == 1) at(Int<1>{}, Int<256>{});
+        else if (p.g == 256 && p.nv == 2) at(Int<2>{}, Int<256>{});
+        else if (p.g == 512) at(Int<2>{}, Int<512>{});
+        else if (p.g == 1024 && p.nv == 2) at(Int<2>{}, Int<1024>{});
+        else if (p.g == 1024) {
+            if constexpr (sizeof(T) == 4) at(Int<4>{}, Int<1024>{});
+        } else {
+            // Wider rows: the column sums first, as dx may lie over dy or x.
+            if (sums)
+                k_ln_cols_any<T><<<dim3((unsigned)ceil_div(cols, 64), (unsigned)slices), 256, 0,
+                                   s>>>((const T*)dy, dy_stride, (const T*)x, x_stride, rows, cols,
+                                        mean, rstd, per, part);
+            if (dx != nullptr)
+                k_ln_dx_any<T, W><<<row_grid(rows), 256, 0, s>>>(
+                    (const T*)dy, dy_stride, (const T*)x, x_stride, rows, cols, mean, rstd,
+                    (const W*)weight, (T*)dx, dx_stride);
+        }
         if (sums)
-            k_ln_join<W><<<cb, 256, 0, s>>>(part, slices, cols, (W*)dweight, (W*)dbias);
+            k_ln_join<W><<<dim3((unsigned)ceil_div(cols, 16), 2), 1024, 0, s>>>(
+                part, slices, cols, (W*)dweight, (W*)dbias);
     });
     SPOPT_LAUNCHED();
     return SPOPT_OK;
