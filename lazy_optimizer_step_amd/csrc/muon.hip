@@ -20,17 +20,20 @@
 // it in bfloat16.
 #include <math.h>
 
+#include <type_traits>
+
 #include "dense.hpp"
 
 namespace spopt {
 
+typedef _Float16 half4 __attribute__((ext_vector_type(4)));
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef float float4v __attribute__((ext_vector_type(4)));
 
 constexpr int kTile = 64;                    // rows, columns and inner axis are padded to it
 constexpr float kXScale = 256.f;             // 2^8
 constexpr float kAScale = 4096.f;            // 2^12
-constexpr int kNormParts = 256;              // partial sums of a matrix's norm, at most
+constexpr int kNormParts = 1024;             // partial sums of a matrix's norm, at most
 
 // The matrix U that a call orthogonalises, formed as it is read.
 template <class G>
@@ -57,16 +60,36 @@ __device__ __forceinline__ double block_sum_d(double v, double* lds) {
 }
 
 // buf <- mu * buf + g where the step keeps a momentum, and each block's share
-// of sum(U^2), in double.  Block (x, z): slice x of matrix z.
+// of sum(U^2), in double.  Block (x, y): slice x of matrix y, 8 values a
+// thread at a time (matrices of odd sizes start anywhere).
 template <class G>
 __global__ __launch_bounds__(256) void k_ns_norm(Source<G> u, float* buf, int64_t numel,
                                                  double* part) {
     __shared__ double lds[4];
     const int64_t base = (int64_t)blockIdx.y * numel;
+    const G* g = u.g + base;
     double s = 0.;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < numel;
-         i += (int64_t)gridDim.x * 256) {
-        if (u.kind != 0) buf[base + i] = u.mu * buf[base + i] + (float)u.g[base + i];
+    const int64_t whole = numel / 8 * 8;
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < whole;
+         i += (int64_t)gridDim.x * 256 * 8) {
+        float v[8];
+        load_v<G, 8>(g + i, v);
+        if (u.kind != 0) {
+            float b[8];
+            load_v<float, 8>(buf + base + i, b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                b[e] = u.mu * b[e] + v[e];
+                v[e] = u.kind == 1 ? b[e] : v[e] + u.mu * b[e];
+            }
+            store_v<float, 8>(buf + base + i, b);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s += (double)v[e] * (double)v[e];
+    }
+    const int64_t i = whole + threadIdx.x;
+    if (blockIdx.x == 0 && i < numel) {
+        if (u.kind != 0) buf[base + i] = u.mu * buf[base + i] + (float)g[i];
         const double v = (double)u.at(base + i);
         s += v * v;
     }
@@ -97,23 +120,31 @@ __global__ __launch_bounds__(256) void k_ns_init(Source<G> u, NsBuffers w, NsSha
     __shared__ double lds[4];
     __shared__ float tile[kTile][kTile + 1];
     const int64_t z = blockIdx.z;
-    const double sq = block_sum_d(
-        (int)threadIdx.x < parts ? w.part[z * kNormParts + threadIdx.x] : 0., lds);
-    const double scale = 1.0 / (sqrt(sq) + eps);
     const int i0 = blockIdx.y * kTile, j0 = blockIdx.x * kTile;
     const int q = threadIdx.x & 63, k = threadIdx.x >> 6;
     const int64_t base = z * sh.m * sh.n;
-    for (int t = k; t < kTile; t += 4) {
-        // Read along the input's rows: those of X, or X's columns.
-        const int i = sh.flip ? i0 + q : i0 + t, j = sh.flip ? j0 + t : j0 + q;
-        float v = 0.f;
-        if (i < sh.r && j < sh.c)
-            v = (float)((double)u.at(base + (sh.flip ? (int64_t)j * sh.r + i
-                                                     : (int64_t)i * sh.c + j)) * scale);
+    // All of the thread's values are asked for first, along the input's rows
+    // (those of X, or X's columns).
+    float v[kTile / 4];
+#pragma unroll
+    for (int t = 0; t < kTile / 4; ++t) {
+        const int a = 4 * t + k;
+        const int i = sh.flip ? i0 + q : i0 + a, j = sh.flip ? j0 + a : j0 + q;
+        const bool in = i < sh.r && j < sh.c;
+        const float x = u.at(base + (in ? sh.flip ? (int64_t)j * sh.r + i
+                                                  : (int64_t)i * sh.c + j : 0));
+        v[t] = in ? x : 0.f;
+    }
+    double sq = 0.;
+    for (int t = threadIdx.x; t < parts; t += 256) sq += w.part[z * kNormParts + t];
+    const double scale = 1.0 / (sqrt(block_sum_d(sq, lds)) + eps);
+#pragma unroll
+    for (int t = 0; t < kTile / 4; ++t) {
+        const float x = (float)((double)v[t] * scale);
         if (sh.flip)
-            tile[q][t] = v;
+            tile[q][4 * t + k] = x;
         else
-            tile[t][q] = v;
+            tile[4 * t + k][q] = x;
     }
     __syncthreads();
     const int64_t xb = z * sh.rp * sh.cp;
@@ -133,18 +164,93 @@ struct NsStep {
     float keep, move;  // kParam*: p <- keep * p - move * X
 };
 
-// One product P Q^T over 64 x 64 tiles, the inner axis 64 at a time through
-// LDS, and what its result is for:
+// Waits until at most N of this wave's loads (into LDS too) are on their way;
+// wait_stage also for its reads of LDS, and for the block's other waves.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_stage() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+template <int MODE>
+struct OutType {
+    typedef __bf16 type;
+};
+template <>
+struct OutType<kParam32> {
+    typedef float type;
+};
+
+// The last step's values to where they go: the result, or the weight's update.
+template <int MODE, int V>
+__device__ __forceinline__ void write_out(typename OutType<MODE>::type* d, const float (&v)[V],
+                                          const NsStep& st) {
+    typedef typename OutType<MODE>::type O;
+    if constexpr (MODE == kOut) {
+        store_v<O, V>(d, v);
+    } else {
+        float p[V];
+        load_v<O, V>(d, p);
+#pragma unroll
+        for (int e = 0; e < V; ++e) p[e] = st.keep * p[e] - st.move * v[e];
+        store_v<O, V>(d, p);
+    }
+}
+
+// A block's tile of BM x BN values, shared out to WGM x WGN waves, and how many
+// stages of the inner axis LDS holds.
+template <int BM_, int BN_, int WGM_, int WGN_, int STAGES_>
+struct Tiling {
+    static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, STAGES = STAGES_;
+    static constexpr int kThreads = WGM * WGN * 64;
+    static constexpr int kStage = (BM + BN) * kTile;  // float16 values of one inner step
+};
+
+// Order of the tiles: blocks go to the 8 XCDs in turn, so block b takes place
+// b / 8 of the (b % 8)th eighth, and each XCD's L2 sees neighbouring tiles.
+__device__ __forceinline__ int64_t xcd_order(int64_t b, int64_t n) {
+    const int64_t q = n / 8, rem = n % 8, x = b % 8;
+    return x * q + (x < rem ? x : rem) + b / 8;
+}
+
+// One product P Q^T, tile by tile, and what its result is for:
 //   kGram  A = X X^T           kPoly  B = b A + c A A     (lower tiles, mirrored)
 //   kNext  X <- a X + B X      kOut / kParam*  the last step's X, written out
-template <int MODE>
-__global__ __launch_bounds__(256) void k_ns_gemm(NsBuffers w, NsShape sh, NsStep st, int from) {
-    constexpr int LD = kTile + 8;  // 144-byte rows: 16-byte reads of 16 rows meet each bank twice
-    __shared__ __align__(16) _Float16 lp[kTile * LD], lq[kTile * LD];
-    const int64_t z = blockIdx.z;
+//
+// The inner axis goes through LDS 64 values at a time: the next stages' rows
+// are on their way straight into LDS while this one is multiplied.  Two stages
+// are enough where several blocks share a CU or the tile is large; a block
+// alone on its CU takes four, as operands that the launch before wrote come
+// from beyond the XCD's own L2.  A row's eight 16-byte chunks lie in an order turned by the row
+// (chunk c at c ^ (row & 7)): the 16 rows that a matrix instruction's operand
+// takes then meet every bank equally, without padding, which the loads into
+// LDS could not leave.
+//
+// Which of the tile's rows lies in which row of LDS is chosen for the end: with
+// Q's rows as the matrix instruction's first operand, lane l holds, of rows
+// FM (l % 16) .. + FM - 1 of its wave's part (FM adjacent ones, from FM
+// instructions), 8 adjacent columns of every 32 (4 of every 16 where a wave has
+// an odd number of 16-column parts).  Rows of the result are written 16 bytes
+// of float16 at a time and columns (the mirrored half, X^T) up to 8 values at a
+// time, with no exchange between lanes.
+template <int MODE, class T>
+__global__ __launch_bounds__(T::kThreads) void k_ns_gemm(NsBuffers w, NsShape sh, NsStep st,
+                                                         int from, int tiles) {
+    constexpr int BM = T::BM, BN = T::BN, WM = BM / T::WGM, WN = BN / T::WGN;
+    constexpr int FM = WM / 16, FN = WN / 16, kWaves = T::WGM * T::WGN;
+    constexpr int kRow = FN % 2 ? 4 : 8;                            // columns of a row's store
+    constexpr int kCol = FM % 8 == 0 ? 8 : FM % 4 == 0 ? 4 : 2;  // rows of a column's store
+    extern __shared__ __align__(16) char lds_raw[];
+    _Float16* const lds = (_Float16*)lds_raw;
+    const int64_t t = xcd_order(blockIdx.x, gridDim.x);
+    const int64_t z = t / tiles;
+    const int tile = (int)(t % tiles);
     const int64_t nx = (int64_t)sh.rp * sh.cp, na = (int64_t)sh.rp * sh.rp;
     const _Float16 *p, *q;
-    int64_t k_len;
+    int k_len, q_rows = sh.rp, ti, tj;
     if (MODE == kGram) {
         p = q = w.x16 + z * nx;
         k_len = sh.cp;
@@ -155,77 +261,185 @@ __global__ __launch_bounds__(256) void k_ns_gemm(NsBuffers w, NsShape sh, NsStep
         p = w.b16 + z * na;
         q = w.xt[from] + z * nx;
         k_len = sh.rp;
+        q_rows = sh.cp;
     }
-    int ti = blockIdx.y, tj = blockIdx.x;
-    if (MODE <= kPoly && tj > ti) return;
-    const int i0 = ti * kTile, j0 = tj * kTile;
-    const int lane = lane_id(), wv = threadIdx.x >> 6;
-    const int wi = (wv >> 1) * 32, wj = (wv & 1) * 32;
-    float4v acc[2][2] = {};
-    for (int64_t k0 = 0; k0 < k_len; k0 += kTile) {
-        __syncthreads();
-        for (int t = threadIdx.x; t < kTile * 8; t += 256) {
-            const int row = t >> 3, ch = (t & 7) * 8;
-            *(half8*)(lp + row * LD + ch) = *(const half8*)(p + (i0 + row) * k_len + k0 + ch);
-            *(half8*)(lq + row * LD + ch) = *(const half8*)(q + (j0 + row) * k_len + k0 + ch);
+    if (MODE <= kPoly) {
+        // Row ti holds tiles 0 .. ti of the lower triangle.
+        ti = (int)((sqrtf(8.f * (float)tile + 1.f) - 1.f) * 0.5f);
+        while ((int64_t)(ti + 1) * (ti + 2) / 2 <= tile) ++ti;
+        while ((int64_t)ti * (ti + 1) / 2 > tile) --ti;
+        tj = tile - (int)((int64_t)ti * (ti + 1) / 2);
+    } else {
+        // Four rows of tiles at a time, column by column.
+        const int tr = (sh.rp + BM - 1) / BM, tc = (sh.cp + BN - 1) / BN;
+        const int band = tile / (4 * tc), in = tile % (4 * tc);
+        const int rows = tr - 4 * band < 4 ? tr - 4 * band : 4;
+        ti = 4 * band + in % rows;
+        tj = in / rows;
+    }
+    const int i0 = ti * BM, j0 = tj * BN;
+    const int lane = lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wi = (wv / T::WGN) * WM, wj = (wv % T::WGN) * WN;
+
+    // Wave wv brings 8 rows at a time, every kWaves-th eight of P's and Q's.
+    constexpr int kLoads = (BM + BN) / 8 / kWaves;
+    static_assert((BM + BN) % (8 * kWaves) == 0, "rows share out evenly");
+    const _Float16* src[kLoads];
+#pragma unroll
+    for (int l = 0; l < kLoads; ++l) {
+        const int row8 = (l * kWaves + wv) * 8, row = row8 + (lane >> 3);
+        const int ch = ((lane & 7) ^ (lane >> 3)) * 8;
+        // Rows past the operand repeat its last one; their products are not written.
+        if (row8 < BM) {
+            const int in = row % WM;
+            const int r = i0 + row - in + (in & 15) * FM + (in >> 4);
+            src[l] = p + (int64_t)(r < sh.rp ? r : sh.rp - 1) * k_len + ch;
+        } else {
+            const int at = row - BM, in = at & (4 * kRow - 1);
+            const int r = j0 + at - in + ((in & 12) >> 2) * kRow + (in >> 4) * 4 + (in & 3);
+            src[l] = q + (int64_t)(r < q_rows ? r : q_rows - 1) * k_len + ch;
         }
-        __syncthreads();
+    }
+    auto stage = [&](int buf, int k0) {
 #pragma unroll
-        for (int kk = 0; kk < kTile; kk += 32) {
-            half8 fa[2], fb[2];
-            const int ko = kk + (lane >> 4) * 8;
+        for (int l = 0; l < kLoads; ++l)
+            __builtin_amdgcn_global_load_lds(
+                (const __attribute__((address_space(1))) void*)(src[l] + k0),
+                (__attribute__((address_space(3))) void*)(lds + buf * T::kStage +
+                                                          (l * kWaves + wv) * 8 * kTile),
+                16, 0, 0);
+    };
+
+    float4v acc[FM][FN] = {};
+    const int steps = k_len / kTile;
+    // Past the end the last step is brought again, so that every wait counts
+    // the same loads; nothing reads it.
+    auto at = [&](int k) { return (k < steps ? k : steps - 1) * kTile; };
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                fa[t] = *(const half8*)(lp + (wi + t * 16 + (lane & 15)) * LD + ko);
-                fb[t] = *(const half8*)(lq + (wj + t * 16 + (lane & 15)) * LD + ko);
-            }
+    for (int k = 0; k < T::STAGES - 1; ++k) stage(k, at(k));
+    int buf = 0;
+    for (int k = 0; k < steps; ++k) {
+        // This stage's loads have landed in every wave, and every wave has read
+        // the stage before, whose place the next loads take.
+        wait_stage<(T::STAGES - 2) * kLoads>();
+        stage(buf == 0 ? T::STAGES - 1 : buf - 1, at(k + T::STAGES - 1));
+        const _Float16* lp = lds + buf * T::kStage + (wi + (lane & 15)) * kTile;
+        const _Float16* lq = lds + buf * T::kStage + (BM + wj + (lane & 15)) * kTile;
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+        for (int kk = 0; kk < 2; ++kk) {
+            half8 fa[FM], fb[FN];
+            const int ch = ((kk * 4 + (lane >> 4)) ^ (lane & 7)) * 8;
 #pragma unroll
-                for (int y = 0; y < 2; ++y)
-                    acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fa[x], fb[y], acc[x][y], 0,
+            for (int x = 0; x < FM; ++x) fa[x] = *(const half8*)(lp + x * 16 * kTile + ch);
+#pragma unroll
+            for (int y = 0; y < FN; ++y) fb[y] = *(const half8*)(lq + y * 16 * kTile + ch);
+#pragma unroll
+            for (int x = 0; x < FM; ++x)
+#pragma unroll
+                for (int y = 0; y < FN; ++y)
+                    acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[y], fa[x], acc[x][y], 0,
                                                                        0, 0);
         }
+        buf = buf + 1 == T::STAGES ? 0 : buf + 1;
     }
+    wait_loads<0>();
+    // The tile's results, row by row and then, from the same registers, column
+    // by column.  `whole`: no part of the tile lies past the matrix.
+    const int ib = i0 + wi + (lane & 15) * FM, jb = j0 + wj + (lane >> 4) * kRow;
+    auto finish = [&](auto whole) {
+        constexpr bool kWhole = decltype(whole)::value;
+        const int i_end = MODE >= kOut ? sh.r : sh.rp;
+        const int j_end = MODE >= kOut ? sh.c : q_rows;
+        const int64_t ob = z * sh.m * sh.n;
+        typedef typename OutType<MODE>::type O;
+        O* const out = (O*)st.out + ob;
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+        for (int x = 0; x < FM; ++x)
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
+            for (int y = 0; y < FN; y += kRow / 4) {
+                const int i = ib + x, j = jb + y * 16;
+                if (!kWhole && (i >= sh.rp || j >= q_rows)) continue;
+                float v[kRow];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = i0 + wi + x * 16 + (lane >> 4) * 4 + e;
-                const int j = j0 + wj + y * 16 + (lane & 15);
-                const float v = acc[x][y][e];
+                for (int e = 0; e < kRow; ++e) v[e] = acc[x][y + e / 4][e & 3];
                 if (MODE == kGram || MODE == kPoly) {
                     const int64_t o = z * na + (int64_t)i * sh.rp + j;
-                    const _Float16 h =
-                        MODE == kGram
-                            ? (_Float16)(v * (kAScale / (kXScale * kXScale)))
-                            : (_Float16)(st.b * (float)w.a16[o] + st.c * (v / kAScale));
-                    _Float16* d = MODE == kGram ? w.a16 : w.b16;
-                    d[o] = h;
-                    d[z * na + (int64_t)j * sh.rp + i] = h;
+                    float a8[kRow];
+                    if (MODE == kPoly) load_v<_Float16, kRow>(w.a16 + o, a8);
+#pragma unroll
+                    for (int e = 0; e < kRow; ++e)
+                        v[e] = MODE == kGram ? v[e] * (kAScale / (kXScale * kXScale))
+                                             : st.b * a8[e] + st.c * (v[e] / kAScale);
+                    store_v<_Float16, kRow>((MODE == kGram ? w.a16 : w.b16) + o, v);
                 } else {
                     const int64_t o = z * nx + (int64_t)i * sh.cp + j;
-                    const float xn = st.a * w.x32[o] + v / (kAScale * kXScale);
+                    float4v xo[kRow / 4];
+#pragma unroll
+                    for (int e = 0; e < kRow; e += 4) xo[e / 4] = *(const float4v*)(w.x32 + o + e);
+#pragma unroll
+                    for (int e = 0; e < kRow; ++e)
+                        v[e] = st.a * xo[e / 4][e & 3] + v[e] / (kAScale * kXScale);
                     if (MODE == kNext) {
-                        const _Float16 h = (_Float16)(xn * kXScale);
-                        w.x32[o] = xn;
-                        w.x16[o] = h;
-                        w.xt[from ^ 1][z * nx + (int64_t)j * sh.rp + i] = h;
-                    } else if (i < sh.r && j < sh.c) {
-                        const int64_t d = z * sh.m * sh.n + (sh.flip ? (int64_t)j * sh.r + i
-                                                                     : (int64_t)i * sh.c + j);
-                        if (MODE == kOut)
-                            ((__bf16*)st.out)[d] = (__bf16)xn;
-                        else if (MODE == kParam32)
-                            ((float*)st.out)[d] = st.keep * ((float*)st.out)[d] - st.move * xn;
-                        else
-                            ((__bf16*)st.out)[d] =
-                                (__bf16)(st.keep * (float)((__bf16*)st.out)[d] - st.move * xn);
+#pragma unroll
+                        for (int e = 0; e < kRow; ++e) {
+                            xo[e / 4][e & 3] = v[e];
+                            v[e] *= kXScale;
+                        }
+#pragma unroll
+                        for (int e = 0; e < kRow; e += 4) *(float4v*)(w.x32 + o + e) = xo[e / 4];
+                        store_v<_Float16, kRow>(w.x16 + o, v);
+                    } else if (!sh.flip) {
+                        O* d = out + (int64_t)i * sh.c + j;
+                        if (kWhole || (i < i_end && j + kRow <= j_end)) {
+                            write_out<MODE, kRow>(d, v, st);
+                        } else if (i < i_end) {
+                            for (int e = 0; e < kRow; ++e)
+                                if (j + e < j_end) {
+                                    const float one[1] = {v[e]};
+                                    write_out<MODE, 1>(d + e, one, st);
+                                }
+                        }
                     }
                 }
+#pragma unroll
+                for (int e = 0; e < kRow; ++e) acc[x][y + e / 4][e & 3] = v[e];
+                // Loads of at most four such parts at once: all of them would spill.
+                if ((x * FN + y) % (4 * kRow / 4) == 0) __builtin_amdgcn_sched_barrier(0);
             }
+        if ((MODE <= kPoly && ti == tj) || (MODE >= kOut && !sh.flip)) return;
+#pragma unroll
+        for (int y = 0; y < FN; ++y)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int x = 0; x < FM; x += kCol) {
+                    const int i = ib + x;
+                    const int j = kRow == 8 ? jb + (y & ~1) * 16 + (y & 1) * 4 + e
+                                            : jb + y * 16 + e;
+                    if (!kWhole && (i >= sh.rp || j >= j_end)) continue;
+                    float v[kCol];
+#pragma unroll
+                    for (int f = 0; f < kCol; ++f) v[f] = acc[x + f][y][e];
+                    if (MODE <= kPoly)
+                        store_v<_Float16, kCol>(
+                            (MODE == kGram ? w.a16 : w.b16) + z * na + (int64_t)j * sh.rp + i, v);
+                    else if (MODE == kNext)
+                        store_v<_Float16, kCol>(w.xt[from ^ 1] + z * nx + (int64_t)j * sh.rp + i,
+                                                v);
+                    else if (kWhole || i + kCol <= i_end)
+                        write_out<MODE, kCol>(out + (int64_t)j * sh.r + i, v, st);
+                    else
+                        for (int f = 0; f < kCol; ++f)
+                            if (i + f < i_end) {
+                                const float one[1] = {v[f]};
+                                write_out<MODE, 1>(out + (int64_t)j * sh.r + i + f, one, st);
+                            }
+                }
+    };
+    if (i0 + BM <= (MODE >= kOut ? sh.r : sh.rp) && j0 + BN <= (MODE >= kOut ? sh.c : q_rows))
+        finish(std::true_type{});
+    else
+        finish(std::false_type{});
 }
 
 // ------------------------------------------------------------------ host ---
@@ -311,6 +525,58 @@ static int ns_check_config(const char* what, const spopt_ns_config& c) {
     return SPOPT_OK;
 }
 
+typedef Tiling<64, 64, 2, 2, 4> TileS4;
+typedef Tiling<64, 64, 2, 2, 2> TileS;
+typedef Tiling<128, 128, 2, 4, 4> TileM4;
+typedef Tiling<128, 128, 2, 4, 2> TileM;
+typedef Tiling<192, 192, 2, 4, 3> TileT;
+typedef Tiling<256, 256, 2, 4, 2> TileL;
+
+template <int MODE, class T>
+static int64_t ns_tiles(const NsShape& sh) {
+    const int64_t tr = ceil_div(sh.rp, T::BM), tc = ceil_div(sh.cp, T::BN);
+    return MODE <= kPoly ? tr * (tr + 1) / 2 : tr * tc;
+}
+
+template <int MODE, class T>
+static int ns_launch(const NsBuffers& w, const NsShape& sh, const NsStep& st, int from,
+                     unsigned nb, hipStream_t s) {
+    const int64_t tiles = ns_tiles<MODE, T>(sh);
+    constexpr int bytes = T::STAGES * T::kStage * (int)sizeof(_Float16);
+    if constexpr (bytes > 64 * 1024) {
+        SPOPT_HIP(hipFuncSetAttribute((const void*)k_ns_gemm<MODE, T>,
+                                      hipFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    }
+    k_ns_gemm<MODE, T><<<(unsigned)(tiles * nb), T::kThreads, bytes, s>>>(w, sh, st, from,
+                                                                        (int)tiles);
+    SPOPT_LAUNCHED();
+    return SPOPT_OK;
+}
+
+// The tiling whose rounds over the 256 CUs take least.  An inner step of 64
+// takes a tile of 64, 128, 192 and 256 about 0.2, 0.5, 1.1 and 1.8 us of its CU
+// (measured on products that fill the card).  Large tiles read less for each
+// product, small ones leave fewer CUs idle, and where each CU has one block,
+// four stages in LDS beat two: 1024 x 1024 by 64 tiles 150 against 184 us for
+// the whole iteration, 2048 x 2048 by 128 tiles 382 against 417 us; with
+// several blocks a CU they lose (4096 x 4096 by 128: 2083 against 1872 us).
+template <int MODE>
+static int ns_product(const NsBuffers& w, const NsShape& sh, const NsStep& st, int from,
+                      unsigned nb, hipStream_t s) {
+    auto rounds = [&](int64_t tiles) { return (double)ceil_div(tiles * nb, 256); };
+    const double ts = rounds(ns_tiles<MODE, TileS>(sh)), tm = rounds(ns_tiles<MODE, TileM>(sh));
+    const double tt = rounds(ns_tiles<MODE, TileT>(sh)), tl = rounds(ns_tiles<MODE, TileL>(sh));
+    const double best = fmin(fmin(ts * 0.2, tm * 0.5), fmin(tt * 1.1, tl * 1.8));
+    if (ts * 0.2 <= best)
+        return ts <= 2 ? ns_launch<MODE, TileS4>(w, sh, st, from, nb, s)
+                       : ns_launch<MODE, TileS>(w, sh, st, from, nb, s);
+    if (tm * 0.5 <= best)
+        return tm <= 1 ? ns_launch<MODE, TileM4>(w, sh, st, from, nb, s)
+                       : ns_launch<MODE, TileM>(w, sh, st, from, nb, s);
+    if (tt * 1.1 <= best) return ns_launch<MODE, TileT>(w, sh, st, from, nb, s);
+    return ns_launch<MODE, TileL>(w, sh, st, from, nb, s);
+}
+
 template <class G>
 static int ns_run(const NsShape& sh, Source<G> u, float* buf, const spopt_ns_config& c,
                   NsBuffers w, int last, NsStep st, hipStream_t s) {
@@ -321,9 +587,10 @@ static int ns_run(const NsShape& sh, Source<G> u, float* buf, const spopt_ns_con
     st.b = (float)c.coef[1];
     st.c = (float)c.coef[2];
     const int tr = sh.rp / kTile, tc = sh.cp / kTile;
-    // The batch is the grid's last axis, at most 65535 matrices at a time.
-    for (int64_t z0 = 0; z0 < sh.batch; z0 += 65535) {
-        const unsigned nb = (unsigned)(sh.batch - z0 < 65535 ? sh.batch - z0 : 65535);
+    // The batch in the grids' last axis: at most so many matrices at a time.
+    const int64_t chunk = 32768;
+    for (int64_t z0 = 0; z0 < sh.batch; z0 += chunk) {
+        const unsigned nb = (unsigned)(sh.batch - z0 < chunk ? sh.batch - z0 : chunk);
         const int64_t nx = (int64_t)sh.rp * sh.cp, na = (int64_t)sh.rp * sh.rp;
         NsBuffers v = w;
         v.part += z0 * kNormParts;
@@ -345,18 +612,14 @@ static int ns_run(const NsShape& sh, Source<G> u, float* buf, const spopt_ns_con
         SPOPT_LAUNCHED();
         for (int k = 0; k < c.steps; ++k) {
             const int from = k & 1;
-            k_ns_gemm<kGram><<<dim3(tr, tr, nb), 256, 0, s>>>(v, sh, sz, from);
-            k_ns_gemm<kPoly><<<dim3(tr, tr, nb), 256, 0, s>>>(v, sh, sz, from);
-            const dim3 gx(tc, tr, nb);
-            if (k + 1 < c.steps)
-                k_ns_gemm<kNext><<<gx, 256, 0, s>>>(v, sh, sz, from);
-            else if (last == kOut)
-                k_ns_gemm<kOut><<<gx, 256, 0, s>>>(v, sh, sz, from);
-            else if (last == kParam32)
-                k_ns_gemm<kParam32><<<gx, 256, 0, s>>>(v, sh, sz, from);
-            else
-                k_ns_gemm<kParam16><<<gx, 256, 0, s>>>(v, sh, sz, from);
-            SPOPT_LAUNCHED();
+            int rc = ns_product<kGram>(v, sh, sz, from, nb, s);
+            if (!rc) rc = ns_product<kPoly>(v, sh, sz, from, nb, s);
+            if (!rc)
+                rc = k + 1 < c.steps    ? ns_product<kNext>(v, sh, sz, from, nb, s)
+                     : last == kOut     ? ns_product<kOut>(v, sh, sz, from, nb, s)
+                     : last == kParam32 ? ns_product<kParam32>(v, sh, sz, from, nb, s)
+                                        : ns_product<kParam16>(v, sh, sz, from, nb, s);
+            if (rc) return rc;
         }
     }
     return SPOPT_OK;
