@@ -3,21 +3,20 @@
 // With X the r x c iterate (r <= c, the input transposed where it is taller
 // than wide), one step is three products:
 //   A = X X^T,   B = b A + c A A,   X <- a X + B X.
-// Every product is written as P Q^T with both operands' inner axis adjacent,
-// which is what the matrix cores' operands take: A from the rows of X, A A
-// from the rows of A (A is symmetric), B X from the rows of X^T, which the
-// kernel that writes X writes as well.
+// The first two are P P^T with the inner axis adjacent in memory, which is what
+// the matrix cores' operands take (A is symmetric); of their symmetric results
+// the lower tiles are computed and mirrored.  For B X the inner axis runs along
+// X's columns: its operand is turned as it is read from LDS.
 //
 // Types.  The operands are float16 and the sums float32.  float16 carries 11
 // bits against bfloat16's 8 at the same rate; its range is met by powers of
 // two in front: X * 2^8, A and B * 2^12 (entries are bounded by the largest
-// singular value, which the host checks).  X is also kept in float32 for the
-// a X term: in the directions of small singular values B is near zero, so
-// rounding errors of X there would come in through a X alone, and grow by
-// a factor of a in every step.  Errors against 64 bits, relative to the
-// result's norm, for 256 to 1024 rows and Gaussian, low-rank and decaying
-// spectra: at most 1.7e-3 so; 7e-3 with X in float16 alone, 6e-2 with all of
-// it in bfloat16.
+// singular value, which the host checks).  X is also carried in float32, for the
+// a X term: in the directions of small singular values B is near zero, so that
+// rounding errors of X come in through a X alone there, and grow by a factor of
+// a in every step.  Errors against 64 bits, relative to the result's norm, for
+// 256 to 1024 rows and Gaussian, low-rank and decaying spectra: at most 1.7e-3;
+// 7e-3 with X in float16 alone, 6e-2 with all of it in bfloat16.
 #include <math.h>
 
 #include <type_traits>
@@ -98,9 +97,8 @@ __global__ __launch_bounds__(256) void k_ns_norm(Source<G> u, float* buf, int64_
 }
 
 struct NsBuffers {
-    float* x32;      // [batch][rp * cp]
-    _Float16* x16;   // [batch][rp * cp]   X * 2^8
-    _Float16* xt[2]; // [batch][cp * rp]   X^T * 2^8
+    _Float16* x[2];  // [batch][rp * cp]   X * 2^8, one step's and the next's
+    float* x32;      // [batch][rp * cp]   X * 2^8
     _Float16* a16;   // [batch][rp * rp]   A * 2^12
     _Float16* b16;   // [batch][rp * rp]   B * 2^12
     double* part;    // [batch][kNormParts]
@@ -125,34 +123,42 @@ __global__ __launch_bounds__(256) void k_ns_init(Source<G> u, NsBuffers w, NsSha
     const int64_t base = z * sh.m * sh.n;
     // All of the thread's values are asked for first, along the input's rows
     // (those of X, or X's columns).
-    float v[kTile / 4];
+    int64_t at[kTile / 4];
+    bool in[kTile / 4];
 #pragma unroll
     for (int t = 0; t < kTile / 4; ++t) {
         const int a = 4 * t + k;
         const int i = sh.flip ? i0 + q : i0 + a, j = sh.flip ? j0 + a : j0 + q;
-        const bool in = i < sh.r && j < sh.c;
-        const float x = u.at(base + (in ? sh.flip ? (int64_t)j * sh.r + i
-                                                  : (int64_t)i * sh.c + j : 0));
-        v[t] = in ? x : 0.f;
+        in[t] = i < sh.r && j < sh.c;
+        at[t] = base + (in[t] ? sh.flip ? (int64_t)j * sh.r + i : (int64_t)i * sh.c + j : 0);
+    }
+    float v[kTile / 4] = {}, b[kTile / 4];
+    if (u.kind != 1)
+#pragma unroll
+        for (int t = 0; t < kTile / 4; ++t) v[t] = (float)u.g[at[t]];
+    if (u.kind != 0) {
+#pragma unroll
+        for (int t = 0; t < kTile / 4; ++t) b[t] = u.buf[at[t]];
+#pragma unroll
+        for (int t = 0; t < kTile / 4; ++t) v[t] = u.kind == 1 ? b[t] : v[t] + u.mu * b[t];
     }
     double sq = 0.;
     for (int t = threadIdx.x; t < parts; t += 256) sq += w.part[z * kNormParts + t];
-    const double scale = 1.0 / (sqrt(block_sum_d(sq, lds)) + eps);
+    const double scale = (double)kXScale / (sqrt(block_sum_d(sq, lds)) + eps);
 #pragma unroll
     for (int t = 0; t < kTile / 4; ++t) {
-        const float x = (float)((double)v[t] * scale);
-        if (sh.flip)
-            tile[q][4 * t + k] = x;
-        else
-            tile[4 * t + k][q] = x;
+        v[t] = in[t] ? (float)((double)v[t] * scale) : 0.f;
+        if (sh.flip) tile[q][4 * t + k] = v[t];
     }
     __syncthreads();
     const int64_t xb = z * sh.rp * sh.cp;
-    for (int t = k; t < kTile; t += 4) {
-        const int64_t o = xb + (int64_t)(i0 + t) * sh.cp + j0 + q;
-        w.x32[o] = tile[t][q];
-        w.x16[o] = (_Float16)(tile[t][q] * kXScale);
-        w.xt[0][xb + (int64_t)(j0 + t) * sh.rp + i0 + q] = (_Float16)(tile[q][t] * kXScale);
+#pragma unroll
+    for (int t = 0; t < kTile / 4; ++t) {
+        const int a = 4 * t + k;
+        const float x = sh.flip ? tile[a][q] : v[t];
+        const int64_t o = xb + (int64_t)(i0 + a) * sh.cp + j0 + q;
+        w.x[0][o] = (_Float16)x;
+        w.x32[o] = x;
     }
 }
 
@@ -173,6 +179,26 @@ __device__ __forceinline__ void wait_loads() {
 template <int N>
 __device__ __forceinline__ void wait_stage() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// 16 bytes a lane straight into LDS, the wave's 64 at adjacent places from `to`
+// (the same for the whole wave).  In assembly, as the compiler would wait for
+// every load that writes LDS before each transposing read of it, also of
+// another stage; wait_stage counts them instead.  No register is written.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // m0 is named as clobbered for the reader
+__device__ __forceinline__ void load_lds16(const _Float16* from, _Float16* to) {
+    const uint32_t m0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)to;
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from),
+                 "s"(m0)
+                 : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+__device__ __forceinline__ half4 read_turned(const _Float16* p) {
+    typedef short short4v __attribute__((ext_vector_type(4)));
+    return __builtin_bit_cast(half4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                         (__attribute__((address_space(3))) short4v*)p));
 }
 
 template <int MODE>
@@ -241,7 +267,7 @@ __global__ __launch_bounds__(T::kThreads) void k_ns_gemm(NsBuffers w, NsShape sh
                                                          int from, int tiles) {
     constexpr int BM = T::BM, BN = T::BN, WM = BM / T::WGM, WN = BN / T::WGN;
     constexpr int FM = WM / 16, FN = WN / 16, kWaves = T::WGM * T::WGN;
-    constexpr int kRow = FN % 2 ? 4 : 8;                            // columns of a row's store
+    constexpr int kRow = MODE >= kNext || FN % 2 ? 4 : 8;        // columns of a row's store
     constexpr int kCol = FM % 8 == 0 ? 8 : FM % 4 == 0 ? 4 : 2;  // rows of a column's store
     extern __shared__ __align__(16) char lds_raw[];
     _Float16* const lds = (_Float16*)lds_raw;
@@ -249,19 +275,18 @@ __global__ __launch_bounds__(T::kThreads) void k_ns_gemm(NsBuffers w, NsShape sh
     const int64_t z = t / tiles;
     const int tile = (int)(t % tiles);
     const int64_t nx = (int64_t)sh.rp * sh.cp, na = (int64_t)sh.rp * sh.rp;
+    constexpr bool kTurn = MODE >= kNext;  // Q's inner axis runs along its rows
     const _Float16 *p, *q;
-    int k_len, q_rows = sh.rp, ti, tj;
+    int k_len = sh.rp, j_len = sh.rp, ti, tj;
     if (MODE == kGram) {
-        p = q = w.x16 + z * nx;
+        p = q = w.x[from] + z * nx;
         k_len = sh.cp;
     } else if (MODE == kPoly) {
         p = q = w.a16 + z * na;
-        k_len = sh.rp;
     } else {
         p = w.b16 + z * na;
-        q = w.xt[from] + z * nx;
-        k_len = sh.rp;
-        q_rows = sh.cp;
+        q = w.x[from] + z * nx;
+        j_len = sh.cp;
     }
     if (MODE <= kPoly) {
         // Row ti holds tiles 0 .. ti of the lower triangle.
@@ -281,33 +306,56 @@ __global__ __launch_bounds__(T::kThreads) void k_ns_gemm(NsBuffers w, NsShape sh
     const int lane = lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wi = (wv / T::WGN) * WM, wj = (wv % T::WGN) * WN;
 
-    // Wave wv brings 8 rows at a time, every kWaves-th eight of P's and Q's.
-    constexpr int kLoads = (BM + BN) / 8 / kWaves;
-    static_assert((BM + BN) % (8 * kWaves) == 0, "rows share out evenly");
-    const _Float16* src[kLoads];
+    // A wave's load brings 64 chunks of 16 bytes to adjacent places in LDS.  Of
+    // an operand with its inner axis adjacent these are 8 rows of 8 chunks; rows
+    // past its end repeat the last one, and their products are not written.
+    constexpr int kLoadsP = BM / 8 / kWaves, kLoadsQ = BN / 8 / kWaves;
+    constexpr int kLoads = kLoadsP + kLoadsQ;
+    static_assert(BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0, "rows share out evenly");
+    const _Float16 *src_p[kLoadsP], *src_q[kLoadsQ];
+    const int ch8 = ((lane & 7) ^ (lane >> 3)) * 8;
 #pragma unroll
-    for (int l = 0; l < kLoads; ++l) {
-        const int row8 = (l * kWaves + wv) * 8, row = row8 + (lane >> 3);
-        const int ch = ((lane & 7) ^ (lane >> 3)) * 8;
-        // Rows past the operand repeat its last one; their products are not written.
-        if (row8 < BM) {
-            const int in = row % WM;
-            const int r = i0 + row - in + (in & 15) * FM + (in >> 4);
-            src[l] = p + (int64_t)(r < sh.rp ? r : sh.rp - 1) * k_len + ch;
+    for (int l = 0; l < kLoadsP; ++l) {
+        const int row = (l * kWaves + wv) * 8 + (lane >> 3), in = row % WM;
+        const int r = i0 + row - in + (in & 15) * FM + (in >> 4);
+        src_p[l] = p + (int64_t)(r < sh.rp ? r : sh.rp - 1) * k_len + ch8;
+    }
+#pragma unroll
+    for (int l = 0; l < kLoadsQ; ++l) {
+        if (kTurn) {
+            // 64 rows (the inner axis) of BN / 8 chunks, those of 16 columns
+            // at place u ^ (row & 3): see turned() below.
+            const int at = (l * kWaves + wv) * 64 + lane;
+            const int row = at / (BN / 8), slot = at % (BN / 8);
+            const int j = j0 + (((slot >> 1) ^ (row & 3)) * 2 + (slot & 1)) * 8;
+            src_q[l] = q + (int64_t)row * sh.cp + (j < sh.cp ? j : sh.cp - 8);
         } else {
-            const int at = row - BM, in = at & (4 * kRow - 1);
+            const int at = (l * kWaves + wv) * 8 + (lane >> 3), in = at & (4 * kRow - 1);
             const int r = j0 + at - in + ((in & 12) >> 2) * kRow + (in >> 4) * 4 + (in & 3);
-            src[l] = q + (int64_t)(r < q_rows ? r : q_rows - 1) * k_len + ch;
+            src_q[l] = q + (int64_t)(r < j_len ? r : j_len - 1) * k_len + ch8;
         }
     }
+    const int64_t step_q = kTurn ? (int64_t)sh.cp : 1;
     auto stage = [&](int buf, int k0) {
+        _Float16* const to = lds + buf * T::kStage;
 #pragma unroll
-        for (int l = 0; l < kLoads; ++l)
-            __builtin_amdgcn_global_load_lds(
-                (const __attribute__((address_space(1))) void*)(src[l] + k0),
-                (__attribute__((address_space(3))) void*)(lds + buf * T::kStage +
-                                                          (l * kWaves + wv) * 8 * kTile),
-                16, 0, 0);
+        for (int l = 0; l < kLoadsP; ++l) load_lds16(src_p[l] + k0, to + (l * kWaves + wv) * 512);
+#pragma unroll
+        for (int l = 0; l < kLoadsQ; ++l)
+            load_lds16(src_q[l] + k0 * step_q, to + BM * kTile + (l * kWaves + wv) * 512);
+    };
+    // Q's operand where it has to be turned: a transposing read gives each of 16
+    // lanes one column's values of 4 rows, lane i naming 4 columns of row i / 4.
+    // The rows' 32-byte parts are laid out so that the 4 rows meet different banks.
+    int turn[FN];
+#pragma unroll
+    for (int y = 0; y < FN; ++y)
+        turn[y] = ((lane >> 4) * 8 + ((lane & 15) >> 2)) * BN +
+                  ((wj / 16 + y) ^ ((lane & 15) >> 2)) * 16 + (lane & 3) * 4;
+    auto turned = [&](const _Float16* lq, int kk, int y) {
+        const half4 a = read_turned(lq + turn[y] + kk * 32 * BN);
+        const half4 b = read_turned(lq + turn[y] + (kk * 32 + 4) * BN);
+        return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
     };
 
     float4v acc[FM][FN] = {};
@@ -324,7 +372,7 @@ __global__ __launch_bounds__(T::kThreads) void k_ns_gemm(NsBuffers w, NsShape sh
         wait_stage<(T::STAGES - 2) * kLoads>();
         stage(buf == 0 ? T::STAGES - 1 : buf - 1, at(k + T::STAGES - 1));
         const _Float16* lp = lds + buf * T::kStage + (wi + (lane & 15)) * kTile;
-        const _Float16* lq = lds + buf * T::kStage + (BM + wj + (lane & 15)) * kTile;
+        const _Float16* lq = lds + buf * T::kStage + BM * kTile;
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
             half8 fa[FM], fb[FN];
@@ -332,7 +380,9 @@ __global__ __launch_bounds__(T::kThreads) void k_ns_gemm(NsBuffers w, NsShape sh
 #pragma unroll
             for (int x = 0; x < FM; ++x) fa[x] = *(const half8*)(lp + x * 16 * kTile + ch);
 #pragma unroll
-            for (int y = 0; y < FN; ++y) fb[y] = *(const half8*)(lq + y * 16 * kTile + ch);
+            for (int y = 0; y < FN; ++y)
+                fb[y] = kTurn ? turned(lq, kk, y)
+                              : *(const half8*)(lq + (wj + y * 16 + (lane & 15)) * kTile + ch);
 #pragma unroll
             for (int x = 0; x < FM; ++x)
 #pragma unroll
@@ -349,7 +399,7 @@ __global__ __launch_bounds__(T::kThreads) void k_ns_gemm(NsBuffers w, NsShape sh
     auto finish = [&](auto whole) {
         constexpr bool kWhole = decltype(whole)::value;
         const int i_end = MODE >= kOut ? sh.r : sh.rp;
-        const int j_end = MODE >= kOut ? sh.c : q_rows;
+        const int j_end = MODE >= kOut ? sh.c : j_len;
         const int64_t ob = z * sh.m * sh.n;
         typedef typename OutType<MODE>::type O;
         O* const out = (O*)st.out + ob;
@@ -358,7 +408,7 @@ __global__ __launch_bounds__(T::kThreads) void k_ns_gemm(NsBuffers w, NsShape sh
 #pragma unroll
             for (int y = 0; y < FN; y += kRow / 4) {
                 const int i = ib + x, j = jb + y * 16;
-                if (!kWhole && (i >= sh.rp || j >= q_rows)) continue;
+                if (!kWhole && (i >= sh.rp || j >= j_len)) continue;
                 float v[kRow];
 #pragma unroll
                 for (int e = 0; e < kRow; ++e) v[e] = acc[x][y + e / 4][e & 3];
@@ -373,22 +423,19 @@ __global__ __launch_bounds__(T::kThreads) void k_ns_gemm(NsBuffers w, NsShape sh
                     store_v<_Float16, kRow>((MODE == kGram ? w.a16 : w.b16) + o, v);
                 } else {
                     const int64_t o = z * nx + (int64_t)i * sh.cp + j;
-                    float4v xo[kRow / 4];
+                    float x0[kRow];
+                    load_v<float, kRow>(w.x32 + o, x0);
+                    // X * 2^8 of the next step
 #pragma unroll
-                    for (int e = 0; e < kRow; e += 4) xo[e / 4] = *(const float4v*)(w.x32 + o + e);
-#pragma unroll
-                    for (int e = 0; e < kRow; ++e)
-                        v[e] = st.a * xo[e / 4][e & 3] + v[e] / (kAScale * kXScale);
+                    for (int e = 0; e < kRow; ++e) v[e] = st.a * x0[e] + v[e] / kAScale;
                     if (MODE == kNext) {
+                        store_v<float, kRow>(w.x32 + o, v);
+                        store_v<_Float16, kRow>(w.x[from ^ 1] + o, v);
+                        continue;
+                    }
 #pragma unroll
-                        for (int e = 0; e < kRow; ++e) {
-                            xo[e / 4][e & 3] = v[e];
-                            v[e] *= kXScale;
-                        }
-#pragma unroll
-                        for (int e = 0; e < kRow; e += 4) *(float4v*)(w.x32 + o + e) = xo[e / 4];
-                        store_v<_Float16, kRow>(w.x16 + o, v);
-                    } else if (!sh.flip) {
+                    for (int e = 0; e < kRow; ++e) v[e] /= kXScale;
+                    if (!sh.flip) {
                         O* d = out + (int64_t)i * sh.c + j;
                         if (kWhole || (i < i_end && j + kRow <= j_end)) {
                             write_out<MODE, kRow>(d, v, st);
@@ -406,7 +453,7 @@ __global__ __launch_bounds__(T::kThreads) void k_ns_gemm(NsBuffers w, NsShape sh
                 // Loads of at most four such parts at once: all of them would spill.
                 if ((x * FN + y) % (4 * kRow / 4) == 0) __builtin_amdgcn_sched_barrier(0);
             }
-        if ((MODE <= kPoly && ti == tj) || (MODE >= kOut && !sh.flip)) return;
+        if ((MODE <= kPoly && ti == tj) || MODE == kNext || (MODE >= kOut && !sh.flip)) return;
 #pragma unroll
         for (int y = 0; y < FN; ++y)
 #pragma unroll
@@ -423,9 +470,6 @@ __global__ __launch_bounds__(T::kThreads) void k_ns_gemm(NsBuffers w, NsShape sh
                     if (MODE <= kPoly)
                         store_v<_Float16, kCol>(
                             (MODE == kGram ? w.a16 : w.b16) + z * na + (int64_t)j * sh.rp + i, v);
-                    else if (MODE == kNext)
-                        store_v<_Float16, kCol>(w.xt[from ^ 1] + z * nx + (int64_t)j * sh.rp + i,
-                                                v);
                     else if (kWhole || i + kCol <= i_end)
                         write_out<MODE, kCol>(out + (int64_t)j * sh.r + i, v, st);
                     else
@@ -436,7 +480,7 @@ __global__ __launch_bounds__(T::kThreads) void k_ns_gemm(NsBuffers w, NsShape sh
                             }
                 }
     };
-    if (i0 + BM <= (MODE >= kOut ? sh.r : sh.rp) && j0 + BN <= (MODE >= kOut ? sh.c : q_rows))
+    if (i0 + BM <= (MODE >= kOut ? sh.r : sh.rp) && j0 + BN <= (MODE >= kOut ? sh.c : j_len))
         finish(std::true_type{});
     else
         finish(std::false_type{});
@@ -467,10 +511,9 @@ static size_t ns_layout(const NsShape& s, char* base, NsBuffers* w) {
     };
     const size_t nx = (size_t)s.batch * s.rp * s.cp, na = (size_t)s.batch * s.rp * s.rp;
     w->part = (double*)take((size_t)s.batch * kNormParts * sizeof(double));
+    w->x[0] = (_Float16*)take(nx * 2);
+    w->x[1] = (_Float16*)take(nx * 2);
     w->x32 = (float*)take(nx * 4);
-    w->x16 = (_Float16*)take(nx * 2);
-    w->xt[0] = (_Float16*)take(nx * 2);
-    w->xt[1] = (_Float16*)take(nx * 2);
     w->a16 = (_Float16*)take(na * 2);
     w->b16 = (_Float16*)take(na * 2);
     return at;
@@ -594,10 +637,9 @@ static int ns_run(const NsShape& sh, Source<G> u, float* buf, const spopt_ns_con
         const int64_t nx = (int64_t)sh.rp * sh.cp, na = (int64_t)sh.rp * sh.rp;
         NsBuffers v = w;
         v.part += z0 * kNormParts;
+        v.x[0] += z0 * nx;
+        v.x[1] += z0 * nx;
         v.x32 += z0 * nx;
-        v.x16 += z0 * nx;
-        v.xt[0] += z0 * nx;
-        v.xt[1] += z0 * nx;
         v.a16 += z0 * na;
         v.b16 += z0 * na;
         Source<G> uz = u;
