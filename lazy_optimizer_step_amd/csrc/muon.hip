@@ -9,9 +9,11 @@
 // X's columns: its operand is turned as it is read from LDS.
 //
 // Types.  The operands are float16 and the sums float32.  float16 carries 11
-// bits against bfloat16's 8 at the same rate; its range is met by powers of
-// two in front: X * 2^8, A and B * 2^12 (entries are bounded by the largest
-// singular value, which the host checks).  X is also carried in float32, for the
+// bits against bfloat16's 8 at the same rate; its range is met by X * 2^6, of
+// which A * 2^12 follows without a factor, and B as it is: entries of B below
+// float16's normal range are off by 2^-25 at most, which a X is not changed by
+// (entries are bounded by the largest singular value, which the host checks).
+// X is also carried in float32, for the
 // a X term: in the directions of small singular values B is near zero, so that
 // rounding errors of X come in through a X alone there, and grow by a factor of
 // a in every step.  Errors against 64 bits, relative to the result's norm, for
@@ -30,8 +32,8 @@ typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef float float4v __attribute__((ext_vector_type(4)));
 
 constexpr int kTile = 64;                    // rows, columns and inner axis are padded to it
-constexpr float kXScale = 256.f;             // 2^8
-constexpr float kAScale = 4096.f;            // 2^12
+constexpr float kXScale = 64.f;              // 2^6
+constexpr float kAScale = kXScale * kXScale; // 2^12
 constexpr int kNormParts = 1024;             // partial sums of a matrix's norm, at most
 
 // The matrix U that a call orthogonalises, formed as it is read.
@@ -97,10 +99,10 @@ __global__ __launch_bounds__(256) void k_ns_norm(Source<G> u, float* buf, int64_
 }
 
 struct NsBuffers {
-    _Float16* x[2];  // [batch][rp * cp]   X * 2^8, one step's and the next's
-    float* x32;      // [batch][rp * cp]   X * 2^8
+    _Float16* x[2];  // [batch][rp * cp]   X * 2^6, one step's and the next's
+    float* x32;      // [batch][rp * cp]   X * 2^6
     _Float16* a16;   // [batch][rp * rp]   A * 2^12
-    _Float16* b16;   // [batch][rp * rp]   B * 2^12
+    _Float16* b16;   // [batch][rp * rp]   B
     double* part;    // [batch][kNormParts]
 };
 
@@ -184,21 +186,28 @@ __device__ __forceinline__ void wait_stage() {
 // 16 bytes a lane straight into LDS, the wave's 64 at adjacent places from `to`
 // (the same for the whole wave).  In assembly, as the compiler would wait for
 // every load that writes LDS before each transposing read of it, also of
-// another stage; wait_stage counts them instead.  No register is written.
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"  // m0 is named as clobbered for the reader
+// another stage; wait_stage counts them instead.  No register is written but
+// m0, which the compiler never keeps a value in.
 __device__ __forceinline__ void load_lds16(const _Float16* from, _Float16* to) {
     const uint32_t m0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)to;
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from),
                  "s"(m0)
-                 : "memory", "m0");
+                 : "memory");
 }
-#pragma clang diagnostic pop
 
 __device__ __forceinline__ half4 read_turned(const _Float16* p) {
     typedef short short4v __attribute__((ext_vector_type(4)));
     return __builtin_bit_cast(half4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                                          (__attribute__((address_space(3))) short4v*)p));
+}
+
+// Where row `row` of BN values has its 32-byte part u in LDS: at u ^ turn_q(row).
+// Rows r .. r + 3 and r + 8 .. r + 11 (or r + 16 .. r + 19) then lie in different
+// eighths of the 256 bytes that LDS gives a cycle.
+template <int BN>
+__device__ __forceinline__ int turn_q(int row) {
+    const int far = (row >> 3 ^ row >> 4) & 1;
+    return BN % 128 == 0 ? (row & 3) | far << 2 : (row >> 1 & 1) | far << 1;
 }
 
 template <int MODE>
@@ -324,10 +333,10 @@ __global__ __launch_bounds__(T::kThreads) void k_ns_gemm(NsBuffers w, NsShape sh
     for (int l = 0; l < kLoadsQ; ++l) {
         if (kTurn) {
             // 64 rows (the inner axis) of BN / 8 chunks, those of 16 columns
-            // at place u ^ (row & 3): see turned() below.
+            // at place u ^ turn_q(row): see turned() below.
             const int at = (l * kWaves + wv) * 64 + lane;
             const int row = at / (BN / 8), slot = at % (BN / 8);
-            const int j = j0 + (((slot >> 1) ^ (row & 3)) * 2 + (slot & 1)) * 8;
+            const int j = j0 + (((slot >> 1) ^ turn_q<BN>(row)) * 2 + (slot & 1)) * 8;
             src_q[l] = q + (int64_t)row * sh.cp + (j < sh.cp ? j : sh.cp - 8);
         } else {
             const int at = (l * kWaves + wv) * 8 + (lane >> 3), in = at & (4 * kRow - 1);
@@ -346,12 +355,14 @@ __global__ __launch_bounds__(T::kThreads) void k_ns_gemm(NsBuffers w, NsShape sh
     };
     // Q's operand where it has to be turned: a transposing read gives each of 16
     // lanes one column's values of 4 rows, lane i naming 4 columns of row i / 4.
-    // The rows' 32-byte parts are laid out so that the 4 rows meet different banks.
+    // The rows' 32-byte parts are laid out so that the 8 rows of 32 lanes meet
+    // different banks of the 64.
     int turn[FN];
 #pragma unroll
-    for (int y = 0; y < FN; ++y)
-        turn[y] = ((lane >> 4) * 8 + ((lane & 15) >> 2)) * BN +
-                  ((wj / 16 + y) ^ ((lane & 15) >> 2)) * 16 + (lane & 3) * 4;
+    for (int y = 0; y < FN; ++y) {
+        const int row = (lane >> 4) * 8 + ((lane & 15) >> 2);  // and 4, 32, 36 on: turned alike
+        turn[y] = row * BN + ((wj / 16 + y) ^ turn_q<BN>(row)) * 16 + (lane & 3) * 4;
+    }
     auto turned = [&](const _Float16* lq, int kk, int y) {
         const half4 a = read_turned(lq + turn[y] + kk * 32 * BN);
         const half4 b = read_turned(lq + turn[y] + (kk * 32 + 4) * BN);
@@ -418,16 +429,16 @@ __global__ __launch_bounds__(T::kThreads) void k_ns_gemm(NsBuffers w, NsShape sh
                     if (MODE == kPoly) load_v<_Float16, kRow>(w.a16 + o, a8);
 #pragma unroll
                     for (int e = 0; e < kRow; ++e)
-                        v[e] = MODE == kGram ? v[e] * (kAScale / (kXScale * kXScale))
-                                             : st.b * a8[e] + st.c * (v[e] / kAScale);
+                        if (MODE == kPoly)
+                            v[e] = st.b / kAScale * a8[e] + st.c / (kAScale * kAScale) * v[e];
                     store_v<_Float16, kRow>((MODE == kGram ? w.a16 : w.b16) + o, v);
                 } else {
                     const int64_t o = z * nx + (int64_t)i * sh.cp + j;
                     float x0[kRow];
                     load_v<float, kRow>(w.x32 + o, x0);
-                    // X * 2^8 of the next step
+                    // X * 2^6 of the next step
 #pragma unroll
-                    for (int e = 0; e < kRow; ++e) v[e] = st.a * x0[e] + v[e] / kAScale;
+                    for (int e = 0; e < kRow; ++e) v[e] = st.a * x0[e] + v[e];
                     if (MODE == kNext) {
                         store_v<float, kRow>(w.x32 + o, v);
                         store_v<_Float16, kRow>(w.x[from ^ 1] + o, v);
@@ -486,6 +497,300 @@ __global__ __launch_bounds__(T::kThreads) void k_ns_gemm(NsBuffers w, NsShape sh
         finish(std::false_type{});
 }
 
+// ------------------------------------------------------- small matrices ---
+
+// A matrix whose X fits one CU, from the gradient to the result in one launch:
+// one block of 8 or 16 waves each.  X lives in registers in float32 (wave v holds all
+// rows of 16 FN columns) and in LDS in float16, A and then B in LDS; the norm
+// is summed, and the momentum moved, as the values are first read.  Padded to
+// 16 R rows (R = 4 or 8) and 16 W FN columns of W waves; R FN <= 16, as the
+// rest of the step needs registers too.
+//
+// LDS rows (X's of 16 W FN values, A's of 128) are laid out with chunk c of 8
+// values of row i at c ^ turn_of(i): the 16 rows of an operand, and the 8 rows
+// that half a wave's transposing read takes, meet different banks of the 64.
+struct SmallRun {
+    int kind;          // as Source
+    int gbf16, mode;   // the gradient's type; kOut, kParam32 or kParam16
+    const void* g;
+    float* buf;
+    float mu;
+    double eps;
+    int steps;
+};
+
+__device__ __forceinline__ int turn_of(int row) {
+    return (((row & 7) ^ ((row >> 1) & 4)) << 1) | ((row >> 3) & 1);  // of row % 16
+}
+
+template <int R, int FN, int W>
+__global__ __launch_bounds__(64 * W) void k_ns_small(SmallRun u, NsShape sh, NsStep st) {
+    constexpr int kX = 16 * W * FN, kA = 128;
+    extern __shared__ __align__(16) char lds_raw[];
+    _Float16* const lx = (_Float16*)lds_raw;
+    _Float16* const la = lx + 16 * R * kX;
+    const int lane = lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l15 = lane & 15, g4 = lane >> 4;
+    const int wj = wv * 16 * FN;
+    const int64_t base = (int64_t)blockIdx.x * sh.m * sh.n;
+    float* const buf = u.buf + (u.kind ? base : 0);
+    // Value e of part (x, y): row 16 x + l15, column wj + 16 y + 4 g4 + e, and
+    // where it lies in the input (fewer than 2^16 values).
+    float4v xv[R][FN];
+    const uint32_t di = sh.flip ? 1 : sh.c, dj = sh.flip ? sh.r : 1;
+    auto index = [&](int x, int y, int e, bool* in) {
+        const int i = 16 * x + l15, j = wj + 16 * y + 4 * g4 + e;
+        *in = i < sh.r && j < sh.c;
+        return *in ? (uint32_t)i * di + (uint32_t)j * dj : 0u;
+    };
+    // Four adjacent columns at once where the rows allow it.
+    const bool by_four = !sh.flip && sh.c % 4 == 0;
+    auto read_row = [&](const auto* from, int x, auto four, float4v (&v)[FN]) {
+        typedef std::remove_cv_t<std::remove_reference_t<decltype(*from)>> E;
+        bool in;
+#pragma unroll
+        for (int y = 0; y < FN; ++y) {
+            if constexpr (decltype(four)::value) {
+                float q[4];
+                load_v<E, 4>(from + index(x, y, 0, &in), q);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[y][e] = in ? q[e] : 0.f;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float q = (float)from[index(x, y, e, &in)];
+                    v[y][e] = in ? q : 0.f;
+                }
+            }
+        }
+    };
+    auto read_all = [&](const auto* from, auto four) {
+        // One row of parts at a time: all in flight would need too many registers.
+#pragma unroll
+        for (int x = 0; x < R; ++x) {
+            read_row(from, x, four, xv[x]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (u.kind == 0) return;
+#pragma unroll
+        for (int x = 0; x < R; ++x) {
+            float4v b[FN];
+            read_row(buf, x, four, b);
+#pragma unroll
+            for (int y = 0; y < FN; ++y) {
+                b[y] = u.mu * b[y] + xv[x][y];
+                xv[x][y] = u.kind == 1 ? b[y] : xv[x][y] + u.mu * b[y];
+                bool in;
+                if constexpr (decltype(four)::value) {
+                    const uint32_t o = index(x, y, 0, &in);
+                    const float q[4] = {b[y][0], b[y][1], b[y][2], b[y][3]};
+                    if (in) store_v<float, 4>(buf + o, q);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t o = index(x, y, e, &in);
+                        if (in) buf[o] = b[y][e];
+                    }
+                }
+            }
+        }
+    };
+    if (by_four) {
+        if (u.gbf16)
+            read_all((const __bf16*)u.g + base, std::true_type{});
+        else
+            read_all((const float*)u.g + base, std::true_type{});
+    } else {
+        if (u.gbf16)
+            read_all((const __bf16*)u.g + base, std::false_type{});
+        else
+            read_all((const float*)u.g + base, std::false_type{});
+    }
+    {
+        double sq = 0.;
+#pragma unroll
+        for (int x = 0; x < R; ++x)
+#pragma unroll
+            for (int y = 0; y < FN; ++y)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sq += (double)xv[x][y][e] * (double)xv[x][y][e];
+        // The scale as a power of two and a factor in [0.5, 1): float32 alone
+        // would not hold every norm's reciprocal.
+        int ex;
+        const float f = (float)frexp(
+            (double)kXScale / (sqrt(block_sum_d(sq, (double*)la)) + u.eps), &ex);
+#pragma unroll
+        for (int x = 0; x < R; ++x)
+#pragma unroll
+            for (int y = 0; y < FN; ++y)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) xv[x][y][e] = ldexpf(xv[x][y][e], ex) * f;
+    }
+    const int c32 = (sh.c + 63) / 64 * 2;  // inner steps of A: columns past them are zero
+    for (int k = 0; k < u.steps; ++k) {
+        // Said to change here, so that the places in LDS are worked out anew in
+        // each step: kept over the loop they would not fit the registers.
+        int ln = lane;
+        asm volatile("" : "+v"(ln));
+        const int l15 = ln & 15, g4 = ln >> 4, ft = turn_of(l15);
+        // 4 adjacent values of row `i` from column `j` on.
+        auto put = [&](_Float16* l, int width, int i, int j, float4v v) {
+            half4 h;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = (_Float16)v[e];
+            *(half4*)(l + i * width + (((j >> 3) ^ ft) << 3) + (j & 7)) = h;
+        };
+        // Values 8 chunk .. + 7 of row `i` (i % 16 == l15).
+        auto rows8 = [&](const _Float16* l, int width, int i, int chunk) {
+            return *(const half8*)(l + i * width + ((chunk ^ ft) << 3));
+        };
+        // A wave's part of an R x R product: rows 16 FA wr .., columns 16 FB wc ..
+        // Of 16 waves' square parts the 6 above the diagonal are mirrored ones.
+        constexpr int FA = R / 4, FB = 4 * R / W;
+        constexpr bool kMirror = W == 16;
+        const int wr = wv / (W / 4), wc = wv % (W / 4);
+        const bool mine = !kMirror || wc <= wr;
+        auto square = [&](const _Float16* l, int width, int k32, float4v (&acc)[FA][FB]) {
+            half8 fa[2][FA], fb[2][FB];
+            auto operands = [&](int k, int q) {
+#pragma unroll
+                for (int x = 0; x < FA; ++x)
+                    fa[q][x] = rows8(l, width, 16 * (FA * wr + x) + l15, 4 * k + g4);
+#pragma unroll
+                for (int y = 0; y < FB; ++y)
+                    fb[q][y] = rows8(l, width, 16 * (FB * wc + y) + l15, 4 * k + g4);
+            };
+            auto multiply = [&](int q) {
+#pragma unroll
+                for (int x = 0; x < FA; ++x)
+#pragma unroll
+                    for (int y = 0; y < FB; ++y)
+                        acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                            fb[q][y], fa[q][x], acc[x][y], 0, 0, 0);
+            };
+            if constexpr (W == 8) {
+                // The next operands are asked for before these are used (k32 is
+                // even); 16 waves have no registers for it, but each other.
+                operands(0, 0);
+                for (int k = 0; k < k32; k += 2) {
+                    operands(k + 1, 1);
+                    multiply(0);
+                    operands(k + 2 < k32 ? k + 2 : 0, 0);
+                    multiply(1);
+                }
+            } else {
+                for (int k = 0; k < k32; ++k) {
+                    operands(k, 0);
+                    multiply(0);
+                }
+            }
+        };
+        auto put_square = [&](const float4v (&v)[FA][FB]) {
+#pragma unroll
+            for (int x = 0; x < FA; ++x)
+#pragma unroll
+                for (int y = 0; y < FB; ++y) {
+                    const int i = 16 * (FA * wr + x) + l15, j = 16 * (FB * wc + y) + 4 * g4;
+                    put(la, kA, i, j, v[x][y]);
+                    if (kMirror && wc < wr)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            la[(j + e) * kA + (((i >> 3) ^ turn_of(j + e)) << 3) + (i & 7)] =
+                                (_Float16)v[x][y][e];
+                }
+        };
+        __syncthreads();  // the norm's sums, or B and the old X, have been read
+#pragma unroll
+        for (int x = 0; x < R; ++x)
+#pragma unroll
+            for (int y = 0; y < FN; ++y) put(lx, kX, 16 * x + l15, wj + 16 * y + 4 * g4, xv[x][y]);
+        __syncthreads();
+        float4v ga[FA][FB] = {}, gb[FA][FB] = {};
+        if (mine) {
+            square(lx, kX, c32, ga);
+            put_square(ga);
+        }
+        __syncthreads();
+        if (mine) {
+            square(la, kA, R / 2, gb);
+#pragma unroll
+            for (int x = 0; x < FA; ++x)
+#pragma unroll
+                for (int y = 0; y < FB; ++y)
+                    gb[x][y] = ga[x][y] * (st.b / kAScale) +
+                               gb[x][y] * (st.c / (kAScale * kAScale));
+        }
+        __syncthreads();
+        if (mine) put_square(gb);
+        __syncthreads();
+        // X <- a X + B X: the accumulators start at a X.
+#pragma unroll
+        for (int x = 0; x < R; ++x)
+#pragma unroll
+            for (int y = 0; y < FN; ++y) xv[x][y] *= st.a;
+#pragma unroll
+        for (int kk = 0; kk < R / 2; ++kk) {
+            half8 fa[R], fb[FN];
+#pragma unroll
+            for (int y = 0; y < FN; ++y) {
+                const int j = wj + 16 * y + 4 * (ln & 3), i = kk * 32 + g4 * 8 + (l15 >> 2);
+                half4 h[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    h[q] = read_turned(lx + (i + 4 * q) * kX +
+                                       (((j >> 3) ^ turn_of(i + 4 * q)) << 3) + (j & 7));
+                fb[y] = __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7);
+            }
+#pragma unroll
+            for (int x = 0; x < R; ++x) fa[x] = rows8(la, kA, 16 * x + l15, 4 * kk + g4);
+#pragma unroll
+            for (int x = 0; x < R; ++x)
+#pragma unroll
+                for (int y = 0; y < FN; ++y)
+                    xv[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[y], fa[x], xv[x][y], 0, 0,
+                                                                      0);
+        }
+    }
+    auto write_all = [&](auto mode, auto four) {
+        constexpr int MODE = decltype(mode)::value;
+        typedef typename OutType<MODE>::type O;
+        O* const out = (O*)st.out + base;
+#pragma unroll
+        for (int x = 0; x < R; ++x) {
+#pragma unroll
+            for (int y = 0; y < FN; ++y) {
+                bool in;
+                xv[x][y] *= 1.f / kXScale;
+                if constexpr (decltype(four)::value) {
+                    const uint32_t o = index(x, y, 0, &in);
+                    const float q[4] = {xv[x][y][0], xv[x][y][1], xv[x][y][2], xv[x][y][3]};
+                    if (in) write_out<MODE, 4>(out + o, q, st);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t o = index(x, y, e, &in);
+                        const float q[1] = {xv[x][y][e]};
+                        if (in) write_out<MODE, 1>(out + o, q, st);
+                    }
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    auto write = [&](auto mode) {
+        if (by_four)
+            write_all(mode, std::true_type{});
+        else
+            write_all(mode, std::false_type{});
+    };
+    if (u.mode == kOut)
+        write(std::integral_constant<int, kOut>{});
+    else if (u.mode == kParam32)
+        write(std::integral_constant<int, kParam32>{});
+    else
+        write(std::integral_constant<int, kParam16>{});
+}
+
 // ------------------------------------------------------------------ host ---
 
 static NsShape ns_shape(int64_t batch, int64_t m, int64_t n) {
@@ -501,9 +806,16 @@ static NsShape ns_shape(int64_t batch, int64_t m, int64_t n) {
     return s;
 }
 
+// The launch for small matrices, where there is one: 128 rows (the smaller
+// side) by 512, 64 by 1024 or less.
+static bool ns_is_small(const NsShape& sh) {
+    return sh.r <= 128 && (int64_t)(sh.r <= 64 ? 64 : 128) * sh.c <= 65536;
+}
+
 // Lays the buffers out from `base` (NULL to count only); returns the bytes.
 static size_t ns_layout(const NsShape& s, char* base, NsBuffers* w) {
     size_t at = 0;
+    if (ns_is_small(s)) return 256;  // unused: every call takes a workspace
     auto take = [&](size_t bytes) {
         char* p = base ? base + at : nullptr;
         at += align_up(bytes, 256);
@@ -620,6 +932,39 @@ static int ns_product(const NsBuffers& w, const NsShape& sh, const NsStep& st, i
     return ns_launch<MODE, TileL>(w, sh, st, from, nb, s);
 }
 
+template <int R, int FN, int W>
+static int ns_small_launch(const SmallRun& u, const NsShape& sh, const NsStep& st, hipStream_t s) {
+    constexpr int bytes = 16 * R * (16 * W * FN + 128) * 2;
+    if constexpr (bytes > 64 * 1024) {
+        SPOPT_HIP(hipFuncSetAttribute((const void*)k_ns_small<R, FN, W>,
+                                      hipFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    }
+    const int64_t chunk = 1 << 22;  // blocks of a grid
+    for (int64_t z = 0; z < sh.batch; z += chunk) {
+        const int64_t nb = sh.batch - z < chunk ? sh.batch - z : chunk, at = z * sh.m * sh.n;
+        SmallRun v = u;
+        NsStep sz = st;
+        v.g = (const char*)u.g + at * (u.gbf16 ? 2 : 4);
+        if (u.buf) v.buf += at;
+        sz.out = (char*)st.out + at * (u.mode == kParam32 ? 4 : 2);
+        k_ns_small<R, FN, W><<<(unsigned)nb, 64 * W, bytes, s>>>(v, sh, sz);
+    }
+    SPOPT_LAUNCHED();
+    return SPOPT_OK;
+}
+
+static int ns_small(const SmallRun& u, const NsShape& sh, const NsStep& st, hipStream_t s) {
+    const int64_t fn = ceil_div(sh.c, 128);
+    if (sh.r <= 64)
+        return fn <= 1   ? ns_small_launch<4, 1, 8>(u, sh, st, s)
+               : fn <= 2 ? ns_small_launch<4, 1, 16>(u, sh, st, s)
+               : fn <= 4 ? ns_small_launch<4, 2, 16>(u, sh, st, s)
+                         : ns_small_launch<4, 4, 16>(u, sh, st, s);
+    return fn <= 1   ? ns_small_launch<8, 1, 8>(u, sh, st, s)
+           : fn <= 2 ? ns_small_launch<8, 1, 16>(u, sh, st, s)
+                     : ns_small_launch<8, 2, 16>(u, sh, st, s);
+}
+
 template <class G>
 static int ns_run(const NsShape& sh, Source<G> u, float* buf, const spopt_ns_config& c,
                   NsBuffers w, int last, NsStep st, hipStream_t s) {
@@ -629,6 +974,10 @@ static int ns_run(const NsShape& sh, Source<G> u, float* buf, const spopt_ns_con
     st.a = (float)c.coef[0];
     st.b = (float)c.coef[1];
     st.c = (float)c.coef[2];
+    if (ns_is_small(sh)) {
+        const SmallRun r = {u.kind, sizeof(G) == 2, last, u.g, buf, u.mu, c.eps, c.steps};
+        return ns_small(r, sh, st, s);
+    }
     const int tr = sh.rp / kTile, tc = sh.cp / kTile;
     // The batch in the grids' last axis: at most so many matrices at a time.
     const int64_t chunk = 32768;

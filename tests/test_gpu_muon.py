@@ -200,6 +200,24 @@ def test_more_matrices_than_a_grid_axis_and_32_bit_offsets():
         assert (R.d(out[at]) - ref).norm() <= bound + R.HALF[BF16] * ref.norm()
 
 
+def test_more_large_matrices_than_one_grid_takes():
+    """Matrices beyond the one-launch kernel's sizes, with 32-bit offsets passed in the workspace."""
+    m, n, batch = 130, 260, 40000
+    g = torch.empty(batch, m, n, dtype=BF16, device="cuda").normal_()
+    out = L.newton_schulz(g)
+    for at in (0, 32767, 32768, 34953, batch - 1):
+        ref, bound = R.ns_error_bound(g[at])
+        assert (R.d(out[at]) - ref).norm() <= bound + R.HALF[BF16] * ref.norm()
+
+
+@pytest.mark.parametrize("shape", [(64, 1024), (1023, 63), (128, 512), (511, 127), (2, 64, 1000),
+                                   (64, 1025), (128, 513), (120, 130), (3, 520, 128), (33, 2100)],
+                         ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_around_the_one_launch_sizes(shape, dtype):
+    check_ns(matrix(*shape).to(dtype).cuda())
+
+
 def test_validate_refuses_and_writes_nothing():
     p, g, buf = (matrix(70, 30, seed=k).cuda() for k in range(3))
     L.muon_step(p, g, buf, lr=0.1, validate=True)
