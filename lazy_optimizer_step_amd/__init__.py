@@ -39,7 +39,9 @@ __all__ = ["coo_from_lookups", "csr_from_coo", "csr_from_lookups", "csr_to_coo",
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # The raw handle of torch.cuda.current_stream(), without the object
+        # around it (0.1 against 2.8 us a call).
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)

@@ -6,6 +6,8 @@
 
 namespace spopt {
 
+inline size_t dtype_bytes(int32_t dtype) { return dtype == SPOPT_DTYPE_F32 ? 4 : 2; }
+
 // V values at p, which need only be aligned to one of them: gfx950 takes
 // 16-byte global accesses at any address, and rows of odd widths or strides
 // start anywhere.

@@ -329,6 +329,11 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_ln_bwd(
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const Chunk<V> c(k * G + gl, cols);
+            if (c.skip == 0) {
+                store_v<float, V>(p + c.at, dw[k]);
+                store_v<float, V>(p + cols + c.at, db[k]);
+                continue;
+            }
 #pragma unroll
             for (int e = 0; e < V; ++e)
                 if (e >= c.skip) {
@@ -379,8 +384,16 @@ __global__ __launch_bounds__(1024) void k_ln_join(const float* part, int64_t sli
     W* out = blockIdx.y ? db : dw;
     if (out == nullptr) return;
     double s = 0.;
-    if (c < cols)
-        for (int64_t i = k; i < slices; i += 64) s += (double)part[(i * 2 + blockIdx.y) * cols + c];
+    if (c < cols) {
+        const float* p = part + blockIdx.y * cols + c;
+        int64_t i = k;
+        for (; i + 192 < slices; i += 256) {  // four loads at once
+            const float v0 = p[i * 2 * cols], v1 = p[(i + 64) * 2 * cols],
+                        v2 = p[(i + 128) * 2 * cols], v3 = p[(i + 192) * 2 * cols];
+            s += ((double)v0 + (double)v1) + ((double)v2 + (double)v3);
+        }
+        for (; i < slices; i += 64) s += (double)p[i * 2 * cols];
+    }
     l[k][q] = s;
     __syncthreads();
     for (int n = 32; n; n >>= 1) {
@@ -415,13 +428,21 @@ static RowPlan ln_plan(int64_t cols, int v, bool backward) {
     return {0, 0, false};
 }
 
-// Row slices of the column sums, one block each: enough to fill the card with
-// rows for every group to loop over, and few enough that the slices' sums stay
-// a small part of the traffic.
-static int64_t ln_slices(int64_t rows, int64_t cols) {
-    const int64_t most = cols <= 1024 ? 1024 : 512;
-    const int64_t s = ceil_div(rows, cols <= 1024 ? 16 : 4);
-    return s < 1 ? 1 : s > most ? most : s;
+// Row slices of the column sums, one block each.  Of narrow rows a block takes
+// several at a time: slices of 16 rows and more, 1024 at most.  Of wide ones a
+// slice's sums are as long as a row, 8 bytes a column against 6 or 12 that a
+// row reads and writes: 256 slices fill the card, more only while their sums
+// stay below an eighth of the rows' traffic (2048 x 16384 bfloat16, 512 slices:
+// half of it), 512 at most.
+static int64_t ln_slices(int64_t rows, int64_t cols, int64_t bytes) {
+    if (cols <= 1024) {
+        const int64_t s = ceil_div(rows, 16);
+        return s < 1 ? 1 : s > 1024 ? 1024 : s;
+    }
+    int64_t s = rows * 3 * bytes / 64;
+    if (s < 256) s = 256;
+    if (s > 512) s = 512;
+    return s > rows ? (rows < 1 ? 1 : rows) : s;
 }
 
 static int ln_check(const char* what, int64_t rows, int64_t cols, int32_t dtype, int32_t wdtype) {
@@ -517,7 +538,7 @@ extern "C" int layer_norm_backward_workspace_size(int64_t rows, int64_t cols, si
         cols > INT64_MAX / 8192)
         return fail(SPOPT_EINVAL, "layer_norm_backward_workspace_size: bad size %lld x %lld",
                     (long long)rows, (long long)cols);
-    *bytes = (size_t)ln_slices(rows, cols) * 2 * (size_t)cols * sizeof(float);
+    *bytes = (size_t)ln_slices(rows, cols, 4) * 2 * (size_t)cols * sizeof(float);
     return SPOPT_OK;
 }
 
@@ -549,7 +570,7 @@ extern "C" int layer_norm_backward(const void* dy, int64_t dy_stride, const void
         });
         if (rc) return rc;
     }
-    int64_t slices = rows == 0 ? 0 : ln_slices(rows, cols);
+    int64_t slices = rows == 0 ? 0 : ln_slices(rows, cols, (int64_t)dtype_bytes(dtype));
     ln_types(dtype, wdtype, [&](auto t, auto wt) {
         using T = decltype(t);
         using W = decltype(wt);

@@ -277,7 +277,7 @@ __global__ __launch_bounds__(T::kThreads) void k_ns_gemm(NsBuffers w, NsShape sh
     constexpr int BM = T::BM, BN = T::BN, WM = BM / T::WGM, WN = BN / T::WGN;
     constexpr int FM = WM / 16, FN = WN / 16, kWaves = T::WGM * T::WGN;
     constexpr int kRow = MODE >= kNext || FN % 2 ? 4 : 8;        // columns of a row's store
-    constexpr int kCol = FM % 8 == 0 ? 8 : FM % 4 == 0 ? 4 : 2;  // rows of a column's store
+    constexpr int kCol = FM % 8 == 0 ? 8 : FM % 4 == 0 ? 4 : FM % 2 ? 1 : 2;  // rows of a column's store
     extern __shared__ __align__(16) char lds_raw[];
     _Float16* const lds = (_Float16*)lds_raw;
     const int64_t t = xcd_order(blockIdx.x, gridDim.x);
@@ -882,6 +882,7 @@ static int ns_check_config(const char* what, const spopt_ns_config& c) {
 
 typedef Tiling<64, 64, 2, 2, 4> TileS4;
 typedef Tiling<64, 64, 2, 2, 2> TileS;
+typedef Tiling<96, 96, 2, 2, 4> TileN;
 typedef Tiling<128, 128, 2, 4, 4> TileM4;
 typedef Tiling<128, 128, 2, 4, 2> TileM;
 typedef Tiling<192, 192, 2, 4, 3> TileT;
@@ -909,26 +910,33 @@ static int ns_launch(const NsBuffers& w, const NsShape& sh, const NsStep& st, in
 }
 
 // The tiling whose rounds over the 256 CUs take least.  An inner step of 64
-// takes a tile of 64, 128, 192 and 256 about 0.2, 0.5, 1.1 and 1.8 us of its CU
-// (measured on products that fill the card).  Large tiles read less for each
-// product, small ones leave fewer CUs idle, and where each CU has one block,
-// four stages in LDS beat two: 1024 x 1024 by 64 tiles 150 against 184 us for
-// the whole iteration, 2048 x 2048 by 128 tiles 382 against 417 us; with
-// several blocks a CU they lose (4096 x 4096 by 128: 2083 against 1872 us).
+// takes a tile of 64, 96, 128, 192 and 256 about 0.2, 0.45, 0.5, 1.1 and 1.8 us
+// of its CU (measured on products that fill the card).  Large tiles read less
+// for each product, small ones leave fewer CUs idle: for the lower triangles of
+// 2048 and 4096 rows, 96 and 192 are 253 tiles where 128 is 136 or 528 and 256
+// is 136 (2048 x 8192: 820 us for the iteration by 96, 864 by 128; 4096 x 4096:
+// 1463 by 192, 1674 by 256).  Where each CU has one block, four stages in LDS
+// beat two: 1024 x 1024 by 64 tiles 150 against 184 us, 2048 x 2048 by 128
+// tiles 382 against 417 us; with several blocks a CU they lose (4096 x 4096 by
+// 128: 2083 against 1872 us).
 template <int MODE>
 static int ns_product(const NsBuffers& w, const NsShape& sh, const NsStep& st, int from,
                       unsigned nb, hipStream_t s) {
     auto rounds = [&](int64_t tiles) { return (double)ceil_div(tiles * nb, 256); };
     const double ts = rounds(ns_tiles<MODE, TileS>(sh)), tm = rounds(ns_tiles<MODE, TileM>(sh));
-    const double tt = rounds(ns_tiles<MODE, TileT>(sh)), tl = rounds(ns_tiles<MODE, TileL>(sh));
-    const double best = fmin(fmin(ts * 0.2, tm * 0.5), fmin(tt * 1.1, tl * 1.8));
-    if (ts * 0.2 <= best)
+    const double cs = 0.2 * ts, cm = 0.5 * tm, ct = 1.1 * rounds(ns_tiles<MODE, TileT>(sh)),
+                 cl = 1.8 * rounds(ns_tiles<MODE, TileL>(sh));
+    const double best = fmin(fmin(cs, cm), fmin(ct, cl));
+    if constexpr (MODE <= kPoly)
+        if (0.45 * rounds(ns_tiles<MODE, TileN>(sh)) < best)
+            return ns_launch<MODE, TileN>(w, sh, st, from, nb, s);
+    if (cs <= best)
         return ts <= 2 ? ns_launch<MODE, TileS4>(w, sh, st, from, nb, s)
                        : ns_launch<MODE, TileS>(w, sh, st, from, nb, s);
-    if (tm * 0.5 <= best)
+    if (cm <= best)
         return tm <= 1 ? ns_launch<MODE, TileM4>(w, sh, st, from, nb, s)
                        : ns_launch<MODE, TileM>(w, sh, st, from, nb, s);
-    if (tt * 1.1 <= best) return ns_launch<MODE, TileT>(w, sh, st, from, nb, s);
+    if (ct <= best) return ns_launch<MODE, TileT>(w, sh, st, from, nb, s);
     return ns_launch<MODE, TileL>(w, sh, st, from, nb, s);
 }
 

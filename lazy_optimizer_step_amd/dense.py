@@ -23,25 +23,29 @@ _DTYPES = {torch.float32: _lib.DTYPE_F32, torch.bfloat16: _lib.DTYPE_BF16,
 
 
 def _rows(t, name, like=None):
-    """(2-D view, rows, cols, row stride) of a device tensor whose last axis holds adjacent
-    values and whose leading axes collapse into evenly spaced rows; never a copy."""
+    """(rows, cols, row stride) of a device tensor whose last axis holds adjacent values and
+    whose leading axes collapse into evenly spaced rows; never a copy."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in _DTYPES:
-        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a ROCm device")
-    if t.dim() < 1 or t.shape[-1] < 1:
-        raise ValueError(f"{name} has no columns: shape {tuple(t.shape)}")
+    shape = t.shape
     if like is not None:
-        if t.shape != like.shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, x {tuple(like.shape)}")
+        if shape != like.shape:
+            raise ValueError(f"{name} has shape {tuple(shape)}, x {tuple(like.shape)}")
         if t.dtype != like.dtype:
             raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
         if t.device != like.device:
             raise ValueError(f"{name} is on {t.device}, x on {like.device}")
-    cols = t.shape[-1]
+    else:
+        if t.dtype not in _DTYPES:
+            raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be on a ROCm device")
+        if len(shape) < 1 or shape[-1] < 1:
+            raise ValueError(f"{name} has no columns: shape {tuple(shape)}")
+    cols = shape[-1]
     rows = t.numel() // cols
+    if t.is_contiguous():
+        return rows, cols, cols
     if cols > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}: the values of a row must be adjacent")
     if rows <= 1:
@@ -49,11 +53,17 @@ def _rows(t, name, like=None):
     try:
         stride = t.view(rows, cols).stride(0)
     except RuntimeError:
-        raise ValueError(f"{name}: the rows of shape {tuple(t.shape)} with strides "
+        raise ValueError(f"{name}: the rows of shape {tuple(shape)} with strides "
                          f"{t.stride()} are not evenly spaced") from None
     if stride < cols:
         raise ValueError(f"{name}: rows overlap (stride {stride} for {cols} columns)")
     return rows, cols, stride
+
+
+def _like(x):
+    """A new contiguous tensor of x's shape and type."""
+    return torch.empty_like(x) if x.is_contiguous() else \
+        torch.empty(x.shape, dtype=x.dtype, device=x.device)
 
 
 def _vector(t, name, x, cols, dtypes):
@@ -76,22 +86,27 @@ def layer_norm_forward(x: torch.Tensor, weight=None, bias=None, *, eps: float = 
     bfloat16 or float16, its rows evenly spaced; weight, bias: x's type or float32 (one type
     for both), or None.  out may be x."""
     rows, cols, xs = _rows(x, "x")
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        _vector(t, name, x, cols, (x.dtype, torch.float32))
+    allowed = (x.dtype, torch.float32)
+    _vector(weight, "weight", x, cols, allowed)
+    _vector(bias, "bias", x, cols, allowed)
     if weight is not None and bias is not None and weight.dtype != bias.dtype:
         raise TypeError(f"weight is {weight.dtype}, bias {bias.dtype}: one type for both")
     w = weight if weight is not None else bias
     wdtype = _DTYPES[w.dtype] if w is not None else _lib.DTYPE_F32
+    ys = cols
+    if out is not None:
+        _, _, ys = _rows(out, "out", x)
+    if mean is not None:
+        _need(mean, torch.float32, "mean", rows)
+    if rstd is not None:
+        _need(rstd, torch.float32, "rstd", rows)
     with _alloc_on(stream):
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            out = _like(x)
         if mean is None:
-            mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+            mean = x.new_empty(x.shape[:-1], dtype=torch.float32)
         if rstd is None:
-            rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    _, _, ys = _rows(out, "out", x)
-    _need(mean, torch.float32, "mean", rows)
-    _need(rstd, torch.float32, "rstd", rows)
+            rstd = torch.empty_like(mean)
     check(_lib.lib().layer_norm_forward(_ptr(x), xs, rows, cols, _DTYPES[x.dtype], _ptr(weight),
                                         _ptr(bias), wdtype, eps, _ptr(out), ys, _ptr(mean),
                                         _ptr(rstd), _stream(stream), _flags(validate)))
@@ -114,28 +129,29 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
     rows, cols, xs = _rows(x, "x")
     _, _, ds = _rows(dy, "dy", x)
     _vector(weight, "weight", x, cols, (x.dtype, torch.float32))
-    given = next((t for t in (weight, dweight, dbias) if t is not None), None)
+    given = weight if weight is not None else dweight if dweight is not None else dbias
     wt = given.dtype if given is not None else torch.float32
+    if wt not in (x.dtype, torch.float32):
+        raise TypeError(f"the weight's gradients must be {x.dtype} or float32, got {wt}")
+    _vector(dweight, "dweight", x, cols, (wt,))
+    _vector(dbias, "dbias", x, cols, (wt,))
     _need(mean, torch.float32, "mean", rows)
     _need(rstd, torch.float32, "rstd", rows)
     os_ = cols
+    if out is not None:
+        _, _, os_ = _rows(out, "out", x)
+    if workspace is not None:
+        _need(workspace, torch.uint8, "workspace")
     with _alloc_on(stream):
-        if want_dx:
-            if out is None:
-                out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            _, _, os_ = _rows(out, "out", x)
+        if want_dx and out is None:
+            out = _like(x)
         if want_dweight and dweight is None:
-            dweight = torch.empty(cols, dtype=wt, device=x.device)
+            dweight = x.new_empty(cols, dtype=wt)
         if want_dbias and dbias is None:
-            dbias = torch.empty(cols, dtype=wt, device=x.device)
-        for t, name in ((dweight, "dweight"), (dbias, "dbias")):
-            _vector(t, name, x, cols, (wt,))
+            dbias = torch.empty_like(dweight) if dweight is not None else x.new_empty(cols, dtype=wt)
         if workspace is None:
-            workspace = torch.empty(max(layer_norm_backward_workspace_size(rows, cols), 1),
-                                    dtype=torch.uint8, device=x.device)
-    _need(workspace, torch.uint8, "workspace")
-    if wt not in (x.dtype, torch.float32):
-        raise TypeError(f"the weight's gradients must be {x.dtype} or float32, got {wt}")
+            workspace = x.new_empty(layer_norm_backward_workspace_size(rows, cols),
+                                    dtype=torch.uint8)
     dx = out if want_dx else None
     dweight, dbias = dweight if want_dweight else None, dbias if want_dbias else None
     check(_lib.lib().layer_norm_backward(_ptr(dy), ds, _ptr(x), xs, rows, cols, _DTYPES[x.dtype],
@@ -225,8 +241,8 @@ def newton_schulz_workspace_size(batch: int, m: int, n: int) -> int:
 
 def _ns_workspace(workspace, batch, m, n, device):
     if workspace is None:
-        workspace = torch.empty(max(newton_schulz_workspace_size(batch, m, n), 1),
-                                dtype=torch.uint8, device=device)
+        return torch.empty(newton_schulz_workspace_size(batch, m, n), dtype=torch.uint8,
+                           device=device)
     return _need(workspace, torch.uint8, "workspace")
 
 
@@ -237,11 +253,12 @@ def newton_schulz(g: torch.Tensor, *, steps: int = 5, coefficients=NS_COEFFICIEN
     orthogonal factor.  g: float32 or bfloat16, contiguous; the result is bfloat16 (its
     products are taken in float16, float32 sums)."""
     batch, m, n = _matrices(g, "g")
+    if out is not None:
+        _need(out, torch.bfloat16, "out", g.numel())
     with _alloc_on(stream):
         if out is None:
-            out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
+            out = torch.empty_like(g, dtype=torch.bfloat16)
         workspace = _ns_workspace(workspace, batch, m, n, g.device)
-    _need(out, torch.bfloat16, "out", g.numel())
     cfg = _ns_config(coefficients, eps, steps)
     check(_lib.lib().newton_schulz(_ptr(g), _DTYPES[g.dtype], batch, m, n, C.byref(cfg), _ptr(out),
                                    _ptr(workspace), workspace.numel(), _stream(stream),
