@@ -497,60 +497,74 @@ __global__ __launch_bounds__(T::kThreads) void k_ns_gemm(NsBuffers w, NsShape sh
         finish(std::false_type{});
 }
 
-// ------------------------------------------------------- small matrices ---
+// -------------------------------------- matrices of up to 128 rows or columns ---
 
-// A matrix whose X fits one CU, from the gradient to the result in one launch:
-// one block of 8 or 16 waves each.  X lives in registers in float32 (wave v holds all
-// rows of 16 FN columns) and in LDS in float16, A and then B in LDS; the norm
-// is summed, and the momentum moved, as the values are first read.  Padded to
-// 16 R rows (R = 4 or 8) and 16 W FN columns of W waves; R FN <= 16, as the
-// rest of the step needs registers too.
+// Up to 16 R rows (R = 4 or 8) and 16 W FN adjacent columns of X, held by a
+// block of W waves: in registers in float32 (wave v has all rows of 16 FN
+// columns) and in LDS in float16, with an R x R square (A, then B) beside it.
 //
-// LDS rows (X's of 16 W FN values, A's of 128) are laid out with chunk c of 8
-// values of row i at c ^ turn_of(i): the 16 rows of an operand, and the 8 rows
-// that half a wave's transposing read takes, meet different banks of the 64.
-struct SmallRun {
-    int kind;          // as Source
-    int gbf16, mode;   // the gradient's type; kOut, kParam32 or kParam16
-    const void* g;
-    float* buf;
-    float mu;
-    double eps;
-    int steps;
-};
-
+// LDS rows (X's of 16 W FN values, the square's of 128) are laid out with chunk
+// c of 8 values of row i at c ^ turn_of(i): the 8 rows of two chunks that LDS
+// gives in a cycle, and the 8 rows of a transposing read, lie in different
+// parts of its 256 bytes.
 __device__ __forceinline__ int turn_of(int row) {
     return (((row & 7) ^ ((row >> 1) & 4)) << 1) | ((row >> 3) & 1);  // of row % 16
 }
 
 template <int R, int FN, int W>
-__global__ __launch_bounds__(64 * W) void k_ns_small(SmallRun u, NsShape sh, NsStep st) {
-    constexpr int kX = 16 * W * FN, kA = 128;
-    extern __shared__ __align__(16) char lds_raw[];
-    _Float16* const lx = (_Float16*)lds_raw;
-    _Float16* const la = lx + 16 * R * kX;
-    const int lane = lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int l15 = lane & 15, g4 = lane >> 4;
-    const int wj = wv * 16 * FN;
-    const int64_t base = (int64_t)blockIdx.x * sh.m * sh.n;
-    float* const buf = u.buf + (u.kind ? base : 0);
-    // Value e of part (x, y): row 16 x + l15, column wj + 16 y + 4 g4 + e, and
-    // where it lies in the input (fewer than 2^16 values).
-    float4v xv[R][FN];
-    const uint32_t di = sh.flip ? 1 : sh.c, dj = sh.flip ? sh.r : 1;
-    auto index = [&](int x, int y, int e, bool* in) {
+struct Panel {
+    static constexpr int kX = 16 * W * FN, kA = 128;
+    static constexpr int FA = R / 4, FB = 4 * R / W;  // a wave's part of the square
+    static constexpr int kBytes = 16 * R * (kX + kA) * 2;
+    // Of 16 waves' square parts the 6 above the diagonal are mirrored ones.
+    static constexpr bool kMirror = W == 16;
+    _Float16 *lx, *la;
+    int lane, l15, g4, ft, wj, wr, wc;
+    uint32_t di, dj;      // strides of X's rows and columns in the input
+    int rows, cols;       // of the input's, from this panel's first column on
+    bool by_four;         // four adjacent columns lie together in the input
+
+    __device__ __forceinline__ Panel(char* lds, const NsShape& sh, int first_col)
+        : lx((_Float16*)lds), la((_Float16*)lds + 16 * R * kX) {
+        const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        wj = wv * 16 * FN;
+        wr = wv / (W / 4);
+        wc = wv % (W / 4);
+        set_lane(lane_id());
+        di = sh.flip ? 1 : sh.c;
+        dj = sh.flip ? sh.r : 1;
+        rows = sh.r;
+        cols = sh.c - first_col;
+        by_four = !sh.flip && sh.c % 4 == 0;
+    }
+    __device__ __forceinline__ void set_lane(int l) {
+        lane = l;
+        l15 = l & 15;
+        g4 = l >> 4;
+        ft = turn_of(l15);
+    }
+    // Has the places in LDS worked out anew from here on: kept over a loop they
+    // would not fit the registers.
+    __device__ __forceinline__ void forget_places() {
+        int l = lane;
+        asm volatile("" : "+v"(l));
+        set_lane(l);
+    }
+    __device__ __forceinline__ bool in_square() const { return !kMirror || wc <= wr; }
+
+    // Value e of part (x, y): row 16 x + l15, column wj + 16 y + 4 g4 + e; where
+    // it lies in the input (within 2^32 values of the panel's first).
+    __device__ __forceinline__ uint32_t index(int x, int y, int e, bool* in) const {
         const int i = 16 * x + l15, j = wj + 16 * y + 4 * g4 + e;
-        *in = i < sh.r && j < sh.c;
+        *in = i < rows && j < cols;
         return *in ? (uint32_t)i * di + (uint32_t)j * dj : 0u;
-    };
-    // Four adjacent columns at once where the rows allow it.
-    const bool by_four = !sh.flip && sh.c % 4 == 0;
-    auto read_row = [&](const auto* from, int x, auto four, float4v (&v)[FN]) {
-        typedef std::remove_cv_t<std::remove_reference_t<decltype(*from)>> E;
+    }
+    template <bool FOUR, class E>
+    __device__ __forceinline__ void read_row(const E* from, int x, float4v (&v)[FN]) const {
         bool in;
 #pragma unroll
         for (int y = 0; y < FN; ++y) {
-            if constexpr (decltype(four)::value) {
+            if constexpr (FOUR) {
                 float q[4];
                 load_v<E, 4>(from + index(x, y, 0, &in), q);
 #pragma unroll
@@ -563,25 +577,30 @@ __global__ __launch_bounds__(64 * W) void k_ns_small(SmallRun u, NsShape sh, NsS
                 }
             }
         }
-    };
-    auto read_all = [&](const auto* from, auto four) {
+    }
+    // U of the panel into `xv`: g, buf or g + mu * buf (kind 0, 1, 2), where
+    // `move` is set with buf <- mu * buf + g before.
+    template <bool FOUR, class E>
+    __device__ __forceinline__ void read_u(const E* g, float* buf, float mu, int kind, bool move,
+                                           float4v (&xv)[R][FN]) const {
         // One row of parts at a time: all in flight would need too many registers.
 #pragma unroll
         for (int x = 0; x < R; ++x) {
-            read_row(from, x, four, xv[x]);
+            read_row<FOUR>(g, x, xv[x]);
             __builtin_amdgcn_sched_barrier(0);
         }
-        if (u.kind == 0) return;
+        if (kind == 0) return;
 #pragma unroll
         for (int x = 0; x < R; ++x) {
             float4v b[FN];
-            read_row(buf, x, four, b);
+            read_row<FOUR>(buf, x, b);
 #pragma unroll
             for (int y = 0; y < FN; ++y) {
-                b[y] = u.mu * b[y] + xv[x][y];
-                xv[x][y] = u.kind == 1 ? b[y] : xv[x][y] + u.mu * b[y];
+                if (move) b[y] = mu * b[y] + xv[x][y];
+                xv[x][y] = kind == 1 ? b[y] : xv[x][y] + mu * b[y];
+                if (!move) continue;
                 bool in;
-                if constexpr (decltype(four)::value) {
+                if constexpr (FOUR) {
                     const uint32_t o = index(x, y, 0, &in);
                     const float q[4] = {b[y][0], b[y][1], b[y][2], b[y][3]};
                     if (in) store_v<float, 4>(buf + o, q);
@@ -594,31 +613,28 @@ __global__ __launch_bounds__(64 * W) void k_ns_small(SmallRun u, NsShape sh, NsS
                 }
             }
         }
-    };
-    if (by_four) {
-        if (u.gbf16)
-            read_all((const __bf16*)u.g + base, std::true_type{});
-        else
-            read_all((const float*)u.g + base, std::true_type{});
-    } else {
-        if (u.gbf16)
-            read_all((const __bf16*)u.g + base, std::false_type{});
-        else
-            read_all((const float*)u.g + base, std::false_type{});
     }
-    {
-        double sq = 0.;
-#pragma unroll
-        for (int x = 0; x < R; ++x)
-#pragma unroll
-            for (int y = 0; y < FN; ++y)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sq += (double)xv[x][y][e] * (double)xv[x][y][e];
-        // The scale as a power of two and a factor in [0.5, 1): float32 alone
-        // would not hold every norm's reciprocal.
+    __device__ __forceinline__ void read_u(const void* g, bool bf16, int64_t base, float* buf,
+                                           float mu, int kind, bool move,
+                                           float4v (&xv)[R][FN]) const {
+        float* const b = kind ? buf + base : nullptr;
+        if (by_four) {
+            if (bf16)
+                read_u<true>((const __bf16*)g + base, b, mu, kind, move, xv);
+            else
+                read_u<true>((const float*)g + base, b, mu, kind, move, xv);
+        } else {
+            if (bf16)
+                read_u<false>((const __bf16*)g + base, b, mu, kind, move, xv);
+            else
+                read_u<false>((const float*)g + base, b, mu, kind, move, xv);
+        }
+    }
+    // xv * 2^6 / (sqrt(sq) + eps): the scale as a power of two and a factor in
+    // [0.5, 1), as float32 alone would not hold every norm's reciprocal.
+    __device__ __forceinline__ void normalise(double sq, double eps, float4v (&xv)[R][FN]) const {
         int ex;
-        const float f = (float)frexp(
-            (double)kXScale / (sqrt(block_sum_d(sq, (double*)la)) + u.eps), &ex);
+        const float f = (float)frexp((double)kXScale / (sqrt(sq) + eps), &ex);
 #pragma unroll
         for (int x = 0; x < R; ++x)
 #pragma unroll
@@ -626,92 +642,78 @@ __global__ __launch_bounds__(64 * W) void k_ns_small(SmallRun u, NsShape sh, NsS
 #pragma unroll
                 for (int e = 0; e < 4; ++e) xv[x][y][e] = ldexpf(xv[x][y][e], ex) * f;
     }
-    const int c32 = (sh.c + 63) / 64 * 2;  // inner steps of A: columns past them are zero
-    for (int k = 0; k < u.steps; ++k) {
-        // Said to change here, so that the places in LDS are worked out anew in
-        // each step: kept over the loop they would not fit the registers.
-        int ln = lane;
-        asm volatile("" : "+v"(ln));
-        const int l15 = ln & 15, g4 = ln >> 4, ft = turn_of(l15);
-        // 4 adjacent values of row `i` from column `j` on.
-        auto put = [&](_Float16* l, int width, int i, int j, float4v v) {
-            half4 h;
+    // 4 adjacent values of row i (i % 16 == l15) from column j on.
+    __device__ __forceinline__ void put(_Float16* l, int width, int i, int j, float4v v) const {
+        half4 h;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) h[e] = (_Float16)v[e];
-            *(half4*)(l + i * width + (((j >> 3) ^ ft) << 3) + (j & 7)) = h;
-        };
-        // Values 8 chunk .. + 7 of row `i` (i % 16 == l15).
-        auto rows8 = [&](const _Float16* l, int width, int i, int chunk) {
-            return *(const half8*)(l + i * width + ((chunk ^ ft) << 3));
-        };
-        // A wave's part of an R x R product: rows 16 FA wr .., columns 16 FB wc ..
-        // Of 16 waves' square parts the 6 above the diagonal are mirrored ones.
-        constexpr int FA = R / 4, FB = 4 * R / W;
-        constexpr bool kMirror = W == 16;
-        const int wr = wv / (W / 4), wc = wv % (W / 4);
-        const bool mine = !kMirror || wc <= wr;
-        auto square = [&](const _Float16* l, int width, int k32, float4v (&acc)[FA][FB]) {
-            half8 fa[2][FA], fb[2][FB];
-            auto operands = [&](int k, int q) {
-#pragma unroll
-                for (int x = 0; x < FA; ++x)
-                    fa[q][x] = rows8(l, width, 16 * (FA * wr + x) + l15, 4 * k + g4);
-#pragma unroll
-                for (int y = 0; y < FB; ++y)
-                    fb[q][y] = rows8(l, width, 16 * (FB * wc + y) + l15, 4 * k + g4);
-            };
-            auto multiply = [&](int q) {
-#pragma unroll
-                for (int x = 0; x < FA; ++x)
-#pragma unroll
-                    for (int y = 0; y < FB; ++y)
-                        acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                            fb[q][y], fa[q][x], acc[x][y], 0, 0, 0);
-            };
-            if constexpr (W == 8) {
-                // The next operands are asked for before these are used (k32 is
-                // even); 16 waves have no registers for it, but each other.
-                operands(0, 0);
-                for (int k = 0; k < k32; k += 2) {
-                    operands(k + 1, 1);
-                    multiply(0);
-                    operands(k + 2 < k32 ? k + 2 : 0, 0);
-                    multiply(1);
-                }
-            } else {
-                for (int k = 0; k < k32; ++k) {
-                    operands(k, 0);
-                    multiply(0);
-                }
-            }
-        };
-        auto put_square = [&](const float4v (&v)[FA][FB]) {
-#pragma unroll
-            for (int x = 0; x < FA; ++x)
-#pragma unroll
-                for (int y = 0; y < FB; ++y) {
-                    const int i = 16 * (FA * wr + x) + l15, j = 16 * (FB * wc + y) + 4 * g4;
-                    put(la, kA, i, j, v[x][y]);
-                    if (kMirror && wc < wr)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            la[(j + e) * kA + (((i >> 3) ^ turn_of(j + e)) << 3) + (i & 7)] =
-                                (_Float16)v[x][y][e];
-                }
-        };
-        __syncthreads();  // the norm's sums, or B and the old X, have been read
+        for (int e = 0; e < 4; ++e) h[e] = (_Float16)v[e];
+        *(half4*)(l + i * width + (((j >> 3) ^ ft) << 3) + (j & 7)) = h;
+    }
+    __device__ __forceinline__ void put_x(const float4v (&xv)[R][FN]) const {
 #pragma unroll
         for (int x = 0; x < R; ++x)
 #pragma unroll
             for (int y = 0; y < FN; ++y) put(lx, kX, 16 * x + l15, wj + 16 * y + 4 * g4, xv[x][y]);
-        __syncthreads();
-        float4v ga[FA][FB] = {}, gb[FA][FB] = {};
-        if (mine) {
-            square(lx, kX, c32, ga);
-            put_square(ga);
+    }
+    __device__ __forceinline__ void put_square(const float4v (&v)[FA][FB]) const {
+#pragma unroll
+        for (int x = 0; x < FA; ++x)
+#pragma unroll
+            for (int y = 0; y < FB; ++y) {
+                const int i = 16 * (FA * wr + x) + l15, j = 16 * (FB * wc + y) + 4 * g4;
+                put(la, kA, i, j, v[x][y]);
+                if (kMirror && wc < wr)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        la[(j + e) * kA + (((i >> 3) ^ turn_of(j + e)) << 3) + (i & 7)] =
+                            (_Float16)v[x][y][e];
+            }
+    }
+    // Values 8 chunk .. + 7 of row i (i % 16 == l15).
+    __device__ __forceinline__ half8 rows8(const _Float16* l, int width, int i, int chunk) const {
+        return *(const half8*)(l + i * width + ((chunk ^ ft) << 3));
+    }
+    // acc += the wave's part of P P^T, P the rows of `l`, over 32 k32 columns.
+    __device__ __forceinline__ void square(const _Float16* l, int width, int k32,
+                                           float4v (&acc)[FA][FB]) const {
+        half8 fa[2][FA], fb[2][FB];
+        auto operands = [&](int k, int q) {
+#pragma unroll
+            for (int x = 0; x < FA; ++x)
+                fa[q][x] = rows8(l, width, 16 * (FA * wr + x) + l15, 4 * k + g4);
+#pragma unroll
+            for (int y = 0; y < FB; ++y)
+                fb[q][y] = rows8(l, width, 16 * (FB * wc + y) + l15, 4 * k + g4);
+        };
+        auto multiply = [&](int q) {
+#pragma unroll
+            for (int x = 0; x < FA; ++x)
+#pragma unroll
+                for (int y = 0; y < FB; ++y)
+                    acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[q][y], fa[q][x],
+                                                                       acc[x][y], 0, 0, 0);
+        };
+        if constexpr (W == 8) {
+            // The next operands are asked for before these are used (k32 is
+            // even); 16 waves have no registers for it, but each other.
+            operands(0, 0);
+            for (int k = 0; k < k32; k += 2) {
+                operands(k + 1, 1);
+                multiply(0);
+                operands(k + 2 < k32 ? k + 2 : 0, 0);
+                multiply(1);
+            }
+        } else {
+            for (int k = 0; k < k32; ++k) {
+                operands(k, 0);
+                multiply(0);
+            }
         }
-        __syncthreads();
-        if (mine) {
+    }
+    // From A * 2^12 in `ga` and, as float16, in LDS: B into LDS.
+    __device__ __forceinline__ void polynomial(const float4v (&ga)[FA][FB], const NsStep& st) const {
+        float4v gb[FA][FB] = {};
+        if (in_square()) {
             square(la, kA, R / 2, gb);
 #pragma unroll
             for (int x = 0; x < FA; ++x)
@@ -721,19 +723,21 @@ __global__ __launch_bounds__(64 * W) void k_ns_small(SmallRun u, NsShape sh, NsS
                                gb[x][y] * (st.c / (kAScale * kAScale));
         }
         __syncthreads();
-        if (mine) put_square(gb);
+        if (in_square()) put_square(gb);
         __syncthreads();
-        // X <- a X + B X: the accumulators start at a X.
+    }
+    // X <- a X + B X: the accumulators start at a X.
+    __device__ __forceinline__ void next(float a, float4v (&xv)[R][FN]) const {
 #pragma unroll
         for (int x = 0; x < R; ++x)
 #pragma unroll
-            for (int y = 0; y < FN; ++y) xv[x][y] *= st.a;
+            for (int y = 0; y < FN; ++y) xv[x][y] *= a;
 #pragma unroll
         for (int kk = 0; kk < R / 2; ++kk) {
             half8 fa[R], fb[FN];
 #pragma unroll
             for (int y = 0; y < FN; ++y) {
-                const int j = wj + 16 * y + 4 * (ln & 3), i = kk * 32 + g4 * 8 + (l15 >> 2);
+                const int j = wj + 16 * y + 4 * (lane & 3), i = kk * 32 + g4 * 8 + (l15 >> 2);
                 half4 h[2];
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
@@ -751,8 +755,9 @@ __global__ __launch_bounds__(64 * W) void k_ns_small(SmallRun u, NsShape sh, NsS
                                                                       0);
         }
     }
-    auto write_all = [&](auto mode, auto four) {
-        constexpr int MODE = decltype(mode)::value;
+    template <int MODE, bool FOUR>
+    __device__ __forceinline__ void write_as(int64_t base, const NsStep& st,
+                                             float4v (&xv)[R][FN]) const {
         typedef typename OutType<MODE>::type O;
         O* const out = (O*)st.out + base;
 #pragma unroll
@@ -761,7 +766,7 @@ __global__ __launch_bounds__(64 * W) void k_ns_small(SmallRun u, NsShape sh, NsS
             for (int y = 0; y < FN; ++y) {
                 bool in;
                 xv[x][y] *= 1.f / kXScale;
-                if constexpr (decltype(four)::value) {
+                if constexpr (FOUR) {
                     const uint32_t o = index(x, y, 0, &in);
                     const float q[4] = {xv[x][y][0], xv[x][y][1], xv[x][y][2], xv[x][y][3]};
                     if (in) write_out<MODE, 4>(out + o, q, st);
@@ -776,19 +781,171 @@ __global__ __launch_bounds__(64 * W) void k_ns_small(SmallRun u, NsShape sh, NsS
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-    };
-    auto write = [&](auto mode) {
+    }
+    template <int MODE>
+    __device__ __forceinline__ void write_as(int64_t base, const NsStep& st,
+                                             float4v (&xv)[R][FN]) const {
         if (by_four)
-            write_all(mode, std::true_type{});
+            write_as<MODE, true>(base, st, xv);
         else
-            write_all(mode, std::false_type{});
-    };
-    if (u.mode == kOut)
-        write(std::integral_constant<int, kOut>{});
-    else if (u.mode == kParam32)
-        write(std::integral_constant<int, kParam32>{});
-    else
-        write(std::integral_constant<int, kParam16>{});
+            write_as<MODE, false>(base, st, xv);
+    }
+    __device__ __forceinline__ void write(int mode, int64_t base, const NsStep& st,
+                                          float4v (&xv)[R][FN]) const {
+        if (mode == kOut)
+            write_as<kOut>(base, st, xv);
+        else if (mode == kParam32)
+            write_as<kParam32>(base, st, xv);
+        else
+            write_as<kParam16>(base, st, xv);
+    }
+};
+
+struct PanelRun {
+    int kind;          // as Source
+    int gbf16, mode;   // the gradient's type; kOut, kParam32 or kParam16
+    const void* g;
+    float* buf;
+    float mu;
+    double eps;
+    int steps;
+    // Wide matrices only: panels of a matrix, slices of its norm, and buffers
+    int panels, parts;
+    const double* part;  // [batch][kNormParts]
+    float* x32;          // [batch][panels][16 R * 16 W FN], as the lanes hold them
+    float* gram;         // [batch][panels][256 R^2], likewise: a panel's share of A * 2^12
+    _Float16* a16;       // [batch][256 R^2], likewise: A * 2^12
+};
+
+// A matrix that one panel holds, from the gradient to the result in one launch,
+// one block each: the norm is summed, and the momentum moved, as the values are
+// first read.
+template <int R, int FN, int W>
+__global__ __launch_bounds__(64 * W) void k_ns_small(PanelRun u, NsShape sh, NsStep st) {
+    extern __shared__ __align__(16) char lds_raw[];
+    typedef Panel<R, FN, W> P;
+    P p(lds_raw, sh, 0);
+    const int64_t base = (int64_t)blockIdx.x * sh.m * sh.n;
+    float4v xv[R][FN];
+    p.read_u(u.g, u.gbf16, base, u.buf, u.mu, u.kind, true, xv);
+    double sq = 0.;
+#pragma unroll
+    for (int x = 0; x < R; ++x)
+#pragma unroll
+        for (int y = 0; y < FN; ++y)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sq += (double)xv[x][y][e] * (double)xv[x][y][e];
+    p.normalise(block_sum_d(sq, (double*)p.la), u.eps, xv);
+    const int c32 = (sh.c + 63) / 64 * 2;  // inner steps of A: columns past them are zero
+    for (int k = 0; k < u.steps; ++k) {
+        p.forget_places();
+        __syncthreads();  // the norm's sums, or B and the old X, have been read
+        p.put_x(xv);
+        __syncthreads();
+        float4v ga[P::FA][P::FB] = {};
+        if (p.in_square()) {
+            p.square(p.lx, P::kX, c32, ga);
+            p.put_square(ga);
+        }
+        __syncthreads();
+        p.polynomial(ga, st);
+        p.next(st.a, xv);
+    }
+    p.write(u.mode, base, st, xv);
+}
+
+// A wide matrix, panel by panel, one block each.  STEP false: U becomes X0.
+// STEP true: with A, which every block turns into B for itself (128^3 products:
+// about a microsecond), X becomes the next X, and after the last step the
+// result.  Either leaves the panel's share of the next A.
+template <int R, int FN, bool STEP>
+__global__ __launch_bounds__(512) void k_ns_panel(PanelRun u, NsShape sh, NsStep st, int last) {
+    extern __shared__ __align__(16) char lds_raw[];
+    typedef Panel<R, FN, 8> P;
+    const int z = blockIdx.x / u.panels, panel = blockIdx.x % u.panels;
+    P p(lds_raw, sh, panel * P::kX);
+    const int64_t base =
+        (int64_t)z * sh.m * sh.n + (int64_t)panel * P::kX * (sh.flip ? sh.r : 1);
+    float4v xv[R][FN];
+    float4v* const mine = (float4v*)u.x32 +
+                          ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 6)) * R * FN * 64 + p.lane;
+    if constexpr (STEP) {
+        const half4* a =
+            (const half4*)u.a16 + ((int64_t)z * 8 + (threadIdx.x >> 6)) * P::FA * P::FB * 64 + p.lane;
+        half4 h[P::FA][P::FB];
+#pragma unroll
+        for (int x = 0; x < P::FA; ++x)
+#pragma unroll
+            for (int y = 0; y < P::FB; ++y) h[x][y] = a[(x * P::FB + y) * 64];
+#pragma unroll
+        for (int x = 0; x < R; ++x)
+#pragma unroll
+            for (int y = 0; y < FN; ++y) xv[x][y] = mine[(x * FN + y) * 64];
+        float4v ga[P::FA][P::FB];
+#pragma unroll
+        for (int x = 0; x < P::FA; ++x)
+#pragma unroll
+            for (int y = 0; y < P::FB; ++y)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) ga[x][y][e] = (float)h[x][y][e];
+        p.put_square(ga);
+        p.put_x(xv);
+        __syncthreads();
+        p.polynomial(ga, st);
+        p.next(st.a, xv);
+        if (last) {
+            p.write(u.mode, base, st, xv);
+            return;
+        }
+        __syncthreads();  // the old X has been read
+    } else {
+        p.read_u(u.g, u.gbf16, base, u.buf, u.mu, u.kind, false, xv);
+        double sq = 0.;
+        for (int t = threadIdx.x; t < u.parts; t += 512) sq += u.part[(int64_t)z * kNormParts + t];
+        p.normalise(block_sum_d(sq, (double*)p.la), u.eps, xv);
+    }
+#pragma unroll
+    for (int x = 0; x < R; ++x)
+#pragma unroll
+        for (int y = 0; y < FN; ++y) mine[(x * FN + y) * 64] = xv[x][y];
+    p.put_x(xv);
+    __syncthreads();
+    float4v ga[P::FA][P::FB] = {};
+    p.square(p.lx, P::kX, P::kX / 32, ga);
+    float4v* const share = (float4v*)u.gram +
+                           ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 6)) * P::FA * P::FB * 64 +
+                           p.lane;
+#pragma unroll
+    for (int x = 0; x < P::FA; ++x)
+#pragma unroll
+        for (int y = 0; y < P::FB; ++y) share[(x * P::FB + y) * 64] = ga[x][y];
+}
+
+// A of each matrix from its panels' shares, in a fixed order: a block takes 64
+// groups of four values, each wave a quarter of the panels.
+__global__ __launch_bounds__(256) void k_ns_panel_sum(PanelRun u, int quads) {
+    __shared__ float4v l[4][64];
+    const int lane = lane_id(), k = threadIdx.x >> 6;
+    const int per = quads / 64;  // blocks of a matrix
+    const int64_t z = blockIdx.x / per;
+    const int at = (int)(blockIdx.x % per) * 64 + lane;
+    const float4v* from = (const float4v*)u.gram + z * u.panels * quads + at;
+    float4v s = {};
+    int i = k;
+    for (; i + 12 < u.panels; i += 16) {
+        const float4v a = from[(int64_t)i * quads], b = from[(int64_t)(i + 4) * quads],
+                      c = from[(int64_t)(i + 8) * quads], d = from[(int64_t)(i + 12) * quads];
+        s += (a + b) + (c + d);
+    }
+    for (; i < u.panels; i += 4) s += from[(int64_t)i * quads];
+    l[k][lane] = s;
+    __syncthreads();
+    if (k != 0) return;
+    s = (l[0][lane] + l[1][lane]) + (l[2][lane] + l[3][lane]);
+    half4 h;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = (_Float16)s[e];
+    ((half4*)u.a16)[z * quads + at] = h;
 }
 
 // ------------------------------------------------------------------ host ---
@@ -806,16 +963,44 @@ static NsShape ns_shape(int64_t batch, int64_t m, int64_t n) {
     return s;
 }
 
-// The launch for small matrices, where there is one: 128 rows (the smaller
-// side) by 512, 64 by 1024 or less.
+// Matrices of up to 128 rows or columns: in one launch where a panel holds them
+// (128 x 512 or 64 x 1024 and less), in panels else.  Few matrices of 128 x 512
+// are better off in panels, which take more CUs: one takes 54 us against 60,
+// 32 of them 88 (of 128 x 600) against 64.
+static bool ns_is_narrow(const NsShape& sh) { return sh.r <= 128; }
 static bool ns_is_small(const NsShape& sh) {
-    return sh.r <= 128 && (int64_t)(sh.r <= 64 ? 64 : 128) * sh.c <= 65536;
+    if (sh.r <= 64) return sh.c <= 1024;
+    return sh.r <= 128 && sh.c <= (sh.batch <= 4 ? 256 : 512);
+}
+// Columns of a wide matrix's panel.
+static int ns_panel_cols(const NsShape& sh) { return sh.r <= 64 ? 256 : 128; }
+
+// Lays the buffers of `batch` wide matrices out from `base` (NULL to count).
+static size_t ns_panel_layout(const NsShape& s, int64_t batch, char* base, PanelRun* u) {
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        char* p = base ? base + at : nullptr;
+        at += align_up(bytes, 256);
+        return p;
+    };
+    const int cols = ns_panel_cols(s), r = s.r <= 64 ? 64 : 128;
+    u->panels = (int)ceil_div(s.c, cols);
+    const size_t n = (size_t)batch * u->panels;
+    u->part = (const double*)take((size_t)batch * kNormParts * sizeof(double));
+    u->x32 = (float*)take(n * r * cols * 4);
+    u->gram = (float*)take(n * r * r * 4);
+    u->a16 = (_Float16*)take((size_t)batch * r * r * 2);
+    return at;
 }
 
 // Lays the buffers out from `base` (NULL to count only); returns the bytes.
 static size_t ns_layout(const NsShape& s, char* base, NsBuffers* w) {
     size_t at = 0;
     if (ns_is_small(s)) return 256;  // unused: every call takes a workspace
+    if (ns_is_narrow(s)) {
+        PanelRun u;
+        return ns_panel_layout(s, s.batch, nullptr, &u);
+    }
     auto take = [&](size_t bytes) {
         char* p = base ? base + at : nullptr;
         at += align_up(bytes, 256);
@@ -941,8 +1126,8 @@ static int ns_product(const NsBuffers& w, const NsShape& sh, const NsStep& st, i
 }
 
 template <int R, int FN, int W>
-static int ns_small_launch(const SmallRun& u, const NsShape& sh, const NsStep& st, hipStream_t s) {
-    constexpr int bytes = 16 * R * (16 * W * FN + 128) * 2;
+static int ns_small_launch(const PanelRun& u, const NsShape& sh, const NsStep& st, hipStream_t s) {
+    constexpr int bytes = Panel<R, FN, W>::kBytes;
     if constexpr (bytes > 64 * 1024) {
         SPOPT_HIP(hipFuncSetAttribute((const void*)k_ns_small<R, FN, W>,
                                       hipFuncAttributeMaxDynamicSharedMemorySize, bytes));
@@ -950,7 +1135,7 @@ static int ns_small_launch(const SmallRun& u, const NsShape& sh, const NsStep& s
     const int64_t chunk = 1 << 22;  // blocks of a grid
     for (int64_t z = 0; z < sh.batch; z += chunk) {
         const int64_t nb = sh.batch - z < chunk ? sh.batch - z : chunk, at = z * sh.m * sh.n;
-        SmallRun v = u;
+        PanelRun v = u;
         NsStep sz = st;
         v.g = (const char*)u.g + at * (u.gbf16 ? 2 : 4);
         if (u.buf) v.buf += at;
@@ -961,7 +1146,7 @@ static int ns_small_launch(const SmallRun& u, const NsShape& sh, const NsStep& s
     return SPOPT_OK;
 }
 
-static int ns_small(const SmallRun& u, const NsShape& sh, const NsStep& st, hipStream_t s) {
+static int ns_small(const PanelRun& u, const NsShape& sh, const NsStep& st, hipStream_t s) {
     const int64_t fn = ceil_div(sh.c, 128);
     if (sh.r <= 64)
         return fn <= 1   ? ns_small_launch<4, 1, 8>(u, sh, st, s)
@@ -973,19 +1158,69 @@ static int ns_small(const SmallRun& u, const NsShape& sh, const NsStep& st, hipS
                      : ns_small_launch<8, 2, 16>(u, sh, st, s);
 }
 
+// Wide matrices: the norm's slices, X0, and two launches a step.
+template <class G, int R, int FN>
+static int ns_panels(PanelRun r, Source<G> u, const NsShape& sh, const NsStep& st,
+                     void* workspace, hipStream_t s) {
+    const int64_t numel = sh.m * sh.n;
+    constexpr int bytes = Panel<R, FN, 8>::kBytes, quads = 64 * R * R;
+    static_assert(bytes <= 64 * 1024, "no attribute is set for more");
+    PanelRun all = r;
+    ns_panel_layout(sh, sh.batch, (char*)workspace, &all);
+    // As many matrices at a time as keep the grids below 2^22 blocks.
+    int64_t chunk = ((int64_t)1 << 22) / all.panels;
+    if (chunk > 4096) chunk = 4096;
+    for (int64_t z0 = 0; z0 < sh.batch; z0 += chunk) {
+        const unsigned nb = (unsigned)(sh.batch - z0 < chunk ? sh.batch - z0 : chunk);
+        PanelRun v = all;
+        Source<G> uz = u;
+        NsStep sz = st;
+        uz.g += z0 * numel;
+        if (u.buf) uz.buf += z0 * numel;
+        v.g = uz.g;
+        if (r.buf) v.buf += z0 * numel;
+        sz.out = (char*)st.out + z0 * numel * (r.mode == kParam32 ? 4 : 2);
+        v.part += z0 * kNormParts;
+        v.x32 += z0 * v.panels * 16 * R * Panel<R, FN, 8>::kX;
+        v.gram += z0 * v.panels * quads * 4;
+        v.a16 += z0 * quads * 4;
+        k_ns_norm<G><<<dim3((unsigned)r.parts, nb), 256, 0, s>>>(uz, v.buf, numel, (double*)v.part);
+        const unsigned grid = nb * (unsigned)v.panels;
+        k_ns_panel<R, FN, false><<<grid, 512, bytes, s>>>(v, sh, sz, 0);
+        for (int k = 0; k < r.steps; ++k) {
+            k_ns_panel_sum<<<nb * (quads / 64), 256, 0, s>>>(v, quads);
+            k_ns_panel<R, FN, true><<<grid, 512, bytes, s>>>(v, sh, sz, k + 1 == r.steps);
+        }
+        SPOPT_LAUNCHED();
+    }
+    return SPOPT_OK;
+}
+
 template <class G>
 static int ns_run(const NsShape& sh, Source<G> u, float* buf, const spopt_ns_config& c,
-                  NsBuffers w, int last, NsStep st, hipStream_t s) {
+                  void* workspace, int last, NsStep st, hipStream_t s) {
     const int64_t numel = sh.m * sh.n;
     int64_t parts = ceil_div(numel, 256 * 16);
     if (parts > kNormParts) parts = kNormParts;
     st.a = (float)c.coef[0];
     st.b = (float)c.coef[1];
     st.c = (float)c.coef[2];
-    if (ns_is_small(sh)) {
-        const SmallRun r = {u.kind, sizeof(G) == 2, last, u.g, buf, u.mu, c.eps, c.steps};
-        return ns_small(r, sh, st, s);
-    }
+    PanelRun pr{};
+    pr.kind = u.kind;
+    pr.gbf16 = sizeof(G) == 2;
+    pr.mode = last;
+    pr.g = u.g;
+    pr.buf = buf;
+    pr.mu = u.mu;
+    pr.eps = c.eps;
+    pr.steps = c.steps;
+    pr.parts = (int)parts;
+    if (ns_is_small(sh)) return ns_small(pr, sh, st, s);
+    if (ns_is_narrow(sh))
+        return sh.r <= 64 ? ns_panels<G, 4, 2>(pr, u, sh, st, workspace, s)
+                          : ns_panels<G, 8, 1>(pr, u, sh, st, workspace, s);
+    NsBuffers w;
+    ns_layout(sh, (char*)workspace, &w);
     const int tr = sh.rp / kTile, tc = sh.cp / kTile;
     // The batch in the grids' last axis: at most so many matrices at a time.
     const int64_t chunk = 32768;
@@ -1026,10 +1261,10 @@ static int ns_run(const NsShape& sh, Source<G> u, float* buf, const spopt_ns_con
 
 static bool is_matrix_type(int32_t t) { return t == SPOPT_DTYPE_F32 || t == SPOPT_DTYPE_BF16; }
 
-// What newton_schulz and muon_step check alike; fills the workspace's layout.
+// What newton_schulz and muon_step check alike.
 static int ns_enter(const char* what, const void* g, int32_t gdtype, const void* out,
-                    const NsShape& sh, const spopt_ns_config& c, void* workspace,
-                    size_t workspace_bytes, NsBuffers* w, hipStream_t s, uint32_t flags) {
+                    const NsShape& sh, const spopt_ns_config& c, const void* workspace,
+                    size_t workspace_bytes, hipStream_t s, uint32_t flags) {
     if (!is_matrix_type(gdtype))
         return fail(SPOPT_EINVAL, "%s: gradient type %d is neither float32 nor bfloat16", what,
                     gdtype);
@@ -1037,11 +1272,11 @@ static int ns_enter(const char* what, const void* g, int32_t gdtype, const void*
     if (rc) return rc;
     if (sh.batch > 0 && (g == nullptr || out == nullptr))
         return fail(SPOPT_EINVAL, "%s: NULL matrix", what);
-    const size_t need = ns_layout(sh, nullptr, w);
+    NsBuffers w;
+    const size_t need = ns_layout(sh, nullptr, &w);
     if (sh.batch > 0 && (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need))
         return fail(SPOPT_EWORKSPACE, "%s: workspace of %zu bytes, needs %zu", what,
                     workspace_bytes, need);
-    ns_layout(sh, (char*)workspace, w);
     if ((flags & SPOPT_VALIDATE) && sh.batch > 0)
         return validate_on_device(s, false, what, [&](uint32_t* status) {
             return launch_check_finite(g, gdtype, sh.batch * sh.m, sh.n, sh.n, status, s);
@@ -1070,17 +1305,16 @@ extern "C" int newton_schulz(const void* g, int32_t dtype, int64_t batch, int64_
     int rc = ns_check_size("newton_schulz", batch, m, n);
     if (rc) return rc;
     const NsShape sh = ns_shape(batch, m, n);
-    NsBuffers w;
-    rc = ns_enter("newton_schulz", g, dtype, out, sh, *config, workspace, workspace_bytes, &w, s,
+    rc = ns_enter("newton_schulz", g, dtype, out, sh, *config, workspace, workspace_bytes, s,
                   flags);
     if (rc || batch == 0) return rc;
     NsStep st{};
     st.out = out;
     if (dtype == SPOPT_DTYPE_F32)
-        return ns_run(sh, Source<float>{(const float*)g, nullptr, 0.f, 0}, nullptr, *config, w,
-                      kOut, st, s);
-    return ns_run(sh, Source<__bf16>{(const __bf16*)g, nullptr, 0.f, 0}, nullptr, *config, w, kOut,
-                  st, s);
+        return ns_run(sh, Source<float>{(const float*)g, nullptr, 0.f, 0}, nullptr, *config,
+                      workspace, kOut, st, s);
+    return ns_run(sh, Source<__bf16>{(const __bf16*)g, nullptr, 0.f, 0}, nullptr, *config,
+                  workspace, kOut, st, s);
 }
 
 extern "C" int muon_step(void* params, int32_t pdtype, float* buf, const void* g, int32_t gdtype,
@@ -1106,8 +1340,7 @@ extern "C" int muon_step(void* params, int32_t pdtype, float* buf, const void* g
     if (batch > 0 && c.momentum != 0.0 && buf == nullptr)
         return fail(SPOPT_EINVAL, "muon_step: a momentum needs its buffer");
     const NsShape sh = ns_shape(batch, m, n);
-    NsBuffers w;
-    rc = ns_enter("muon_step", g, gdtype, params, sh, c.ns, workspace, workspace_bytes, &w, s,
+    rc = ns_enter("muon_step", g, gdtype, params, sh, c.ns, workspace, workspace_bytes, s,
                   flags);
     if (rc || batch == 0) return rc;
     NsStep st{};
@@ -1118,8 +1351,8 @@ extern "C" int muon_step(void* params, int32_t pdtype, float* buf, const void* g
     const int kind = c.momentum == 0.0 ? 0 : c.nesterov ? 2 : 1;
     float* b = kind ? buf : nullptr;
     if (gdtype == SPOPT_DTYPE_F32)
-        return ns_run(sh, Source<float>{(const float*)g, b, (float)c.momentum, kind}, b, c.ns, w,
-                      last, st, s);
-    return ns_run(sh, Source<__bf16>{(const __bf16*)g, b, (float)c.momentum, kind}, b, c.ns, w,
-                  last, st, s);
+        return ns_run(sh, Source<float>{(const float*)g, b, (float)c.momentum, kind}, b, c.ns,
+                      workspace, last, st, s);
+    return ns_run(sh, Source<__bf16>{(const __bf16*)g, b, (float)c.momentum, kind}, b, c.ns,
+                  workspace, last, st, s);
 }

@@ -211,11 +211,35 @@ def test_more_large_matrices_than_one_grid_takes():
 
 
 @pytest.mark.parametrize("shape", [(64, 1024), (1023, 63), (128, 512), (511, 127), (2, 64, 1000),
-                                   (64, 1025), (128, 513), (120, 130), (3, 520, 128), (33, 2100)],
+                                   (64, 1025), (128, 513), (120, 130), (128, 256), (6, 128, 512),
+                                   (6, 400, 100), (3, 520, 128), (33, 2100)],
                          ids=lambda s: "x".join(map(str, s)))
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 def test_around_the_one_launch_sizes(shape, dtype):
     check_ns(matrix(*shape).to(dtype).cuda())
+
+
+@pytest.mark.parametrize("shape", [(1, 3000), (40, 5001), (5000, 64), (100, 1028), (2, 1500, 100),
+                                   (128, 4096), (3, 65, 700)],
+                         ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("pd,gd,momentum,nesterov", [(F32, F32, 0.95, True), (BF16, BF16, 0.9, False),
+                                                     (F32, BF16, 0.0, True)],
+                         ids=["f32", "bf16", "plain"])
+def test_muon_on_wide_matrices(shape, pd, gd, momentum, nesterov):
+    """Up to 128 rows or columns and more than one block holds."""
+    p = (matrix(*shape, kind="gauss", seed=5) * 0.05).to(pd).cuda()
+    buf = matrix(*shape, seed=8).cuda() if momentum else None
+    check_muon(p, matrix(*shape).to(gd).cuda(), buf, lr=0.02, momentum=momentum,
+               nesterov=nesterov, weight_decay=0.1, scale=1.5, steps=2)
+
+
+def test_more_wide_matrices_than_one_grid_takes():
+    batch, m, n = 4100, 64, 1025
+    g = torch.empty(batch, m, n, dtype=BF16, device="cuda").normal_()
+    out = L.newton_schulz(g)
+    for at in (0, 4095, 4096, batch - 1):
+        ref, bound = R.ns_error_bound(g[at])
+        assert (R.d(out[at]) - ref).norm() <= bound + R.HALF[BF16] * ref.norm()
 
 
 def test_validate_refuses_and_writes_nothing():
