@@ -13,12 +13,15 @@
 // which A * 2^12 follows without a factor, and B as it is: entries of B below
 // float16's normal range are off by 2^-25 at most, which a X is not changed by
 // (entries are bounded by the largest singular value, which the host checks).
-// X is also carried in float32, for the
-// a X term: in the directions of small singular values B is near zero, so that
-// rounding errors of X come in through a X alone there, and grow by a factor of
-// a in every step.  Errors against 64 bits, relative to the result's norm, for
-// 256 to 1024 rows and Gaussian, low-rank and decaying spectra: at most 1.7e-3;
-// 7e-3 with X in float16 alone, 6e-2 with all of it in bfloat16.
+// X is also carried in float32, for the a X term: in the directions of small
+// singular values B is near zero, so that rounding errors of X come in through
+// a X alone there, and grow by a factor of a in every step.  B's diagonal joins
+// that term, in float32 too: as X's rows become orthonormal it nears b + c
+// while the rest of B vanishes, and float16 would round it to 5e-4.  Errors
+// against 64 bits, relative to the result's norm, for 64 to 1024 rows and
+// Gaussian, low-rank and decaying spectra: at most 1.3e-3; 2.6e-3 with the
+// diagonal in float16, 7e-3 with X in float16 alone, 6e-2 with all of it in
+// bfloat16.
 #include <math.h>
 
 #include <type_traits>
@@ -102,7 +105,8 @@ struct NsBuffers {
     _Float16* x[2];  // [batch][rp * cp]   X * 2^6, one step's and the next's
     float* x32;      // [batch][rp * cp]   X * 2^6
     _Float16* a16;   // [batch][rp * rp]   A * 2^12
-    _Float16* b16;   // [batch][rp * rp]   B
+    _Float16* b16;   // [batch][rp * rp]   B but for its diagonal
+    float* diag;     // [batch][rp]        B's diagonal
     double* part;    // [batch][kNormParts]
 };
 
@@ -429,16 +433,22 @@ __global__ __launch_bounds__(T::kThreads) void k_ns_gemm(NsBuffers w, NsShape sh
                     if (MODE == kPoly) load_v<_Float16, kRow>(w.a16 + o, a8);
 #pragma unroll
                     for (int e = 0; e < kRow; ++e)
-                        if (MODE == kPoly)
+                        if (MODE == kPoly) {
                             v[e] = st.b / kAScale * a8[e] + st.c / (kAScale * kAScale) * v[e];
+                            if (i == j + e) {
+                                w.diag[z * sh.rp + i] = v[e];
+                                v[e] = 0.f;
+                            }
+                        }
                     store_v<_Float16, kRow>((MODE == kGram ? w.a16 : w.b16) + o, v);
                 } else {
                     const int64_t o = z * nx + (int64_t)i * sh.cp + j;
                     float x0[kRow];
                     load_v<float, kRow>(w.x32 + o, x0);
+                    const float a = st.a + w.diag[z * sh.rp + i];
                     // X * 2^6 of the next step
 #pragma unroll
-                    for (int e = 0; e < kRow; ++e) v[e] = st.a * x0[e] + v[e];
+                    for (int e = 0; e < kRow; ++e) v[e] = a * x0[e] + v[e];
                     if (MODE == kNext) {
                         store_v<float, kRow>(w.x32 + o, v);
                         store_v<_Float16, kRow>(w.x[from ^ 1] + o, v);
@@ -515,17 +525,20 @@ template <int R, int FN, int W>
 struct Panel {
     static constexpr int kX = 16 * W * FN, kA = 128;
     static constexpr int FA = R / 4, FB = 4 * R / W;  // a wave's part of the square
-    static constexpr int kBytes = 16 * R * (kX + kA) * 2;
+    static constexpr int kBytes = 16 * R * ((kX + kA) * 2 + 4);
     // Of 16 waves' square parts the 6 above the diagonal are mirrored ones.
     static constexpr bool kMirror = W == 16;
     _Float16 *lx, *la;
+    float* diag;          // B's diagonal
     int lane, l15, g4, ft, wj, wr, wc;
     uint32_t di, dj;      // strides of X's rows and columns in the input
     int rows, cols;       // of the input's, from this panel's first column on
     bool by_four;         // four adjacent columns lie together in the input
 
     __device__ __forceinline__ Panel(char* lds, const NsShape& sh, int first_col)
-        : lx((_Float16*)lds), la((_Float16*)lds + 16 * R * kX) {
+        : lx((_Float16*)lds),
+          la((_Float16*)lds + 16 * R * kX),
+          diag((float*)(lds + 16 * R * (kX + kA) * 2)) {
         const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         wj = wv * 16 * FN;
         wr = wv / (W / 4);
@@ -719,8 +732,17 @@ struct Panel {
             for (int x = 0; x < FA; ++x)
 #pragma unroll
                 for (int y = 0; y < FB; ++y)
-                    gb[x][y] = ga[x][y] * (st.b / kAScale) +
-                               gb[x][y] * (st.c / (kAScale * kAScale));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        // A as the square was taken of it: its rounding then moves
+                        // both terms, which nearly cancel.
+                        gb[x][y][e] = (float)(_Float16)ga[x][y][e] * (st.b / kAScale) +
+                                      gb[x][y][e] * (st.c / (kAScale * kAScale));
+                        if (FA * wr + x == FB * wc + y && l15 == 4 * g4 + e) {
+                            diag[16 * (FA * wr + x) + l15] = gb[x][y][e];
+                            gb[x][y][e] = 0.f;
+                        }
+                    }
         }
         __syncthreads();
         if (in_square()) put_square(gb);
@@ -729,9 +751,11 @@ struct Panel {
     // X <- a X + B X: the accumulators start at a X.
     __device__ __forceinline__ void next(float a, float4v (&xv)[R][FN]) const {
 #pragma unroll
-        for (int x = 0; x < R; ++x)
+        for (int x = 0; x < R; ++x) {
+            const float f = a + diag[16 * x + l15];
 #pragma unroll
-            for (int y = 0; y < FN; ++y) xv[x][y] *= a;
+            for (int y = 0; y < FN; ++y) xv[x][y] *= f;
+        }
 #pragma unroll
         for (int kk = 0; kk < R / 2; ++kk) {
             half8 fa[R], fb[FN];
@@ -963,14 +987,11 @@ static NsShape ns_shape(int64_t batch, int64_t m, int64_t n) {
     return s;
 }
 
-// Matrices of up to 128 rows or columns: in one launch where a panel holds them
-// (128 x 512 or 64 x 1024 and less), in panels else.  Few matrices of 128 x 512
-// are better off in panels, which take more CUs: one takes 54 us against 60,
-// 32 of them 88 (of 128 x 600) against 64.
+// Matrices of up to 128 rows or columns: in one launch where a panel holds them,
+// in panels else.
 static bool ns_is_narrow(const NsShape& sh) { return sh.r <= 128; }
 static bool ns_is_small(const NsShape& sh) {
-    if (sh.r <= 64) return sh.c <= 1024;
-    return sh.r <= 128 && sh.c <= (sh.batch <= 4 ? 256 : 512);
+    return sh.r <= 64 ? sh.c <= 1024 : sh.r <= 128 && sh.c <= 256;
 }
 // Columns of a wide matrix's panel.
 static int ns_panel_cols(const NsShape& sh) { return sh.r <= 64 ? 256 : 128; }
@@ -1013,6 +1034,7 @@ static size_t ns_layout(const NsShape& s, char* base, NsBuffers* w) {
     w->x32 = (float*)take(nx * 4);
     w->a16 = (_Float16*)take(na * 2);
     w->b16 = (_Float16*)take(na * 2);
+    w->diag = (float*)take((size_t)s.batch * s.rp * 4);
     return at;
 }
 
@@ -1153,9 +1175,8 @@ static int ns_small(const PanelRun& u, const NsShape& sh, const NsStep& st, hipS
                : fn <= 2 ? ns_small_launch<4, 1, 16>(u, sh, st, s)
                : fn <= 4 ? ns_small_launch<4, 2, 16>(u, sh, st, s)
                          : ns_small_launch<4, 4, 16>(u, sh, st, s);
-    return fn <= 1   ? ns_small_launch<8, 1, 8>(u, sh, st, s)
-           : fn <= 2 ? ns_small_launch<8, 1, 16>(u, sh, st, s)
-                     : ns_small_launch<8, 2, 16>(u, sh, st, s);
+    return fn <= 1 ? ns_small_launch<8, 1, 8>(u, sh, st, s)
+                   : ns_small_launch<8, 1, 16>(u, sh, st, s);
 }
 
 // Wide matrices: the norm's slices, X0, and two launches a step.
@@ -1164,7 +1185,10 @@ static int ns_panels(PanelRun r, Source<G> u, const NsShape& sh, const NsStep& s
                      void* workspace, hipStream_t s) {
     const int64_t numel = sh.m * sh.n;
     constexpr int bytes = Panel<R, FN, 8>::kBytes, quads = 64 * R * R;
-    static_assert(bytes <= 64 * 1024, "no attribute is set for more");
+    SPOPT_HIP(hipFuncSetAttribute((const void*)k_ns_panel<R, FN, false>,
+                                  hipFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    SPOPT_HIP(hipFuncSetAttribute((const void*)k_ns_panel<R, FN, true>,
+                                  hipFuncAttributeMaxDynamicSharedMemorySize, bytes));
     PanelRun all = r;
     ns_panel_layout(sh, sh.batch, (char*)workspace, &all);
     // As many matrices at a time as keep the grids below 2^22 blocks.
@@ -1234,6 +1258,7 @@ static int ns_run(const NsShape& sh, Source<G> u, float* buf, const spopt_ns_con
         v.x32 += z0 * nx;
         v.a16 += z0 * na;
         v.b16 += z0 * na;
+        v.diag += z0 * sh.rp;
         Source<G> uz = u;
         uz.g += z0 * numel;
         if (u.buf) uz.buf += z0 * numel;

@@ -76,7 +76,7 @@ def ln_backward_bounds(dy, x, mu, rs, w, wdtype):
 
 def newton_schulz(g, steps=5, coef=(3.4445, -4.7750, 2.0315), eps=1e-7, rounded=False):
     """The iteration in 64 bits; `rounded` puts in the kernels' roundings of the operands to
-    float16 (X * 2^6, A * 2^12, B) and nothing else."""
+    float16 (X * 2^6, A * 2^12, B but for its diagonal) and nothing else."""
     def r16(t, s):
         return (t * s).half().double() / s if rounded else t
     x = d(g)
@@ -87,7 +87,9 @@ def newton_schulz(g, steps=5, coef=(3.4445, -4.7750, 2.0315), eps=1e-7, rounded=
     for _ in range(steps):
         xh = r16(x, 64.0)
         gram = r16(xh @ xh.mT.contiguous(), 4096.0)
-        x = a * x + r16(b * gram + c * (gram @ gram.mT.contiguous()), 1.0) @ xh
+        poly = b * gram + c * (gram @ gram.mT.contiguous())
+        diag = poly.diagonal(dim1=-2, dim2=-1)[..., None]
+        x = (a + diag) * x + r16(poly - torch.diag_embed(diag[..., 0]), 1.0) @ xh
     return x.mT if flip else x
 
 
