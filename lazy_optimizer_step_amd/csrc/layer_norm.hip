@@ -12,7 +12,7 @@
 
 namespace spopt {
 
-// Sum over the G lanes of a group that share a row (G = 16, 32 or 64): every
+// Sum over the G lanes of a group that share a row (G = 4 to 64): every
 // lane gets it.  The first four exchanges stay in the vector unit: quads, then
 // mirrors of 8 and 16 lanes, which join sums that are already alike within
 // each half.
@@ -24,8 +24,8 @@ __device__ __forceinline__ float lane_sum(float v) {
     };
     v += dpp(v, std::integral_constant<int, 0xB1>{});   // quad_perm 1,0,3,2
     v += dpp(v, std::integral_constant<int, 0x4E>{});   // quad_perm 2,3,0,1
-    v += dpp(v, std::integral_constant<int, 0x141>{});  // row_half_mirror
-    v += dpp(v, std::integral_constant<int, 0x140>{});  // row_mirror
+    if (G >= 8) v += dpp(v, std::integral_constant<int, 0x141>{});   // row_half_mirror
+    if (G >= 16) v += dpp(v, std::integral_constant<int, 0x140>{});  // row_mirror
     if (G >= 32) v += __shfl_xor(v, 16, kWave);
     if (G >= 64) v += __shfl_xor(v, 32, kWave);
     return v;
@@ -372,35 +372,37 @@ __global__ __launch_bounds__(256) void k_ln_cols_any(const T* dy, int64_t ds, co
     }
 }
 
-// dweight and dbias from the slices' sums: a block takes 16 columns of one of
-// the two, 64 threads on each column's slices, joined in double in a fixed
+// dweight and dbias from the slices' sums: a block takes 32 columns of one of
+// the two, 16 threads on each column's slices, joined in double in a fixed
 // order.
 template <class W>
-__global__ __launch_bounds__(1024) void k_ln_join(const float* part, int64_t slices, int64_t cols,
-                                                  W* dw, W* db) {
-    __shared__ double l[64][17];
-    const int q = threadIdx.x & 15, k = threadIdx.x >> 4;
-    const int64_t c = (int64_t)blockIdx.x * 16 + q;
+__global__ __launch_bounds__(512) void k_ln_join(const float* part, int64_t slices, int64_t cols,
+                                                 W* dw, W* db) {
+    __shared__ double l[16][33];
+    const int q = threadIdx.x & 31, k = threadIdx.x >> 5;
+    const int64_t c = (int64_t)blockIdx.x * 32 + q;
     W* out = blockIdx.y ? db : dw;
     if (out == nullptr) return;
     double s = 0.;
     if (c < cols) {
         const float* p = part + blockIdx.y * cols + c;
         int64_t i = k;
-        for (; i + 192 < slices; i += 256) {  // four loads at once
-            const float v0 = p[i * 2 * cols], v1 = p[(i + 64) * 2 * cols],
-                        v2 = p[(i + 128) * 2 * cols], v3 = p[(i + 192) * 2 * cols];
-            s += ((double)v0 + (double)v1) + ((double)v2 + (double)v3);
+        for (; i + 112 < slices; i += 128) {  // eight loads at once
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = p[(i + 16 * e) * 2 * cols];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += (double)v[e];
         }
-        for (; i < slices; i += 64) s += (double)p[i * 2 * cols];
+        for (; i < slices; i += 16) s += (double)p[i * 2 * cols];
     }
     l[k][q] = s;
     __syncthreads();
-    for (int n = 32; n; n >>= 1) {
-        if (k < n) l[k][q] += l[k + n][q];
-        __syncthreads();
-    }
-    if (k == 0 && c < cols) out[c] = (W)(float)l[0][q];
+    if (k != 0 || c >= cols) return;
+    s = 0.;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s += l[e][q];
+    out[c] = (W)(float)s;
 }
 
 // How a row is shared out: G lanes of NV chunks of V values hold it.
@@ -413,9 +415,9 @@ struct RowPlan {
 // up to 32 values a lane forward (16 backward, which keeps dy, x and two sums
 // of each), a block beyond, as then several rows' loads still fit a CU.
 static RowPlan ln_plan(int64_t cols, int v, bool backward) {
-    static const RowPlan fwd[] = {{16, 1}, {32, 1}, {64, 1}, {64, 2}, {64, 4}, {256, 2}, {256, 4},
+    static const RowPlan fwd[] = {{4, 1}, {8, 1}, {16, 1}, {32, 1}, {64, 1}, {64, 2}, {64, 4}, {256, 2}, {256, 4},
                                   {256, 8}, {1024, 4}};
-    static const RowPlan bwd[] = {{16, 1}, {32, 1}, {64, 1}, {64, 2}, {256, 1}, {256, 2}, {512, 2},
+    static const RowPlan bwd[] = {{4, 1}, {8, 1}, {16, 1}, {32, 1}, {64, 1}, {64, 2}, {256, 1}, {256, 2}, {512, 2},
                                   {1024, 2}, {1024, 4}};
     if (cols < v) return {16, 1, true};
     if (backward) {
@@ -434,15 +436,15 @@ static RowPlan ln_plan(int64_t cols, int v, bool backward) {
 // row reads and writes: 256 slices fill the card, more only while their sums
 // stay below an eighth of the rows' traffic (2048 x 16384 bfloat16, 512 slices:
 // half of it), 512 at most.
-static int64_t ln_slices(int64_t rows, int64_t cols, int64_t bytes) {
-    if (cols <= 1024) {
-        const int64_t s = ceil_div(rows, 16);
-        return s < 1 ? 1 : s > 1024 ? 1024 : s;
-    }
-    int64_t s = rows * 3 * bytes / 64;
-    if (s < 256) s = 256;
-    if (s > 512) s = 512;
-    return s > rows ? (rows < 1 ? 1 : rows) : s;
+static int64_t ln_slices(int64_t rows, int64_t cols, int64_t bytes, int64_t* per) {
+    int64_t s = cols <= 1024 ? ceil_div(rows, 16) : rows * 3 * bytes / 64;
+    if (cols > 1024 && s < 256) s = 256;
+    const int64_t most = cols <= 1024 ? 1024 : 512;
+    if (s > most) s = most;
+    *per = s < 1 ? 1 : ceil_div(rows, s);
+    if (*per < 1) *per = 1;
+    s = ceil_div(rows, *per);  // no empty slice
+    return s < 1 ? 1 : s;
 }
 
 static int ln_check(const char* what, int64_t rows, int64_t cols, int32_t dtype, int32_t wdtype) {
@@ -515,6 +517,8 @@ extern "C" int layer_norm_forward(const void* x, int64_t x_stride, int64_t rows,
         };
         auto at = [&](auto nv, auto g) { go(Int<V>{}, nv, g); };
         if (p.one) go(Int<1>{}, Int<1>{}, Int<16>{});
+        else if (p.g == 4) at(Int<1>{}, Int<4>{});
+        else if (p.g == 8) at(Int<1>{}, Int<8>{});
         else if (p.g == 16) at(Int<1>{}, Int<16>{});
         else if (p.g == 32) at(Int<1>{}, Int<32>{});
         else if (p.g == 64 && p.nv == 1) at(Int<1>{}, Int<64>{});
@@ -538,7 +542,9 @@ extern "C" int layer_norm_backward_workspace_size(int64_t rows, int64_t cols, si
         cols > INT64_MAX / 8192)
         return fail(SPOPT_EINVAL, "layer_norm_backward_workspace_size: bad size %lld x %lld",
                     (long long)rows, (long long)cols);
-    *bytes = (size_t)ln_slices(rows, cols, 4) * 2 * (size_t)cols * sizeof(float);
+    int64_t per;
+    const int64_t two = ln_slices(rows, cols, 2, &per), four = ln_slices(rows, cols, 4, &per);
+    *bytes = (size_t)(two > four ? two : four) * 2 * (size_t)cols * sizeof(float);
     return SPOPT_OK;
 }
 
@@ -570,15 +576,15 @@ extern "C" int layer_norm_backward(const void* dy, int64_t dy_stride, const void
         });
         if (rc) return rc;
     }
-    int64_t slices = rows == 0 ? 0 : ln_slices(rows, cols, (int64_t)dtype_bytes(dtype));
+    int64_t per;
+    int64_t slices = ln_slices(rows, cols, (int64_t)dtype_bytes(dtype), &per);
+    if (rows == 0) slices = 0;
     ln_types(dtype, wdtype, [&](auto t, auto wt) {
         using T = decltype(t);
         using W = decltype(wt);
         constexpr int V = 16 / sizeof(T);
         float* part = sums ? (float*)workspace : nullptr;
         const RowPlan p = ln_plan(cols, V, true);
-        const int64_t per = slices ? ceil_div(rows, slices) : 0;
-        if (slices) slices = ceil_div(rows, per);  // no empty slice
         auto go = [&](auto v, auto nv, auto g) {
             constexpr int G = decltype(g)::value;
             k_ln_bwd<T, W, decltype(v)::value, decltype(nv)::value, G>
@@ -589,6 +595,8 @@ extern "C" int layer_norm_backward(const void* dy, int64_t dy_stride, const void
         auto at = [&](auto nv, auto g) { go(Int<V>{}, nv, g); };
         if (rows == 0 || (!sums && dx == nullptr)) {
         } else if (p.one) go(Int<1>{}, Int<1>{}, Int<16>{});
+        else if (p.g == 4) at(Int<1>{}, Int<4>{});
+        else if (p.g == 8) at(Int<1>{}, Int<8>{});
         else if (p.g == 16) at(Int<1>{}, Int<16>{});
         else if (p.g == 32) at(Int<1>{}, Int<32>{});
         else if (p.g == 64 && p.nv == 1) at(Int<1>{}, Int<64>{});
@@ -611,7 +619,7 @@ extern "C" int layer_norm_backward(const void* dy, int64_t dy_stride, const void
                     (const W*)weight, (T*)dx, dx_stride);
         }
         if (sums)
-            k_ln_join<W><<<dim3((unsigned)ceil_div(cols, 16), 2), 1024, 0, s>>>(
+            k_ln_join<W><<<dim3((unsigned)ceil_div(cols, 32), 2), 512, 0, s>>>(
                 part, slices, cols, (W*)dweight, (W*)dbias);
     });
     SPOPT_LAUNCHED();
