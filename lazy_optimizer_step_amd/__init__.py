@@ -41,7 +41,7 @@ def _stream(stream) -> int:
     if stream is None:
         # The raw handle of torch.cuda.current_stream(), without the object
         # around it (0.1 against 2.8 us a call).
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)

@@ -10,6 +10,7 @@ C ABI's names and only marshal arguments, as the package's other functions do;
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import math
 
 import torch
@@ -100,19 +101,21 @@ def layer_norm_forward(x: torch.Tensor, weight=None, bias=None, *, eps: float = 
         _need(mean, torch.float32, "mean", rows)
     if rstd is not None:
         _need(rstd, torch.float32, "rstd", rows)
-    with _alloc_on(stream):
-        if out is None:
-            out = _like(x)
-        if mean is None:
-            mean = x.new_empty(x.shape[:-1], dtype=torch.float32)
-        if rstd is None:
-            rstd = torch.empty_like(mean)
-    check(_lib.lib().layer_norm_forward(_ptr(x), xs, rows, cols, _DTYPES[x.dtype], _ptr(weight),
-                                        _ptr(bias), wdtype, eps, _ptr(out), ys, _ptr(mean),
-                                        _ptr(rstd), _stream(stream), _flags(validate)))
+    if out is None or mean is None or rstd is None:
+        with _alloc_on(stream):
+            if out is None:
+                out = _like(x)
+            if mean is None:
+                mean = x.new_empty(x.shape[:-1], dtype=torch.float32)
+            if rstd is None:
+                rstd = torch.empty_like(mean)
+    check(_lib.lib().layer_norm_forward(
+        x.data_ptr(), xs, rows, cols, _DTYPES[x.dtype], _ptr(weight), _ptr(bias), wdtype, eps,
+        out.data_ptr(), ys, mean.data_ptr(), rstd.data_ptr(), _stream(stream), _flags(validate)))
     return out, mean, rstd
 
 
+@functools.lru_cache(maxsize=1024)
 def layer_norm_backward_workspace_size(rows: int, cols: int) -> int:
     out = C.c_size_t(0)
     check(_lib.lib().layer_norm_backward_workspace_size(rows, cols, C.byref(out)))
@@ -233,6 +236,7 @@ def _ns_config(coefficients, eps, steps) -> _lib.NsConfig:
     return _lib.NsConfig((C.c_double * 3)(a, b, c), eps, steps)
 
 
+@functools.lru_cache(maxsize=1024)
 def newton_schulz_workspace_size(batch: int, m: int, n: int) -> int:
     out = C.c_size_t(0)
     check(_lib.lib().newton_schulz_workspace_size(batch, m, n, C.byref(out)))
