@@ -102,6 +102,17 @@ __global__ __launch_bounds__(256) void k_ns_norm(Source<G> u, float* buf, int64_
     if (threadIdx.x == 0) part[(int64_t)blockIdx.y * kNormParts + blockIdx.x] = s;
 }
 
+// x * 2^6 / (norm + eps) for the norm's square: the scale as a power of two and
+// a factor in [0.5, 1), as float32 alone would not hold every norm's reciprocal.
+struct NormScale {
+    int ex;
+    float f;
+    __device__ __forceinline__ NormScale(double sq, double eps) {
+        f = (float)frexp((double)kXScale / (sqrt(sq) + eps), &ex);
+    }
+    __device__ __forceinline__ float operator()(float x) const { return ldexpf(x, ex) * f; }
+};
+
 struct NsBuffers {
     _Float16* x[2];  // [batch][rp * cp]   X * 2^6, one step's and the next's
     float* x32;      // [batch][rp * cp]   X * 2^6
@@ -119,7 +130,9 @@ struct NsShape {
 
 // X0 = U / (|U| + eps) into the padded buffers, rows and columns beyond the
 // matrix as zeros.  One 64 x 64 tile of X per block, through LDS where X is the
-// input's transpose.  HBM bounds it: 4096 x 4096 float32 36 us (4.7 TB/s).
+// input's transpose.  HBM bounds it: 4096 x 4096 float32 31 us (5.4 TB/s, part of
+// it in the last-level cache); single values in place of fours took 36 us, and
+// 12.8 in place of 8.6 us at 1024 x 1024.
 template <class G>
 __global__ __launch_bounds__(256) void k_ns_init(Source<G> u, NsBuffers w, NsShape sh, int parts,
                                                  double eps) {
@@ -127,46 +140,62 @@ __global__ __launch_bounds__(256) void k_ns_init(Source<G> u, NsBuffers w, NsSha
     __shared__ float tile[kTile][kTile + 1];
     const int64_t z = blockIdx.z;
     const int i0 = blockIdx.y * kTile, j0 = blockIdx.x * kTile;
-    const int q = threadIdx.x & 63, k = threadIdx.x >> 6;
+    const int q = (threadIdx.x & 15) * 4, k = threadIdx.x >> 4;
     const int64_t base = z * sh.m * sh.n;
-    // All of the thread's values are asked for first, along the input's rows
-    // (those of X, or X's columns).
-    int64_t at[kTile / 4];
-    bool in[kTile / 4];
+    // Four adjacent values of four of the input's rows (those of X, or X's
+    // columns) are asked for before anything is waited for.
+    const int lines = sh.flip ? sh.c : sh.r, width = sh.flip ? sh.r : sh.c;
+    const int line0 = sh.flip ? j0 : i0, first = (sh.flip ? i0 : j0) + q;
+    const bool quad = first + 4 <= width;
+    float v[4][4] = {}, b[4][4];
+    auto read = [&](const auto* from, float (&x)[4][4]) {
+        typedef std::remove_cv_t<std::remove_reference_t<decltype(*from)>> E;
 #pragma unroll
-    for (int t = 0; t < kTile / 4; ++t) {
-        const int a = 4 * t + k;
-        const int i = sh.flip ? i0 + q : i0 + a, j = sh.flip ? j0 + a : j0 + q;
-        in[t] = i < sh.r && j < sh.c;
-        at[t] = base + (in[t] ? sh.flip ? (int64_t)j * sh.r + i : (int64_t)i * sh.c + j : 0);
-    }
-    float v[kTile / 4] = {}, b[kTile / 4];
-    if (u.kind != 1)
+        for (int t = 0; t < 4; ++t) {
+            const int line = line0 + 16 * t + k;
+            // Lines past the matrix read its last one, and count as zeros below.
+            const E* p = from + base + (int64_t)(line < lines ? line : lines - 1) * width;
+            if (quad) {
+                load_v<E, 4>(p + first, x[t]);
+            } else {
 #pragma unroll
-        for (int t = 0; t < kTile / 4; ++t) v[t] = (float)u.g[at[t]];
+                for (int e = 0; e < 4; ++e) x[t][e] = (float)p[first + e < width ? first + e : 0];
+            }
+        }
+    };
+    if (u.kind != 1) read(u.g, v);
     if (u.kind != 0) {
+        read(u.buf, b);
 #pragma unroll
-        for (int t = 0; t < kTile / 4; ++t) b[t] = u.buf[at[t]];
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int t = 0; t < kTile / 4; ++t) v[t] = u.kind == 1 ? b[t] : v[t] + u.mu * b[t];
+            for (int e = 0; e < 4; ++e)
+                v[t][e] = u.kind == 1 ? b[t][e] : v[t][e] + u.mu * b[t][e];
     }
     double sq = 0.;
     for (int t = threadIdx.x; t < parts; t += 256) sq += w.part[z * kNormParts + t];
-    const double scale = (double)kXScale / (sqrt(block_sum_d(sq, lds)) + eps);
+    const NormScale scale(block_sum_d(sq, lds), eps);
 #pragma unroll
-    for (int t = 0; t < kTile / 4; ++t) {
-        v[t] = in[t] ? (float)((double)v[t] * scale) : 0.f;
-        if (sh.flip) tile[q][4 * t + k] = v[t];
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool in = line0 + 16 * t + k < lines && first + e < width;
+            v[t][e] = in ? scale(v[t][e]) : 0.f;
+            if (sh.flip) tile[q + e][16 * t + k] = v[t][e];
+        }
+    if (sh.flip) {
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[t][e] = tile[16 * t + k][q + e];
     }
-    __syncthreads();
     const int64_t xb = z * sh.rp * sh.cp;
 #pragma unroll
-    for (int t = 0; t < kTile / 4; ++t) {
-        const int a = 4 * t + k;
-        const float x = sh.flip ? tile[a][q] : v[t];
-        const int64_t o = xb + (int64_t)(i0 + a) * sh.cp + j0 + q;
-        w.x[0][o] = (_Float16)x;
-        w.x32[o] = x;
+    for (int t = 0; t < 4; ++t) {
+        const int64_t o = xb + (int64_t)(i0 + 16 * t + k) * sh.cp + j0 + q;
+        store_v<_Float16, 4>(w.x[0] + o, v[t]);
+        store_v<float, 4>(w.x32 + o, v[t]);
     }
 }
 
@@ -444,7 +473,7 @@ __global__ __launch_bounds__(T::kThreads) void k_ns_gemm(NsBuffers w, NsShape sh
                     for (int e = 0; e < kRow; ++e)
                         if (MODE == kPoly) {
                             v[e] = st.b / kAScale * a8[e] + st.c / (kAScale * kAScale) * v[e];
-                            if (i == j + e) {
+                            if (ti == tj && i == j + e) {
                                 w.diag[z * sh.rp + i] = v[e];
                                 v[e] = 0.f;
                             }
@@ -652,17 +681,14 @@ struct Panel {
                 read_u<false>((const float*)g + base, b, mu, kind, move, xv);
         }
     }
-    // xv * 2^6 / (sqrt(sq) + eps): the scale as a power of two and a factor in
-    // [0.5, 1), as float32 alone would not hold every norm's reciprocal.
     __device__ __forceinline__ void normalise(double sq, double eps, float4v (&xv)[R][FN]) const {
-        int ex;
-        const float f = (float)frexp((double)kXScale / (sqrt(sq) + eps), &ex);
+        const NormScale scale(sq, eps);
 #pragma unroll
         for (int x = 0; x < R; ++x)
 #pragma unroll
             for (int y = 0; y < FN; ++y)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) xv[x][y][e] = ldexpf(xv[x][y][e], ex) * f;
+                for (int e = 0; e < 4; ++e) xv[x][y][e] = scale(xv[x][y][e]);
     }
     // 4 adjacent values of row i (i % 16 == l15) from column j on.
     __device__ __forceinline__ void put(_Float16* l, int width, int i, int j, float4v v) const {
@@ -747,11 +773,19 @@ struct Panel {
                         // both terms, which nearly cancel.
                         gb[x][y][e] = (float)(_Float16)ga[x][y][e] * (st.b / kAScale) +
                                       gb[x][y][e] * (st.c / (kAScale * kAScale));
-                        if (FA * wr + x == FB * wc + y && l15 == 4 * g4 + e) {
+                    }
+#pragma unroll
+            for (int x = 0; x < FA; ++x)
+#pragma unroll
+                for (int y = 0; y < FB; ++y) {
+                    if (FA * wr + x != FB * wc + y) continue;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (l15 == 4 * g4 + e) {
                             diag[16 * (FA * wr + x) + l15] = gb[x][y][e];
                             gb[x][y][e] = 0.f;
                         }
-                    }
+                }
         }
         __syncthreads();
         if (in_square()) put_square(gb);

@@ -233,6 +233,12 @@ def test_muon_on_wide_matrices(shape, pd, gd, momentum, nesterov):
                nesterov=nesterov, weight_decay=0.1, scale=1.5, steps=2)
 
 
+@pytest.mark.parametrize("shape", [(1, 1 << 20), ((1 << 20) - 3, 2), (130, 50001), (70000, 131)],
+                         ids=lambda s: f"{s[0]}x{s[1]}")
+def test_longest_sides(shape):
+    check_ns(matrix(*shape).to(BF16).cuda())
+
+
 def test_more_wide_matrices_than_one_grid_takes():
     batch, m, n = 4100, 64, 1025
     g = torch.empty(batch, m, n, dtype=BF16, device="cuda").normal_()
