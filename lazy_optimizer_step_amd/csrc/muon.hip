@@ -416,34 +416,72 @@ __global__ __launch_bounds__(T::kThreads) void k_ns_gemm(NsBuffers w, NsShape sh
     // Past the end the last step is brought again, so that every wait counts
     // the same loads; nothing reads it.
     auto at = [&](int k) { return (k < steps ? k : steps - 1) * kTile; };
-#pragma unroll
-    for (int k = 0; k < T::STAGES - 1; ++k) stage(k, at(k));
-    int buf = 0;
-    for (int k = 0; k < steps; ++k) {
-        // This stage's loads have landed in every wave, and every wave has read
-        // the stage before, whose place the next loads take.
-        wait_stage<(T::STAGES - 2) * kLoads>();
-        stage(buf == 0 ? T::STAGES - 1 : buf - 1, at(k + T::STAGES - 1));
+    half8 fa0[FM], fb0[FN], fa1[FM], fb1[FN];
+    // Half kk of a stage's operands into registers.
+    auto operands = [&](int buf, int kk, half8 (&fa)[FM], half8 (&fb)[FN]) {
         const _Float16* lp = lds + buf * T::kStage + (wi + (lane & 15)) * kTile;
         const _Float16* lq = lds + buf * T::kStage + BM * kTile;
+        const int ch = ((kk * 4 + (lane >> 4)) ^ (lane & 7)) * 8;
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            half8 fa[FM], fb[FN];
-            const int ch = ((kk * 4 + (lane >> 4)) ^ (lane & 7)) * 8;
-#pragma unroll
-            for (int x = 0; x < FM; ++x) fa[x] = *(const half8*)(lp + x * 16 * kTile + ch);
-#pragma unroll
-            for (int y = 0; y < FN; ++y)
-                fb[y] = kTurn ? turned(lq, kk, y)
+        for (int y = 0; y < FN; ++y)
+            fb[y] = kTurn ? turned(lq, kk, y)
                               : *(const half8*)(lq + (wj + y * 16 + (lane & 15)) * kTile + ch);
 #pragma unroll
-            for (int x = 0; x < FM; ++x)
+        for (int x = 0; x < FM; ++x) fa[x] = *(const half8*)(lp + x * 16 * kTile + ch);
+    };
+    auto multiply = [&](half8 (&fa)[FM], half8 (&fb)[FN]) {
 #pragma unroll
-                for (int y = 0; y < FN; ++y)
-                    acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[y], fa[x], acc[x][y], 0,
-                                                                       0, 0);
+        for (int x = 0; x < FM; ++x)
+#pragma unroll
+            for (int y = 0; y < FN; ++y)
+                acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[y], fa[x],
+                                                                   acc[x][y], 0, 0, 0);
+    };
+    int buf = 0;
+    if constexpr (BM < 192) {
+#pragma unroll
+        for (int k = 0; k < T::STAGES - 1; ++k) stage(k, at(k));
+        for (int k = 0; k < steps; ++k) {
+            // This stage's loads have landed in every wave, and every wave has
+            // read the stage before, whose place the next loads take.
+            wait_stage<(T::STAGES - 2) * kLoads>();
+            stage(buf == 0 ? T::STAGES - 1 : buf - 1, at(k + T::STAGES - 1));
+            operands(buf, 0, fa0, fb0);
+            multiply(fa0, fb0);
+            operands(buf, 1, fa1, fb1);
+            multiply(fa1, fb1);
+            buf = buf + 1 == T::STAGES ? 0 : buf + 1;
         }
-        buf = buf + 1 == T::STAGES ? 0 : buf + 1;
+    } else {
+        // Large tiles read each half's operands while the half before is
+        // multiplied, a read every few products: 4096 x 4096 1420 against 1457
+        // us.  Small ones lose by the longer start: 1024 x 512 by 16 267 to 257.
+        constexpr int kReads = FM + (kTurn ? 2 : 1) * FN, kPer = FM * FN / kReads;
+        auto weave = [&] {
+#pragma unroll
+            for (int g = 0; g < kReads; ++g) {
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);     // a read of LDS
+                __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);  // matrix instructions
+            }
+            __builtin_amdgcn_sched_group_barrier(0x008, FM * FN - kPer * kReads, 0);
+        };
+#pragma unroll
+        for (int k = 0; k < T::STAGES; ++k) stage(k, at(k));
+        wait_stage<(T::STAGES - 1) * kLoads>();
+        operands(0, 0, fa0, fb0);
+        for (int k = 0; k < steps; ++k) {
+            operands(buf, 1, fa1, fb1);
+            multiply(fa0, fb0);
+            weave();
+            // The next stage's loads have landed in every wave, and every wave
+            // has read this one, whose place the loads after them take.
+            wait_stage<(T::STAGES - 2) * kLoads>();
+            stage(buf, at(k + T::STAGES));
+            buf = buf + 1 == T::STAGES ? 0 : buf + 1;
+            operands(buf, 0, fa0, fb0);
+            multiply(fa1, fb1);
+            weave();
+        }
     }
     wait_loads<0>();
     // The tile's results, row by row and then, from the same registers, column
