@@ -308,8 +308,8 @@ __device__ __forceinline__ int64_t xcd_order(int64_t b, int64_t n) {
 // time, with no exchange between lanes.
 //
 // Measured at 4096 x 4096 (what the product alone is worth at the 1.1 PFLOP/s
-// that the library's float16 product of this size reaches): A 78 to 87 us and
-// A A 81 to 91 us in 253 tiles of 192 (62 us), B X 138 to 157 us in 256 tiles of
+// that the library's float16 product of this size reaches): A 73 to 81 us and
+// A A 77 to 85 us in 253 tiles of 192 (62 us), B X 132 to 147 us in 256 tiles of
 // 256 (125 us; the 10 bytes a value of its epilogue are another 33 us of HBM
 // time).  LDS reads meet no bank conflict; matrix instructions are issued 45%
 // of the time.
