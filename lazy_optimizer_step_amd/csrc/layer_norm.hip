@@ -199,7 +199,8 @@ __global__ __launch_bounds__(256) void k_ln_dx_any(const T* dy, int64_t ds, cons
 template <class T, class W, int V, int NV, int G>
 __global__ __launch_bounds__(G < 256 ? 256 : G) void k_ln_bwd(
     const T* dy, int64_t ds, const T* x, int64_t xs, int64_t rows, int cols, const float* mean,
-    const float* rstd, const W* w, T* dx, int64_t os, int64_t per, float* part) {
+    const float* rstd, const W* w, T* dx, int64_t os, int64_t per, float* part, W* dwo,
+    W* dbo) {
     constexpr int RPB = G < 256 ? 256 / G : 1;
     // 1024 threads have 128 registers each: no room for a row ahead.
     constexpr bool kAhead = G < 1024;
@@ -313,6 +314,16 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_ln_bwd(
     }
     if (part == nullptr) return;
     float* p = part + (int64_t)blockIdx.x * 2 * cols;
+    // A single slice's sums are the gradients.
+    auto put = [&](int col, float sw, float sb) {
+        if (gridDim.x > 1) {
+            p[col] = sw;
+            p[cols + col] = sb;
+            return;
+        }
+        if (dwo) dwo[col] = (W)sw;
+        if (dbo) dbo[col] = (W)sb;
+    };
     if constexpr (G < 256) {
         // Lane gl of every group holds the same columns: join the groups.
         __shared__ float jw[RPB][G * NV * V], jb[RPB][G * NV * V];
@@ -333,24 +344,20 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_ln_bwd(
                 sw += jw[q][i];
                 sb += jb[q][i];
             }
-            p[c.at + i % V] = sw;
-            p[cols + c.at + i % V] = sb;
+            put(c.at + i % V, sw, sb);
         }
     } else {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const Chunk<V> c(k * G + gl, cols);
-            if (c.skip == 0) {
+            if (c.skip == 0 && gridDim.x > 1) {
                 store_v<float, V>(p + c.at, dw[k]);
                 store_v<float, V>(p + cols + c.at, db[k]);
                 continue;
             }
 #pragma unroll
             for (int e = 0; e < V; ++e)
-                if (e >= c.skip) {
-                    p[c.at + e] = dw[k][e];
-                    p[cols + c.at + e] = db[k][e];
-                }
+                if (e >= c.skip) put(c.at + e, dw[k][e], db[k][e]);
         }
     }
 }
@@ -447,8 +454,15 @@ static RowPlan ln_plan(int64_t cols, int v, bool backward) {
 // slice's sums are as long as a row, 8 bytes a column against 6 or 12 that a
 // row reads and writes: 256 slices fill the card, more only while their sums
 // stay below an eighth of the rows' traffic (2048 x 16384 bfloat16, 512 slices:
-// half of it), 512 at most.
+// half of it), 512 at most.  Rows that one block is through with in four rounds
+// are one slice, whose sums need no second launch (4 x 1024: 3.5 us of kernels
+// for 6.4, 12 us for 16 on the host).
 static int64_t ln_slices(int64_t rows, int64_t cols, int64_t bytes, int64_t* per) {
+    const RowPlan p = ln_plan(cols, (int)(16 / bytes), true);
+    if (p.g != 0 && rows <= 4 * (p.g < 256 ? 256 / p.g : 1)) {
+        *per = rows < 1 ? 1 : rows;
+        return 1;
+    }
     int64_t s = cols <= 1024 ? ceil_div(rows, 16) : rows * 3 * bytes / 64;
     if (cols > 1024 && s < 256) s = 256;
     const int64_t most = cols <= 1024 ? 1024 : 512;
@@ -602,7 +616,7 @@ extern "C" int layer_norm_backward(const void* dy, int64_t dy_stride, const void
             k_ln_bwd<T, W, decltype(v)::value, decltype(nv)::value, G>
                 <<<(unsigned)slices, G < 256 ? 256 : G, 0, s>>>(
                     (const T*)dy, dy_stride, (const T*)x, x_stride, rows, (int)cols, mean, rstd,
-                    (const W*)weight, (T*)dx, dx_stride, per, part);
+                    (const W*)weight, (T*)dx, dx_stride, per, part, (W*)dweight, (W*)dbias);
         };
         auto at = [&](auto nv, auto g) { go(Int<V>{}, nv, g); };
         if (rows == 0 || (!sums && dx == nullptr)) {
@@ -630,7 +644,8 @@ extern "C" int layer_norm_backward(const void* dy, int64_t dy_stride, const void
                     (const T*)dy, dy_stride, (const T*)x, x_stride, rows, cols, mean, rstd,
                     (const W*)weight, (T*)dx, dx_stride);
         }
-        if (sums)
+        const bool direct = p.g != 0 && slices == 1;
+        if (sums && !direct)
             k_ln_join<W><<<dim3((unsigned)ceil_div(cols, 32), 2), 512, 0, s>>>(
                 part, slices, cols, (W*)dweight, (W*)dbias);
     });
