@@ -11,6 +11,9 @@ Pages followed (see the header for the full contract): the optirs_gpu
 sparse_optimizer module page (COO/CSR gradients, sparse SGD, Lazy and
 DormancyDecay Adam with global-step bias correction) and, where it is silent,
 the DiskSparseAdam README (duplicates summed and sorted, validated inputs).
+
+Beside the table's step: layer norm and Muon (dense.py, include/dense_ops.h),
+which no page covers.
 """
 from __future__ import annotations
 
