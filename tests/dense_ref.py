@@ -74,12 +74,13 @@ def ln_backward_bounds(dy, x, mu, rs, w, wdtype):
     return e_dx, e_dw + t, e_db + t
 
 
-def newton_schulz(g, steps=5, coef=(3.4445, -4.7750, 2.0315), eps=1e-7, rounded=False):
+def newton_schulz(g, steps=5, coef=(3.4445, -4.7750, 2.0315), eps=1e-7, rounded=False,
+                  on="cpu"):
     """The iteration in 64 bits; `rounded` puts in the kernels' roundings of the operands to
     float16 (X * 2^6, A * 2^12, B but for its diagonal) and nothing else."""
     def r16(t, s):
         return (t * s).half().double() / s if rounded else t
-    x = d(g)
+    x = g.detach().to(on).double()
     flip = x.shape[-2] > x.shape[-1]
     x = x.mT.contiguous() if flip else x
     x = x / (x.flatten(-2).norm(dim=-1)[..., None, None] + eps)

@@ -62,6 +62,17 @@ def test_large(shape):
     check_ns(matrix(*shape).to(BF16).cuda())
 
 
+@pytest.mark.parametrize("shape", [(2048, 2048), (4096, 4096), (4100, 4160), (5700, 5700),
+                                   (3, 2000, 2500)], ids=lambda s: "x".join(map(str, s)))
+def test_largest_tiles(shape):
+    """Sizes that take the 96, 192 and 256 tiles; the 64-bit iteration runs on the GPU."""
+    g = matrix(*shape).to(BF16).cuda()
+    out = L.newton_schulz(g)
+    ref, bound = R.ns_error_bound(g, on="cuda")
+    off = (out.double() - ref).flatten(-2).norm(dim=-1)
+    assert (off <= bound + R.HALF[BF16] * ref.flatten(-2).norm(dim=-1)).all()
+
+
 @pytest.mark.parametrize("steps,coefficients", [
     (1, (3.4445, -4.7750, 2.0315)), (10, (2.0, -1.5, 0.5)), (6, (1.5, -0.5, 0.0)),
     (2, (1.875, -1.25, 0.375)), (7, (3.4445, -4.7750, 2.0315))])
@@ -246,6 +257,29 @@ def test_more_wide_matrices_than_one_grid_takes():
     for at in (0, 4095, 4096, batch - 1):
         ref, bound = R.ns_error_bound(g[at])
         assert (R.d(out[at]) - ref).norm() <= bound + R.HALF[BF16] * ref.norm()
+
+
+@pytest.mark.parametrize("shape", [(128, 200), (100, 900), (1500, 1500), (2048, 2100), (4100, 4096),
+                                   (5, 700, 800)], ids=lambda s: "x".join(map(str, s)))
+def test_graph_of_every_form(shape):
+    """Captured steps replay the eager ones bit for bit, also with LDS beyond the default size."""
+    p0, grad = torch.randn(shape, device="cuda"), torch.randn(shape, device="cuda")
+    a, b = p0.clone(), p0.clone()
+    bufs = [torch.zeros(shape, device="cuda") for _ in range(2)]
+    ws = torch.empty(L.newton_schulz_workspace_size(shape[0] if len(shape) > 2 else 1,
+                                                    *shape[-2:]), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    g_in = torch.zeros_like(grad)
+    with torch.cuda.graph(graph):
+        L.muon_step(b, g_in, bufs[1], lr=0.1, workspace=ws)
+    for k in range(3):
+        g = torch.roll(grad, k, -1)
+        L.muon_step(a, g, bufs[0], lr=0.1)
+        g_in.copy_(g)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, b) and torch.equal(*bufs)
 
 
 def test_validate_refuses_and_writes_nothing():
