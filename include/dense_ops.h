@@ -78,13 +78,22 @@ SPOPT_API int layer_norm_backward(const void* dy, int64_t dy_stride, const void*
  * (X transposed where m > n, so that A is r x r).  Each step takes every
  * singular value s of X to coef[0] s + coef[1] s^3 + coef[2] s^5 and leaves
  * the singular vectors, so the result is near the orthogonal factor of U.
- * The products are taken in float16 with float32 sums, on matrix cores: X with
- * 2^6 and A with 2^12 in front, which keeps them inside float16's range.  X
- * itself is carried from step to step in float32, as is the diagonal of
- * coef[1] A + coef[2] A A.  The result is within about 1.5e-3 (norm) of the
- * iteration's in 64 bits, before its rounding to bfloat16.  The
- * scaling holds for singular values up to 2 and |coef[1] s^2 + coef[2] s^4| up
- * to 8; coefficients that leave these bounds in any of the steps are refused
+ * The products are taken in float16 with float32 sums, on matrix cores, for
+ * float32 gradients too: X with 2^6 and A with 2^12 in front, which keeps them
+ * inside float16's range.  X itself is carried from step to step in float32, as
+ * is the diagonal of coef[1] A + coef[2] A A.
+ * Accuracy, as the norm of the difference from the iteration in 64 bits over
+ * the result's norm, before the rounding to bfloat16, for 5 steps of 3.4445,
+ * -4.7750, 2.0315: below 4e-3 where U's shorter side is 8 or more and its
+ * values are unlike (Gaussian, of low rank, with few rows that are not zero:
+ * 3e-4 to 2.5e-3), below 1e-2 for any U (the largest: 2 or 3 rows, constant
+ * matrices).  Directions that U lacks hold what rounding puts there, times
+ * coef[0] for each later step: for U of low rank the result is within 5e-3 by 8
+ * steps, off by up to 2e-2 by 10, and by as much as its own norm from 14 on; of
+ * full rank by up to 2e-2 by 16 and 4e-2 by 64.  Coefficients that converge
+ * (coef[0] of 2 and less) leave it within 3e-3 of any of these by 16 steps.
+ * The scaling holds for singular values up to 2 and |coef[1] s^2 + coef[2] s^4|
+ * up to 8; coefficients that leave these bounds in any of the steps are refused
  * (on the host, from the largest value that [0, 1] reaches).
  *   steps in [1, 64], coef finite, eps finite and > 0. */
 typedef struct spopt_ns_config {

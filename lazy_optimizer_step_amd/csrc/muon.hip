@@ -15,13 +15,24 @@
 // (entries are bounded by the largest singular value, which the host checks).
 // X is also carried in float32, for the a X term: in the directions of small
 // singular values B is near zero, so that rounding errors of X come in through
-// a X alone there, and grow by a factor of a in every step.  B's diagonal joins
-// that term, in float32 too: as X's rows become orthonormal it nears b + c
-// while the rest of B vanishes, and float16 would round it to 5e-4.  Errors
-// against 64 bits, relative to the result's norm, for 64 to 1024 rows and
-// Gaussian, low-rank and decaying spectra: at most 1.3e-3; 2.6e-3 with the
-// diagonal in float16, 7e-3 with X in float16 alone, 6e-2 with all of it in
-// bfloat16.
+// a X alone there, and grow by a factor of a in every step.  B's diagonal keeps
+// float32's digits: as X's rows become orthonormal it nears b + c while the
+// rest of B vanishes, and float16 alone would round it to 5e-4.
+//
+// Which X the diagonal meets.  With E the rounding of X to float16, B (X + E)
+// is off by B E, which lies in B's range, that is in directions that X has.
+// The diagonal times X in float32 in place of X + E takes diag E out of that:
+// what is left is smaller where B is nearly diagonal, but of a matrix of low
+// rank or with few rows that are not zero it lies in directions that X lacks,
+// and each later step multiplies it by a.  So while steps follow that would,
+// the diagonal's float16 part stays in the product and its remainder joins
+// a X; in the last two steps (and of a single row, which lacks no direction)
+// all of it joins a X.  Errors against 64 bits, relative to the result's norm,
+// by 5 steps in an emulation of these roundings: rank 1 of 64 x 64 7e-4, 4 rows
+// of 512 that are not zero 1.6e-3, Gaussian 128 x 128 1.2e-3.  With all of the
+// diagonal beside a X throughout 9e-3, 3.8e-2 and 1.0e-3, only its remainder
+// throughout 7e-4, 1.7e-3 and 1.5e-3.  The largest met are of matrices with 2
+// or 3 rows (6e-3) and of constant ones, whose values all round alike (5e-3).
 #include <math.h>
 
 #include <type_traits>
@@ -117,8 +128,8 @@ struct NsBuffers {
     _Float16* x[2];  // [batch][rp * cp]   X * 2^6, one step's and the next's
     float* x32;      // [batch][rp * cp]   X * 2^6
     _Float16* a16;   // [batch][rp * rp]   A * 2^12
-    _Float16* b16;   // [batch][rp * rp]   B but for its diagonal
-    float* diag;     // [batch][rp]        B's diagonal
+    _Float16* b16;   // [batch][rp * rp]   B, its diagonal as ns_split says
+    float* diag;     // [batch][rp]        B's diagonal but for what b16 holds of it
     double* part;    // [batch][kNormParts]
 };
 
@@ -201,8 +212,14 @@ __global__ __launch_bounds__(256) void k_ns_init(Source<G> u, NsBuffers w, NsSha
 
 enum : int { kGram = 0, kPoly = 1, kNext = 2, kOut = 3, kParam32 = 4, kParam16 = 5 };
 
+// Whether it does, `left` steps before the last, for X of `rows` rows.
+__host__ __device__ __forceinline__ int ns_split(int left, int rows) {
+    return left >= 2 && rows > 1;
+}
+
 struct NsStep {
     float a, b, c;
+    int split;       // whether the product holds the float16 part of B's diagonal
     void* out;       // kOut: bfloat16; kParam*: the weight
     float keep, move;  // kParam*: p <- keep * p - move * X
 };
@@ -512,8 +529,9 @@ __global__ __launch_bounds__(T::kThreads) void k_ns_gemm(NsBuffers w, NsShape sh
                         if (MODE == kPoly) {
                             v[e] = st.b / kAScale * a8[e] + st.c / (kAScale * kAScale) * v[e];
                             if (ti == tj && i == j + e) {
-                                w.diag[z * sh.rp + i] = v[e];
-                                v[e] = 0.f;
+                                const float in = st.split ? (float)(_Float16)v[e] : 0.f;
+                                w.diag[z * sh.rp + i] = v[e] - in;
+                                v[e] = in;
                             }
                         }
                     store_v<_Float16, kRow>((MODE == kGram ? w.a16 : w.b16) + o, v);
@@ -605,7 +623,7 @@ struct Panel {
     // Of 16 waves' square parts the 6 above the diagonal are mirrored ones.
     static constexpr bool kMirror = W == 16;
     _Float16 *lx, *la;
-    float* diag;          // B's diagonal
+    float* diag;          // B's diagonal but for what `la` holds of it
     int lane, l15, g4, ft, wj, wr, wc;
     uint32_t di, dj;      // strides of X's rows and columns in the input
     int rows, cols;       // of the input's, from this panel's first column on
@@ -796,8 +814,10 @@ struct Panel {
             }
         }
     }
-    // From A * 2^12 in `ga` and, as float16, in LDS: B into LDS.
-    __device__ __forceinline__ void polynomial(const float4v (&ga)[FA][FB], const NsStep& st) const {
+    // From A * 2^12 in `ga` and, as float16, in LDS: B into LDS, its diagonal as
+    // `split` (ns_split) says.
+    __device__ __forceinline__ void polynomial(const float4v (&ga)[FA][FB], const NsStep& st,
+                                               bool split) const {
         float4v gb[FA][FB] = {};
         if (in_square()) {
             square(la, kA, R / 2, gb);
@@ -820,8 +840,9 @@ struct Panel {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (l15 == 4 * g4 + e) {
-                            diag[16 * (FA * wr + x) + l15] = gb[x][y][e];
-                            gb[x][y][e] = 0.f;
+                            const float in = split ? (float)(_Float16)gb[x][y][e] : 0.f;
+                            diag[16 * (FA * wr + x) + l15] = gb[x][y][e] - in;
+                            gb[x][y][e] = in;
                         }
                 }
         }
@@ -829,7 +850,7 @@ struct Panel {
         if (in_square()) put_square(gb);
         __syncthreads();
     }
-    // X <- a X + B X: the accumulators start at a X.
+    // X <- a X + B X: the accumulators start at a X and `diag` X.
     __device__ __forceinline__ void next(float a, float4v (&xv)[R][FN]) const {
 #pragma unroll
         for (int x = 0; x < R; ++x) {
@@ -955,7 +976,7 @@ __global__ __launch_bounds__(64 * W) void k_ns_small(PanelRun u, NsShape sh, NsS
             p.put_square(ga);
         }
         __syncthreads();
-        p.polynomial(ga, st);
+        p.polynomial(ga, st, ns_split(u.steps - 1 - k, sh.r));
         p.next(st.a, xv);
     }
     p.write(u.mode, base, st, xv);
@@ -963,13 +984,13 @@ __global__ __launch_bounds__(64 * W) void k_ns_small(PanelRun u, NsShape sh, NsS
 
 // A wide matrix, panel by panel, one block each.  STEP false: U becomes X0.
 // STEP true: with A, which every block turns into B for itself (128^3 products:
-// about a microsecond), X becomes the next X, and after the last step the
+// about a microsecond), X becomes the next X, and with no step left the
 // result.  Either leaves the panel's share of the next A.  Latency bounds both:
 // 8 us a step for 8 panels (1001 x 128) or 32 (4096 x 128); in tiled products A's
 // long sum ran in three blocks and the same matrices took 80 and 139 us in all,
 // against 56 and 64.
 template <int R, int FN, bool STEP>
-__global__ __launch_bounds__(512) void k_ns_panel(PanelRun u, NsShape sh, NsStep st, int last) {
+__global__ __launch_bounds__(512) void k_ns_panel(PanelRun u, NsShape sh, NsStep st, int left) {
     extern __shared__ __align__(16) char lds_raw[];
     typedef Panel<R, FN, 8> P;
     const int z = blockIdx.x / u.panels, panel = blockIdx.x % u.panels;
@@ -1001,9 +1022,9 @@ __global__ __launch_bounds__(512) void k_ns_panel(PanelRun u, NsShape sh, NsStep
         p.put_square(ga);
         p.put_x(xv);
         __syncthreads();
-        p.polynomial(ga, st);
+        p.polynomial(ga, st, ns_split(left, sh.r));
         p.next(st.a, xv);
-        if (last) {
+        if (left == 0) {
             p.write(u.mode, base, st, xv);
             return;
         }
@@ -1299,7 +1320,7 @@ static int ns_panels(PanelRun r, Source<G> u, const NsShape& sh, const NsStep& s
         k_ns_panel<R, FN, false><<<grid, 512, bytes, s>>>(v, sh, sz, 0);
         for (int k = 0; k < r.steps; ++k) {
             k_ns_panel_sum<<<nb * (quads / 64), 256, 0, s>>>(v, quads);
-            k_ns_panel<R, FN, true><<<grid, 512, bytes, s>>>(v, sh, sz, k + 1 == r.steps);
+            k_ns_panel<R, FN, true><<<grid, 512, bytes, s>>>(v, sh, sz, r.steps - 1 - k);
         }
         SPOPT_LAUNCHED();
     }
@@ -1357,6 +1378,7 @@ static int ns_run(const NsShape& sh, Source<G> u, float* buf, const spopt_ns_con
         SPOPT_LAUNCHED();
         for (int k = 0; k < c.steps; ++k) {
             const int from = k & 1;
+            sz.split = ns_split(c.steps - 1 - k, sh.r);
             int rc = ns_product<kGram>(v, sh, sz, from, nb, s);
             if (!rc) rc = ns_product<kPoly>(v, sh, sz, from, nb, s);
             if (!rc)
