@@ -1261,7 +1261,8 @@ static int ns_small_launch(const PanelRun& u, const NsShape& sh, const NsStep& s
         SPOPT_HIP(hipFuncSetAttribute((const void*)k_ns_small<R, FN, W>,
                                       hipFuncAttributeMaxDynamicSharedMemorySize, bytes));
     }
-    const int64_t chunk = 1 << 22;  // blocks of a grid
+    // Blocks of a grid: HIP takes fewer than 2^32 threads along an axis.
+    constexpr int64_t chunk = ((int64_t)1 << 30) / (64 * W);
     for (int64_t z = 0; z < sh.batch; z += chunk) {
         const int64_t nb = sh.batch - z < chunk ? sh.batch - z : chunk, at = z * sh.m * sh.n;
         PanelRun v = u;
@@ -1270,8 +1271,8 @@ static int ns_small_launch(const PanelRun& u, const NsShape& sh, const NsStep& s
         if (u.buf) v.buf += at;
         sz.out = (char*)st.out + at * (u.mode == kParam32 ? 4 : 2);
         k_ns_small<R, FN, W><<<(unsigned)nb, 64 * W, bytes, s>>>(v, sh, sz);
+        SPOPT_LAUNCHED();
     }
-    SPOPT_LAUNCHED();
     return SPOPT_OK;
 }
 
