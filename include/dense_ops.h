@@ -41,7 +41,7 @@ extern "C" {
  * an infinity gives NaN in that row alone; so may one whose centred squares
  * sum to more than float32 holds (values of about 1e18 and more).
  * Errors: SPOPT_EINVAL (NULL x or y with rows > 0, rows < 0, cols < 1, a stride
- * below cols, unknown or mismatched types, eps not finite and > 0). */
+ * below cols, unknown or mismatched types, eps not finite and > 0 as a float). */
 SPOPT_API int layer_norm_forward(const void* x, int64_t x_stride, int64_t rows, int64_t cols,
                                  int32_t dtype, const void* weight, const void* bias,
                                  int32_t wdtype, double eps, void* y, int64_t y_stride,

@@ -516,8 +516,9 @@ extern "C" int layer_norm_forward(const void* x, int64_t x_stride, int64_t rows,
     hipStream_t s = (hipStream_t)stream;
     int rc = ln_check("layer_norm_forward", rows, cols, dtype, wdtype);
     if (rc) return rc;
-    if (!(eps > 0.0) || !isfinite(eps))
-        return fail(SPOPT_EINVAL, "layer_norm_forward: eps must be finite and > 0");
+    // The kernels add it in float32: one that becomes 0 there would divide a constant row by 0.
+    if (!((float)eps > 0.f) || !isfinite((float)eps))
+        return fail(SPOPT_EINVAL, "layer_norm_forward: eps must be finite and > 0 in float32");
     if (rows == 0) return SPOPT_OK;
     if (x == nullptr || y == nullptr) return fail(SPOPT_EINVAL, "layer_norm_forward: NULL x or y");
     if (bad_stride(x_stride, rows, cols) || bad_stride(y_stride, rows, cols))
