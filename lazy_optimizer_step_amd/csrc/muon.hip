@@ -46,7 +46,8 @@ typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef float float4v __attribute__((ext_vector_type(4)));
 
 constexpr int kTile = 64;                    // rows, columns and inner axis are padded to it
-constexpr float kXScale = 64.f;              // 2^6
+constexpr int kXExp = 6;
+constexpr float kXScale = 1 << kXExp;
 constexpr float kAScale = kXScale * kXScale; // 2^12
 constexpr int kNormParts = 1024;             // partial sums of a matrix's norm, at most
 
@@ -114,12 +115,14 @@ __global__ __launch_bounds__(256) void k_ns_norm(Source<G> u, float* buf, int64_
 }
 
 // x * 2^6 / (norm + eps) for the norm's square: the scale as a power of two and
-// a factor in [0.5, 1), as float32 alone would not hold every norm's reciprocal.
+// a factor in (1, 2], as float32 alone would not hold every norm's reciprocal,
+// nor float64 that of the smallest eps.
 struct NormScale {
     int ex;
     float f;
     __device__ __forceinline__ NormScale(double sq, double eps) {
-        f = (float)frexp((double)kXScale / (sqrt(sq) + eps), &ex);
+        f = (float)(1.0 / frexp(sqrt(sq) + eps, &ex));
+        ex = kXExp - ex;
     }
     __device__ __forceinline__ float operator()(float x) const { return ldexpf(x, ex) * f; }
 };
