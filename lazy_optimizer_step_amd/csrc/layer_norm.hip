@@ -371,22 +371,25 @@ __global__ __launch_bounds__(256) void k_ln_cols_any(const T* dy, int64_t ds, co
                                                      int64_t per, float* part) {
     __shared__ float lw[4][64], lb[4][64];
     const int lane = lane_id(), k = threadIdx.x >> 6;
-    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
     const int64_t r0 = blockIdx.y * per, r1 = r0 + per < rows ? r0 + per : rows;
-    float sw = 0.f, sb = 0.f;
-    if (c < cols)
-        for (int64_t r = r0 + k; r < r1; r += 4) {
-            const float g = (float)dy[r * ds + c];
-            sw += g * (((float)x[r * xs + c] - mean[r]) * rstd[r]);
-            sb += g;
+    for (int64_t c0 = (int64_t)blockIdx.x * 64; c0 < cols; c0 += (int64_t)gridDim.x * 64) {
+        const int64_t c = c0 + lane;
+        float sw = 0.f, sb = 0.f;
+        if (c < cols)
+            for (int64_t r = r0 + k; r < r1; r += 4) {
+                const float g = (float)dy[r * ds + c];
+                sw += g * (((float)x[r * xs + c] - mean[r]) * rstd[r]);
+                sb += g;
+            }
+        lw[k][lane] = sw;
+        lb[k][lane] = sb;
+        __syncthreads();
+        if (k == 0 && c < cols) {
+            float* p = part + (int64_t)blockIdx.y * 2 * cols + c;
+            p[0] = (lw[0][lane] + lw[1][lane]) + (lw[2][lane] + lw[3][lane]);
+            p[cols] = (lb[0][lane] + lb[1][lane]) + (lb[2][lane] + lb[3][lane]);
         }
-    lw[k][lane] = sw;
-    lb[k][lane] = sb;
-    __syncthreads();
-    if (k == 0 && c < cols) {
-        float* p = part + (int64_t)blockIdx.y * 2 * cols + c;
-        p[0] = (lw[0][lane] + lw[1][lane]) + (lw[2][lane] + lw[3][lane]);
-        p[cols] = (lb[0][lane] + lb[1][lane]) + (lb[2][lane] + lb[3][lane]);
+        __syncthreads();  // lw and lb have been read
     }
 }
 
@@ -399,29 +402,33 @@ __global__ __launch_bounds__(512) void k_ln_join(const float* part, int64_t slic
                                                  W* dw, W* db) {
     __shared__ double l[16][33];
     const int q = threadIdx.x & 31, k = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + q;
     W* out = blockIdx.y ? db : dw;
     if (out == nullptr) return;
-    double s = 0.;
-    if (c < cols) {
-        const float* p = part + blockIdx.y * cols + c;
-        int64_t i = k;
-        for (; i + 112 < slices; i += 128) {  // eight loads at once
-            float v[8];
+    for (int64_t c0 = (int64_t)blockIdx.x * 32; c0 < cols; c0 += (int64_t)gridDim.x * 32) {
+        const int64_t c = c0 + q;
+        double s = 0.;
+        if (c < cols) {
+            const float* p = part + blockIdx.y * cols + c;
+            int64_t i = k;
+            for (; i + 112 < slices; i += 128) {  // eight loads at once
+                float v[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = p[(i + 16 * e) * 2 * cols];
+                for (int e = 0; e < 8; ++e) v[e] = p[(i + 16 * e) * 2 * cols];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s += (double)v[e];
+                for (int e = 0; e < 8; ++e) s += (double)v[e];
+            }
+            for (; i < slices; i += 16) s += (double)p[i * 2 * cols];
         }
-        for (; i < slices; i += 16) s += (double)p[i * 2 * cols];
-    }
-    l[k][q] = s;
-    __syncthreads();
-    if (k != 0 || c >= cols) return;
-    s = 0.;
+        l[k][q] = s;
+        __syncthreads();
+        if (k == 0 && c < cols) {
+            s = 0.;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) s += l[e][q];
-    out[c] = (W)(float)s;
+            for (int e = 0; e < 16; ++e) s += l[e][q];
+            out[c] = (W)(float)s;
+        }
+        __syncthreads();  // l has been read
+    }
 }
 
 // How a row is shared out: G lanes of NV chunks of V values hold it.
@@ -502,6 +509,12 @@ static void ln_types(int32_t dtype, int32_t wdtype, F&& f) {
 
 template <int N>
 using Int = std::integral_constant<int, N>;
+
+// Blocks along the columns: HIP takes fewer than 2^32 threads along an axis.
+static unsigned col_grid(int64_t cols, int per) {
+    const int64_t n = ceil_div(cols, per);
+    return (unsigned)(n < (1 << 20) ? n : 1 << 20);
+}
 
 static unsigned row_grid(int64_t rows) { return (unsigned)(rows < 65536 ? rows : 65536); }
 
@@ -637,7 +650,7 @@ extern "C" int layer_norm_backward(const void* dy, int64_t dy_stride, const void
         } else {
             // Wider rows: the column sums first, as dx may lie over dy or x.
             if (sums)
-                k_ln_cols_any<T><<<dim3((unsigned)ceil_div(cols, 64), (unsigned)slices), 256, 0,
+                k_ln_cols_any<T><<<dim3(col_grid(cols, 64), (unsigned)slices), 256, 0,
                                    s>>>((const T*)dy, dy_stride, (const T*)x, x_stride, rows, cols,
                                         mean, rstd, per, part);
             if (dx != nullptr)
@@ -647,7 +660,7 @@ extern "C" int layer_norm_backward(const void* dy, int64_t dy_stride, const void
         }
         const bool direct = p.g != 0 && slices == 1;
         if (sums && !direct)
-            k_ln_join<W><<<dim3((unsigned)ceil_div(cols, 32), 2), 512, 0, s>>>(
+            k_ln_join<W><<<dim3(col_grid(cols, 32), 2), 512, 0, s>>>(
                 part, slices, cols, (W*)dweight, (W*)dbias);
     });
     SPOPT_LAUNCHED();
