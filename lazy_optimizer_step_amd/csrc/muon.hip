@@ -242,7 +242,9 @@ __device__ __forceinline__ void wait_stage() {
 // (the same for the whole wave).  In assembly, as the compiler would wait for
 // every load that writes LDS before each transposing read of it, also of
 // another stage; wait_stage counts them instead.  No register is written but
-// m0, which the compiler never keeps a value in.
+// m0: reserved, so that the compiler allocates nothing to it (and warns where it
+// is listed as clobbered), and no instruction that it makes of this file reads
+// it.
 __device__ __forceinline__ void load_lds16(const _Float16* from, _Float16* to) {
     const uint32_t m0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)to;
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from),
