@@ -160,7 +160,7 @@ __global__ __launch_bounds__(256) void k_ln_fwd_any(const T* x, int64_t xs, int6
 }
 
 // dx of one row per block, any width: two passes over the row, the second mostly
-// from cache.  2000 x 20000 bfloat16: 119 us, and 54 us for the column sums.
+// from cache.  2000 x 20000 bfloat16: 77 us, and 56 us for the column sums.
 template <class T, class W>
 __global__ __launch_bounds__(256) void k_ln_dx_any(const T* dy, int64_t ds, const T* x,
                                                    int64_t xs, int64_t rows, int64_t cols,
@@ -194,8 +194,11 @@ __global__ __launch_bounds__(256) void k_ln_dx_any(const T* dy, int64_t ds, cons
 // part[slice][2][cols].  One pass: dx and the column sums from separate kernels
 // read dy and x twice (119 us against 22 at 65536 x 128, 290 against 86 at
 // 16384 x 4096).  Measured: 65536 x 128 float32 17.3 us (5.8 TB/s with what the
-// last-level cache holds), 16384 x 4096 bfloat16 81 us (5.0 TB/s), 777 x 5003
-// 14 us (195 blocks of 4 rows: the latency of each row's loads).
+// last-level cache holds), 16384 x 4096 bfloat16 82 us (4.9 TB/s), 777 x 5003
+// 14 us (195 blocks of 4 rows: the latency of each row's loads).  From 8193
+// columns on (G = 1024) a row with its two sums a column is more than 128
+// registers hold: 29 to 57 of a lane go to scratch and back; 2048 x 16384
+// bfloat16 65 us and 7 for the join, for 39 at the copy's rate.
 template <class T, class W, int V, int NV, int G>
 __global__ __launch_bounds__(G < 256 ? 256 : G) void k_ln_bwd(
     const T* dy, int64_t ds, const T* x, int64_t xs, int64_t rows, int cols, const float* mean,
@@ -362,73 +365,67 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_ln_bwd(
     }
 }
 
-// Sums of dy * xhat and dy over one slice of rows (blockIdx.y) for 64 columns:
-// four rows at a time, joined in LDS.  part: [slices][2][cols].
+// Sums of dy * xhat and dy over one slice of rows (blockIdx.y) for 64 columns
+// from c0 on: four rows at a time, joined in LDS.  part: [slices][2][cols].
 template <class T>
 __global__ __launch_bounds__(256) void k_ln_cols_any(const T* dy, int64_t ds, const T* x,
                                                      int64_t xs, int64_t rows, int64_t cols,
                                                      const float* mean, const float* rstd,
-                                                     int64_t per, float* part) {
+                                                     int64_t per, float* part, int64_t c0) {
     __shared__ float lw[4][64], lb[4][64];
     const int lane = lane_id(), k = threadIdx.x >> 6;
+    const int64_t c = c0 + (int64_t)blockIdx.x * 64 + lane;
     const int64_t r0 = blockIdx.y * per, r1 = r0 + per < rows ? r0 + per : rows;
-    for (int64_t c0 = (int64_t)blockIdx.x * 64; c0 < cols; c0 += (int64_t)gridDim.x * 64) {
-        const int64_t c = c0 + lane;
-        float sw = 0.f, sb = 0.f;
-        if (c < cols)
-            for (int64_t r = r0 + k; r < r1; r += 4) {
-                const float g = (float)dy[r * ds + c];
-                sw += g * (((float)x[r * xs + c] - mean[r]) * rstd[r]);
-                sb += g;
-            }
-        lw[k][lane] = sw;
-        lb[k][lane] = sb;
-        __syncthreads();
-        if (k == 0 && c < cols) {
-            float* p = part + (int64_t)blockIdx.y * 2 * cols + c;
-            p[0] = (lw[0][lane] + lw[1][lane]) + (lw[2][lane] + lw[3][lane]);
-            p[cols] = (lb[0][lane] + lb[1][lane]) + (lb[2][lane] + lb[3][lane]);
+    float sw = 0.f, sb = 0.f;
+    if (c < cols)
+        for (int64_t r = r0 + k; r < r1; r += 4) {
+            const float g = (float)dy[r * ds + c];
+            sw += g * (((float)x[r * xs + c] - mean[r]) * rstd[r]);
+            sb += g;
         }
-        __syncthreads();  // lw and lb have been read
+    lw[k][lane] = sw;
+    lb[k][lane] = sb;
+    __syncthreads();
+    if (k == 0 && c < cols) {
+        float* p = part + (int64_t)blockIdx.y * 2 * cols + c;
+        p[0] = (lw[0][lane] + lw[1][lane]) + (lw[2][lane] + lw[3][lane]);
+        p[cols] = (lb[0][lane] + lb[1][lane]) + (lb[2][lane] + lb[3][lane]);
     }
 }
 
 // dweight and dbias from the slices' sums: a block takes 32 columns of one of
 // the two, 16 threads on each column's slices, joined in double in a fixed
-// order.  Latency bounds it: 4 to 7 us at every size met, with eight loads in
-// flight (23 us for 512 slices of 16384 columns with one).
+// order.  Latency bounds it: 4 to 7 us up to 256 slices of 16384 columns, 12 us
+// for 250 of 20000, with eight loads in flight (23 us for 512 slices of 16384
+// columns with one).
 template <class W>
 __global__ __launch_bounds__(512) void k_ln_join(const float* part, int64_t slices, int64_t cols,
-                                                 W* dw, W* db) {
+                                                 W* dw, W* db, int64_t c0) {
     __shared__ double l[16][33];
     const int q = threadIdx.x & 31, k = threadIdx.x >> 5;
+    const int64_t c = c0 + (int64_t)blockIdx.x * 32 + q;
     W* out = blockIdx.y ? db : dw;
     if (out == nullptr) return;
-    for (int64_t c0 = (int64_t)blockIdx.x * 32; c0 < cols; c0 += (int64_t)gridDim.x * 32) {
-        const int64_t c = c0 + q;
-        double s = 0.;
-        if (c < cols) {
-            const float* p = part + blockIdx.y * cols + c;
-            int64_t i = k;
-            for (; i + 112 < slices; i += 128) {  // eight loads at once
-                float v[8];
+    double s = 0.;
+    if (c < cols) {
+        const float* p = part + blockIdx.y * cols + c;
+        int64_t i = k;
+        for (; i + 112 < slices; i += 128) {  // eight loads at once
+            float v[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = p[(i + 16 * e) * 2 * cols];
+            for (int e = 0; e < 8; ++e) v[e] = p[(i + 16 * e) * 2 * cols];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s += (double)v[e];
-            }
-            for (; i < slices; i += 16) s += (double)p[i * 2 * cols];
+            for (int e = 0; e < 8; ++e) s += (double)v[e];
         }
-        l[k][q] = s;
-        __syncthreads();
-        if (k == 0 && c < cols) {
-            s = 0.;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) s += l[e][q];
-            out[c] = (W)(float)s;
-        }
-        __syncthreads();  // l has been read
+        for (; i < slices; i += 16) s += (double)p[i * 2 * cols];
     }
+    l[k][q] = s;
+    __syncthreads();
+    if (k != 0 || c >= cols) return;
+    s = 0.;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s += l[e][q];
+    out[c] = (W)(float)s;
 }
 
 // How a row is shared out: G lanes of NV chunks of V values hold it.
@@ -510,10 +507,14 @@ static void ln_types(int32_t dtype, int32_t wdtype, F&& f) {
 template <int N>
 using Int = std::integral_constant<int, N>;
 
-// Blocks along the columns: HIP takes fewer than 2^32 threads along an axis.
-static unsigned col_grid(int64_t cols, int per) {
-    const int64_t n = ceil_div(cols, per);
-    return (unsigned)(n < (1 << 20) ? n : 1 << 20);
+// Calls launch(c0, blocks) for ranges of the columns, `per` a block: HIP takes
+// fewer than 2^32 threads along an axis.  (Further columns in turn by each block
+// instead made k_ln_cols_any 62 us for 56 at 2000 x 20000.)
+template <class F>
+static void by_columns(int64_t cols, int per, F&& launch) {
+    const int64_t range = (int64_t)per << 20;
+    for (int64_t c0 = 0; c0 < cols; c0 += range)
+        launch(c0, (unsigned)ceil_div(cols - c0 < range ? cols - c0 : range, per));
 }
 
 static unsigned row_grid(int64_t rows) { return (unsigned)(rows < 65536 ? rows : 65536); }
@@ -650,9 +651,11 @@ extern "C" int layer_norm_backward(const void* dy, int64_t dy_stride, const void
         } else {
             // Wider rows: the column sums first, as dx may lie over dy or x.
             if (sums)
-                k_ln_cols_any<T><<<dim3(col_grid(cols, 64), (unsigned)slices), 256, 0,
-                                   s>>>((const T*)dy, dy_stride, (const T*)x, x_stride, rows, cols,
-                                        mean, rstd, per, part);
+                by_columns(cols, 64, [&](int64_t c0, unsigned blocks) {
+                    k_ln_cols_any<T><<<dim3(blocks, (unsigned)slices), 256, 0, s>>>(
+                        (const T*)dy, dy_stride, (const T*)x, x_stride, rows, cols, mean, rstd,
+                        per, part, c0);
+                });
             if (dx != nullptr)
                 k_ln_dx_any<T, W><<<row_grid(rows), 256, 0, s>>>(
                     (const T*)dy, dy_stride, (const T*)x, x_stride, rows, cols, mean, rstd,
@@ -660,8 +663,10 @@ extern "C" int layer_norm_backward(const void* dy, int64_t dy_stride, const void
         }
         const bool direct = p.g != 0 && slices == 1;
         if (sums && !direct)
-            k_ln_join<W><<<dim3(col_grid(cols, 32), 2), 512, 0, s>>>(
-                part, slices, cols, (W*)dweight, (W*)dbias);
+            by_columns(cols, 32, [&](int64_t c0, unsigned blocks) {
+                k_ln_join<W><<<dim3(blocks, 2), 512, 0, s>>>(part, slices, cols, (W*)dweight,
+                                                             (W*)dbias, c0);
+            });
     });
     SPOPT_LAUNCHED();
     return SPOPT_OK;
