@@ -60,7 +60,8 @@ SPOPT_API int layer_norm_backward_workspace_size(int64_t rows, int64_t cols, siz
  *   weight      [cols] of `wdtype` or NULL.
  *   dweight, dbias  [cols] of `wdtype`, either may be NULL.  Written, not added
  *               to; all zero for rows == 0.
- * The sums over rows are formed in 32 bits in a fixed order and joined in 64.
+ * The sums over rows are formed in 32 bits in a fixed order, over slices of the
+ * rows where they are many, which are joined in 64.
  * Workspace: device, 16-byte aligned, layer_norm_backward_workspace_size bytes.
  * Errors: as layer_norm_forward, and SPOPT_EWORKSPACE. */
 SPOPT_API int layer_norm_backward(const void* dy, int64_t dy_stride, const void* x,

@@ -330,11 +330,13 @@ __device__ __forceinline__ int64_t xcd_order(int64_t b, int64_t n) {
 // time, with no exchange between lanes.
 //
 // Measured at 4096 x 4096 (what the product alone is worth at the 1.1 PFLOP/s
-// that the library's float16 product of this size reaches): A 73 to 81 us and
-// A A 77 to 85 us in 253 tiles of 192 (62 us), B X 132 to 147 us in 256 tiles of
+// that the library's float16 product of this size reaches): A 72 to 81 us and
+// A A 75 to 85 us in 253 tiles of 192 (62 us), B X 131 to 147 us in 256 tiles of
 // 256 (125 us; the 10 bytes a value of its epilogue are another 33 us of HBM
 // time).  LDS reads meet no bank conflict; matrix instructions are issued 45%
-// of the time.
+// of the time.  The 256 tile's accumulators leave its epilogues short of
+// registers: 45 of a lane go to scratch and back in kPoly, 10 to 16 in the last
+// step's forms, none in kNext.
 template <int MODE, class T>
 __global__ __launch_bounds__(T::kThreads) void k_ns_gemm(NsBuffers w, NsShape sh, NsStep st,
                                                          int from, int tiles) {
@@ -477,7 +479,7 @@ __global__ __launch_bounds__(T::kThreads) void k_ns_gemm(NsBuffers w, NsShape sh
     } else {
         // Large tiles read each half's operands while the half before is
         // multiplied, a read every few products: 4096 x 4096 1420 against 1457
-        // us.  Small ones lose by the longer start: 1024 x 512 by 16 267 to 257.
+        // us, timed in turn.  Small ones lose by the longer start: 1024 x 512 by 16 267 to 257.
         constexpr int kReads = FM + (kTurn ? 2 : 1) * FN, kPer = FM * FN / kReads;
         auto weave = [&] {
 #pragma unroll
@@ -952,7 +954,9 @@ struct PanelRun {
 // one block each: the norm is summed, and the momentum moved, as the values are
 // first read.  A step of 128 x 128 takes 3.3 us, about evenly of LDS reads, matrix
 // instructions and conversions; the whole iteration 24 us (17 launches of the
-// tiled products: 65 us), as much for 256 matrices as for one.
+// tiled products: 65 us), 26 us for 256 matrices.  64 rows of 513 to 1024
+// columns (R, FN, W = 4, 4, 16) are more than the registers of 16 waves hold:
+// 128 of a lane go to scratch and back; 64 x 1024 44 us.
 template <int R, int FN, int W>
 __global__ __launch_bounds__(64 * W) void k_ns_small(PanelRun u, NsShape sh, NsStep st) {
     extern __shared__ __align__(16) char lds_raw[];
@@ -993,7 +997,7 @@ __global__ __launch_bounds__(64 * W) void k_ns_small(PanelRun u, NsShape sh, NsS
 // result.  Either leaves the panel's share of the next A.  Latency bounds both:
 // 8 us a step for 8 panels (1001 x 128) or 32 (4096 x 128); in tiled products A's
 // long sum ran in three blocks and the same matrices took 80 and 139 us in all,
-// against 56 and 64.
+// against 57 and 62.
 template <int R, int FN, bool STEP>
 __global__ __launch_bounds__(512) void k_ns_panel(PanelRun u, NsShape sh, NsStep st, int left) {
     extern __shared__ __align__(16) char lds_raw[];

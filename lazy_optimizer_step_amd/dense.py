@@ -255,7 +255,8 @@ def newton_schulz(g: torch.Tensor, *, steps: int = 5, coefficients=NS_COEFFICIEN
                   validate: bool = False) -> torch.Tensor:
     """The Newton-Schulz iteration of a matrix (or each of a batch, leading axes), near its
     orthogonal factor.  g: float32 or bfloat16, contiguous; the result is bfloat16 (its
-    products are taken in float16, float32 sums)."""
+    products are taken in float16 for either, with float32 sums; dense_ops.h states the
+    accuracy)."""
     batch, m, n = _matrices(g, "g")
     if out is not None:
         _need(out, torch.bfloat16, "out", g.numel())
@@ -298,7 +299,9 @@ class Muon:
 
     adjust: the factor in front of the orthogonalised update, by the matrix's
     shape m x n: "spectral" sqrt(max(1, m / n)), "rms" 0.2 sqrt(max(m, n))
-    (updates of the size Adam's have), or a number."""
+    (updates of the size Adam's have), or a number.  The object keeps its momentum and
+    a workspace of newton_schulz_workspace_size bytes (12 a value of a large square
+    matrix); weights that should share one take muon_step(workspace=...)."""
 
     def __init__(self, params: torch.Tensor, lr: float, momentum: float = 0.95,
                  nesterov: bool = True, weight_decay: float = 0.0, adjust="spectral",
