@@ -1,0 +1,236 @@
+"""The loss at the end of a model over an embedding table, and the dropout inside it, as measured cases.
+
+Softmax cross entropy of a hidden state against every row of an output table (the logits are never kept), its
+gradients, and dropout whose mask comes out of a counter-based generator, forward (with the residual stream
+added) and backward.  A case is one call of one of them.
+"""
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+IGNORED = -100
+
+
+def listed():
+    return [
+        # eight bags of tokens over an odd number of classes, each row's own loss: latency
+        {"name": "loss 8x128x1001 f16", "op": "ce_forward", "rows": 8, "cols": 128, "classes": 1001, "dtype": "f16", "reduction": "none", "smoothing": 0.1, "ignored": 0.0},
+        # one token scored against a whole vocabulary: the table is read once
+        {"name": "loss 1x1024x50001 bf16", "op": "ce_forward", "rows": 1, "cols": 1024, "classes": 50001, "dtype": "bf16", "reduction": "mean", "smoothing": 0.0, "ignored": 0.0},
+        # a batch of lookups out of a 128-column table, all in 32 bits as the table is
+        {"name": "loss 8192x128x50021 f32", "op": "ce_forward", "rows": 8192, "cols": 128, "classes": 50021, "dtype": "f32", "reduction": "mean", "smoothing": 0.0, "ignored": 0.1},
+        # a training batch of a wide model over a large vocabulary
+        {"name": "loss 4096x2048x131072 bf16", "op": "ce_forward", "rows": 4096, "cols": 2048, "classes": 131072, "dtype": "bf16", "reduction": "mean", "smoothing": 0.0, "ignored": 0.1},
+        # the small batch's gradients, in 32 bits: latency
+        {"name": "gradients 8x128x1001 f32", "op": "ce_backward", "rows": 8, "cols": 128, "classes": 1001, "dtype": "f32", "reduction": "mean", "smoothing": 0.0, "ignored": 0.0},
+        # a ragged batch at odd sizes, labels smoothed, a weight for each row's loss
+        {"name": "gradients 1000x520x32003 f16", "op": "ce_backward", "rows": 1000, "cols": 520, "classes": 32003, "dtype": "f16", "reduction": "none", "smoothing": 0.1, "ignored": 0.1},
+        # the lookups' gradients
+        {"name": "gradients 8192x128x50021 f32", "op": "ce_backward", "rows": 8192, "cols": 128, "classes": 50021, "dtype": "f32", "reduction": "mean", "smoothing": 0.0, "ignored": 0.1},
+        # the gradients of a training batch of a wide model over a large vocabulary
+        {"name": "gradients 8192x4096x131072 bf16", "op": "ce_backward", "rows": 8192, "cols": 4096, "classes": 131072, "dtype": "bf16", "reduction": "mean", "smoothing": 0.0, "ignored": 0.1},
+        # a few tokens: latency
+        {"name": "dropout 4x1024 bf16", "op": "dropout_forward", "rows": 4, "cols": 1024, "dtype": "bf16", "p": 0.1, "residual": False},
+        # the branch of a wide model's block, back onto its residual stream
+        {"name": "dropout 16384x4096 bf16 residual", "op": "dropout_forward", "rows": 16384, "cols": 4096, "dtype": "bf16", "p": 0.1, "residual": True},
+        # the gradient on its way back to a batch of lookups
+        {"name": "dropout backward 65536x128 f32", "op": "dropout_backward", "rows": 65536, "cols": 128, "dtype": "f32", "p": 0.2, "residual": False},
+        # an odd width
+        {"name": "dropout backward 777x5003 f16", "op": "dropout_backward", "rows": 777, "cols": 5003, "dtype": "f16", "p": 0.5, "residual": False},
+    ]
+
+
+def _between(rng, low, high):
+    """A whole number, its logarithm uniform over [low, high]."""
+    return min(high, max(low, round(math.exp(rng.uniform(math.log(low), math.log(high))))))
+
+
+def draw(rng):
+    op = rng.choice(["ce_forward", "ce_backward", "dropout_forward", "dropout_backward"])
+    dtype = rng.choice(["f32", "bf16", "f16"])
+    if op in ("ce_forward", "ce_backward"):
+        return {"op": op, "rows": _between(rng, 1, 8192), "cols": _between(rng, 16, 2048 if dtype == "f32" else 4096), "classes": _between(rng, 2, 131072), "dtype": dtype,
+                "reduction": rng.choice(["mean", "sum", "none"]), "smoothing": rng.choice([0.0, 0.0, 0.1]), "ignored": rng.choice([0.0, 0.1, 0.5])}
+    cols = _between(rng, 16, 16384)
+    rows = _between(rng, 1, min(131072, (16384 * 4096 >> (dtype == "f32")) // cols))
+    return {"op": op, "rows": rows, "cols": cols, "dtype": dtype, "p": rng.choice([0.05, 0.1, 0.2, 0.5]), "residual": op == "dropout_forward" and rng.random() < 0.5}
+
+
+def prepare(case, seed):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+
+    def randn(*shape):
+        return torch.randn(shape, device="cuda", generator=gen)
+
+    def rand(*shape):
+        return torch.rand(shape, device="cuda", generator=gen)
+
+    s = dict(case)
+    t, rows, cols = DTYPES[case["dtype"]], case["rows"], case["cols"]
+    if case["op"].startswith("dropout"):
+        s["seed"], s["offset"] = seed * 0x9E3779B97F4A7C15 % 2 ** 63, seed % 1000
+        s["x"] = randn(rows, cols).to(t)
+        if case["residual"]:
+            s["stream"] = (2 * randn(rows, cols)).to(t)
+        return s
+    classes = case["classes"]
+    # the hidden state is of a norm's output; its target's row has drawn it near (training has begun), and targets
+    # fall off along the table as words do
+    weight = randn(classes, cols) * (2 / math.sqrt(cols))
+    targets = (classes * rand(rows) ** 3).long().clamp(max=classes - 1)
+    x = randn(rows, cols) + rand(rows, 1) * weight[targets]
+    targets[rand(rows) < case["ignored"]] = IGNORED
+    s["x"], s["weight"], s["targets"] = x.to(t), weight.to(t), targets
+    if case["op"] == "ce_backward":
+        # what the forward pass kept
+        w = s["weight"].float().t()
+        s["lse"] = torch.cat([torch.logsumexp((part.float() @ w).double(), 1) for part in s["x"].split(1024)]).float()
+        s["dloss"] = 0.5 + rand(rows) if case["reduction"] == "none" else 0.5 + rand(1)[0]
+    return s
+
+
+def _philox(index, seed, offset):
+    """The four 32-bit words of Philox4x32-10 (Salmon et al., 2011) at each counter (index, offset), as int64."""
+    low = 0xFFFFFFFF
+
+    def product(a, m):
+        # high and low words of a * m, within 63 bits
+        p, q = a * (m & 0xFFFF), a * (m >> 16)
+        return (q + (p >> 16)) >> 16, (p + ((q & 0xFFFF) << 16)) & low
+
+    c = [index & low, index >> 32, torch.full_like(index, offset & low), torch.full_like(index, offset >> 32)]
+    k0, k1 = seed & low, seed >> 32
+    for _ in range(10):
+        h0, l0 = product(c[0], 0xD2511F53)
+        h1, l1 = product(c[2], 0xCD9E8D57)
+        c = [h1 ^ c[1] ^ k0, l1, h0 ^ c[3] ^ k1, l0]
+        k0, k1 = (k0 + 0x9E3779B9) & low, (k1 + 0xBB67AE85) & low
+    return c
+
+
+def _kept(numel, p, seed, offset, device):
+    """Which values stay: value i takes the i % 8 th 16 bits of counter i / 8, and stays if they are at least p 2^16."""
+    words = torch.stack(_philox(torch.arange((numel + 7) // 8, device=device), seed, offset), 1)
+    bits = torch.stack([words & 0xFFFF, words >> 16], 2).flatten()[:numel]
+    return bits >= round(p * 65536)
+
+
+def _gradient_of_logits(state, logits):
+    """The gradient with respect to the logits, in their place; rows that are ignored get zeros."""
+    targets, e, classes = state["targets"], state["smoothing"], state["classes"]
+    valid = targets != IGNORED
+    g = logits.sub_(state["lse"][:, None]).exp_().sub_(e / classes)
+    rows = torch.arange(g.shape[0], device=g.device)
+    at = targets.clamp(min=0)
+    g[rows, at] -= 1 - e
+    scale = state["dloss"]
+    if state["reduction"] == "mean":
+        scale = scale / valid.sum().clamp(min=1)
+    return g.mul_(torch.where(valid, scale, 0.0)[:, None])
+
+
+def run(state):
+    op = state["op"]
+    if own:
+        import lazy_optimizer_step_amd as L
+        if op == "ce_forward":
+            loss, lse = L.linear_cross_entropy_forward(state["x"], state["weight"], state["targets"], reduction=state["reduction"], ignore_index=IGNORED,
+                                                       label_smoothing=state["smoothing"])
+            return {"loss": loss, "lse": lse}
+        if op == "ce_backward":
+            dx, dw = L.linear_cross_entropy_backward(state["dloss"], state["x"], state["weight"], state["targets"], state["lse"], reduction=state["reduction"],
+                                                     ignore_index=IGNORED, label_smoothing=state["smoothing"])
+            return {"dx": dx, "dweight": dw}
+        if op == "dropout_forward":
+            return {"y": L.dropout_forward(state["x"], state["p"], state["seed"], offset=state["offset"], residual=state.get("stream"))}
+        return {"dx": L.dropout_backward(state["x"], state["p"], state["seed"], offset=state["offset"])}
+    x = state["x"]
+    if op.startswith("dropout"):
+        keep = _kept(x.numel(), state["p"], state["seed"], state["offset"], x.device).view(x.shape)
+        y = torch.where(keep, x.float() * (65536 / (65536 - round(state["p"] * 65536))), 0.0)
+        if "stream" in state:
+            y = y + state["stream"].float()
+        return {"y" if op == "dropout_forward" else "dx": y.to(x.dtype)}
+    xf, wf, targets = x.float(), state["weight"].float(), state["targets"]
+    logits = xf @ wf.t()
+    if op == "ce_backward":
+        g = _gradient_of_logits(state, logits)
+        return {"dx": (g @ wf).to(x.dtype), "dweight": (g.t() @ xf).to(x.dtype)}
+    top = logits.max(1, keepdim=True).values
+    lse = torch.log((logits - top).exp().sum(1)) + top[:, 0]
+    valid, e = targets != IGNORED, state["smoothing"]
+    loss = lse - (1 - e) * logits[torch.arange(len(lse), device=lse.device), targets.clamp(min=0)] - e * logits.mean(1)
+    loss = torch.where(valid, loss, 0.0)
+    if state["reduction"] != "none":
+        loss = loss.sum()
+    if state["reduction"] == "mean":
+        loss = loss / valid.sum().clamp(min=1)
+    return {"loss": loss, "lse": lse}
+
+
+def work(case):
+    e = {"f32": 4, "bf16": 2, "f16": 2}[case["dtype"]]
+    n, d = case["rows"], case["cols"]
+    if case["op"].startswith("dropout"):
+        return {"bytes": (3 if case["residual"] else 2) * n * d * e, "flops": 2 * n * d}
+    v = case["classes"]
+    if case["op"] == "ce_forward":
+        return {"bytes": (n + v) * d * e + 12 * n + (4 * n if case["reduction"] == "none" else 4), "flops": 2 * n * v * d + 4 * n * v}
+    # the logits again, and the two products of their gradient
+    return {"bytes": 2 * (n + v) * d * e + 12 * n + (4 * n if case["reduction"] == "none" else 4), "flops": 6 * n * v * d + 4 * n * v}
+
+
+def _words_of(counters, seed, offset):
+    """The same generator in unsigned 64-bit arithmetic on the host: [counters, 8] of 16 bits."""
+    u = np.uint64
+    low, half = u(0xFFFFFFFF), u(32)
+    x0, x1 = counters & low, counters >> half
+    x2, x3 = np.full_like(counters, offset & 0xFFFFFFFF), np.full_like(counters, offset >> 32)
+    key = [seed & 0xFFFFFFFF, seed >> 32]
+    for turn in range(10):
+        a, b = x0 * u(0xD2511F53), x2 * u(0xCD9E8D57)
+        ka, kb = (u((key[i] + turn * step) & 0xFFFFFFFF) for i, step in ((0, 0x9E3779B9), (1, 0xBB67AE85)))
+        x0, x1, x2, x3 = (b >> half) ^ x1 ^ ka, b & low, (a >> half) ^ x3 ^ kb, a & low
+    return np.stack([x0, x1, x2, x3], 1).astype("<u4").view("<u2")
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    x = s["x"].double()
+    if case["op"].startswith("dropout"):
+        few = 1 << 20
+        counters = -(-x.numel() // 8)
+        bits = np.concatenate([_words_of(np.arange(a, min(a + few, counters), dtype=np.uint64), s["seed"], s["offset"]) for a in range(0, counters, few)])
+        stays = torch.from_numpy((bits >= round(65536 * case["p"])).reshape(-1)[:x.numel()]).to(x.device).view(x.shape)
+        y = x * stays / (1 - round(65536 * case["p"]) / 65536)
+        return {"dx": y} if case["op"] == "dropout_backward" else {"y": torch.add(y, s["stream"].double()) if case["residual"] else y}
+    weight, targets, e, classes = s["weight"].double(), s["targets"], case["smoothing"], case["classes"]
+    counted = (targets != IGNORED).double()
+    share = counted / max(1.0, float(counted.sum())) if case["reduction"] == "mean" else counted
+    # the distribution that the softmax is held against, a few rows at a time
+    each = max(1, (1 << 27) // classes)
+    lses, losses, dxs = [], [], []
+    dweight = torch.zeros_like(weight)
+    for a in range(0, case["rows"], each):
+        part, goal = x[a:a + each], targets[a:a + each].clamp(min=0)
+        logits = torch.matmul(part, weight.T)
+        lse = torch.logsumexp(logits, -1)
+        lses.append(lse)
+        if case["op"] == "ce_forward":
+            nll = (lse - logits.gather(1, goal[:, None])[:, 0]) * (1 - e) + (lse - logits.sum(1) / classes) * e
+            losses.append(nll * counted[a:a + each])
+            continue
+        wanted = torch.full_like(logits, e / classes).scatter_add_(1, goal[:, None], torch.full_like(lse, 1 - e)[:, None])
+        # the user's lse, as the call takes it
+        delta = (torch.exp(logits - s["lse"][a:a + each].double()[:, None]) - wanted) * (share[a:a + each] * s["dloss"].double().expand(case["rows"])[a:a + each])[:, None]
+        dxs.append(torch.matmul(delta, weight))
+        dweight.addmm_(delta.T, part)
+    if case["op"] == "ce_backward":
+        return {"dx": torch.cat(dxs), "dweight": dweight}
+    loss = torch.cat(losses)
+    return {"loss": loss if case["reduction"] == "none" else (torch.cat(losses) * share).sum() if case["reduction"] == "mean" else loss.sum(), "lse": torch.cat(lses)}
