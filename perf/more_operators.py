@@ -90,6 +90,7 @@ def prepare(case, seed):
         # what the forward pass kept
         w = s["weight"].float().t()
         s["lse"] = torch.cat([torch.logsumexp((part.float() @ w).double(), 1) for part in s["x"].split(1024)]).float()
+        s["lse"] *= targets != IGNORED
         s["dloss"] = 0.5 + rand(rows) if case["reduction"] == "none" else 0.5 + rand(1)[0]
     return s
 
@@ -165,7 +166,7 @@ def run(state):
     lse = torch.log((logits - top).exp().sum(1)) + top[:, 0]
     valid, e = targets != IGNORED, state["smoothing"]
     loss = lse - (1 - e) * logits[torch.arange(len(lse), device=lse.device), targets.clamp(min=0)] - e * logits.mean(1)
-    loss = torch.where(valid, loss, 0.0)
+    loss, lse = torch.where(valid, loss, 0.0), torch.where(valid, lse, 0.0)
     if state["reduction"] != "none":
         loss = loss.sum()
     if state["reduction"] == "mean":
@@ -220,7 +221,7 @@ def exact(case, seed):
         part, goal = x[a:a + each], targets[a:a + each].clamp(min=0)
         logits = torch.matmul(part, weight.T)
         lse = torch.logsumexp(logits, -1)
-        lses.append(lse)
+        lses.append(lse * counted[a:a + each])
         if case["op"] == "ce_forward":
             nll = (lse - logits.gather(1, goal[:, None])[:, 0]) * (1 - e) + (lse - logits.sum(1) / classes) * e
             losses.append(nll * counted[a:a + each])
