@@ -1,8 +1,9 @@
 /*
  * dense_ops.h - C ABI of the dense operators that stand between a table's
- * looked-up rows and the loss: layer norm (forward and backward), the
- * Newton-Schulz orthogonalisation of a matrix, and the Muon step that applies
- * it to a weight.
+ * looked-up rows and the loss, and of the loss: layer norm and dropout (forward
+ * and backward), the Newton-Schulz orthogonalisation of a matrix, the Muon step
+ * that applies it to a weight, and the softmax cross entropy over a table of
+ * classes (forward and backward).
  *
  * The conventions are those of sparse_opt.h: device pointers owned by the
  * caller, `stream` a hipStream_t as void*, SPOPT_OK or a negative spopt_status,
@@ -144,6 +145,111 @@ typedef struct spopt_muon_config {
 SPOPT_API int muon_step(void* params, int32_t pdtype, float* buf, const void* g, int32_t gdtype,
                         int64_t batch, int64_t m, int64_t n, const spopt_muon_config* config,
                         void* workspace, size_t workspace_bytes, void* stream, uint32_t flags);
+
+/* ---- the loss over a table of classes ------------------------------------ */
+
+#define SPOPT_REDUCE_NONE 0
+#define SPOPT_REDUCE_SUM 1
+#define SPOPT_REDUCE_MEAN 2
+
+/* Softmax cross entropy of rows x cols hidden states against a table of
+ * classes x cols, with z = x weight^T, e = label_smoothing and t = targets[i]:
+ *   lse_i  = log(sum over j of exp(z_ij)),
+ *   loss_i = lse_i - (1 - e) z_it - (e / classes) sum over j of z_ij.
+ * The rows x classes logits are never stored.  Rows whose target is
+ * ignore_index do not count: their loss and lse are 0, and what x holds there
+ * reaches nothing.
+ *   x         rows x cols of `dtype`, row k at x + k * x_stride.
+ *   weight    classes x cols of `dtype`, with its row stride.
+ *   targets   int64 [rows]; one that is neither a class nor ignore_index gives
+ *             NaN for its loss (SPOPT_ERANGE under SPOPT_VALIDATE).
+ *   loss      float: [rows] for SPOPT_REDUCE_NONE; one value, the sum over the
+ *             rows that count or their mean, for SPOPT_REDUCE_SUM and _MEAN (0
+ *             where no row counts).
+ *   lse       float [rows], what the backward pass takes.
+ * Types: 16-bit operands are multiplied as they are, with float32 sums.  Each
+ * value of float32 operands is taken as two float16 after a power of two that
+ * brings the operand's largest finite value (of x: in rows that count) to
+ * 2^14: 22 bits, for values below 2^-18 of the largest an absolute 2^-40 of it.
+ * The products of the two low parts are left out, sums are float32.  A NaN or
+ * an infinity in x makes its row NaN (of 16-bit types an infinity may cancel
+ * instead), in weight every row.
+ * Workspace: device, 16-byte aligned, linear_cross_entropy_workspace_size bytes
+ * for the pass (backward 0 or 1).  Inputs with cols a multiple of 64, strides
+ * multiples of 8 and 16-byte aligned bases are read in place where they are of
+ * 16 bits; others are copied into it, the weight up to 256 MiB at a time.
+ * Errors: SPOPT_EINVAL (NULL, sizes, a stride below cols, types, reduction,
+ * label_smoothing outside [0, 1]), SPOPT_EWORKSPACE; rows up to 2^28, cols to
+ * 2^20, classes to 2^30, either matrix to 2^38 values.  SPOPT_VALIDATE reads
+ * the targets, the rows of x that count, and weight. */
+SPOPT_API int linear_cross_entropy_workspace_size(int64_t rows, int64_t cols, int64_t classes,
+                                                  int32_t dtype, int32_t backward, size_t* bytes);
+SPOPT_API int linear_cross_entropy_forward(const void* x, int64_t x_stride, const void* weight,
+                                           int64_t weight_stride, int64_t rows, int64_t cols,
+                                           int64_t classes, int32_t dtype, const int64_t* targets,
+                                           int64_t ignore_index, double label_smoothing,
+                                           int32_t reduction, float* loss, float* lse,
+                                           void* workspace, size_t workspace_bytes, void* stream,
+                                           uint32_t flags);
+
+/* The gradients of linear_cross_entropy_forward, with c_i = dloss[i], dloss[0]
+ * or dloss[0] / (rows that count) by the reduction, 0 for rows that do not:
+ *   g_ij = c_i (exp(z_ij - lse_i) - (1 - e) [j == t] - e / classes),
+ *   dx = g weight, dweight = g^T x.
+ *   dloss     float: [rows] for SPOPT_REDUCE_NONE, else one value.
+ *   lse       float [rows], as the forward pass wrote it.
+ *   dx        rows x cols of `dtype`, with its row stride, or NULL.  Rows that do
+ *             not count get zeros.
+ *   dweight   classes x cols of `dtype`, with its row stride, or NULL.  Written,
+ *             not added to; all zero for rows == 0.
+ * None of the outputs may overlap another, an input or the workspace.
+ * g is rounded to the operands' type before the products (float32: taken as two
+ * float16 like the operands, after a power of two that brings the largest c_i
+ * to 2^13); sums are float32, rounded once.  g exists for one piece of the
+ * classes at a time, of up to 512 MiB (or 2048 classes).  A row whose target is
+ * neither a class nor ignore_index makes its row of dx and all of dweight NaN.
+ * Workspace, errors and validation as above. */
+SPOPT_API int linear_cross_entropy_backward(
+    const float* dloss, const void* x, int64_t x_stride, const void* weight, int64_t weight_stride,
+    int64_t rows, int64_t cols, int64_t classes, int32_t dtype, const int64_t* targets,
+    int64_t ignore_index, double label_smoothing, int32_t reduction, const float* lse, void* dx,
+    int64_t dx_stride, void* dweight, int64_t dweight_stride, void* workspace,
+    size_t workspace_bytes, void* stream, uint32_t flags);
+
+/* ---- dropout ------------------------------------------------------------- */
+
+/* Dropout whose mask is a function of (seed, offset, index) and is never
+ * stored: with q = round(p * 2^16) and value i = row * cols + col,
+ *   y_i = (bits_i >= q ? x_i * 2^16 / (2^16 - q) : 0) + residual_i,
+ * bits_i the (i % 8)th 16 bits, from the lowest of the first word on, of
+ * Philox4x32-10 (Salmon et al., "Parallel random numbers: as easy as 1, 2, 3",
+ * 2011) at counter words (i / 8 low, i / 8 high, offset low, offset high) under
+ * the key words (seed low, seed high).  So p counts in steps of 2^-16, and the
+ * factor is that of the p taken: the mean of y is x.  Offsets give independent
+ * masks under one seed (one for each layer and step).
+ *   x, y      rows x cols of `dtype`, each with its row stride; y may be x or
+ *             residual (then with the same stride).
+ *   residual  rows x cols of `dtype` with its row stride, or NULL: 0.
+ *   p         in [0, 1]; q == 2^16 drops every value.
+ *   d_seed    device int64[1] or NULL.  Where given, the seed is read from it when
+ *             the call's kernel runs, so that a captured call can be replayed
+ *             with other masks; `seed` is not used.
+ * Values that are dropped are not looked at: a NaN or an infinity there leaves
+ * nothing.  y is formed in float32 and rounded once.  Rows and strides only
+ * change where values lie, not which are dropped.
+ * Errors: SPOPT_EINVAL (NULL x or y with rows > 0, rows < 0, cols < 1, a stride
+ * below cols, unknown type, p outside [0, 1]). */
+SPOPT_API int dropout_forward(const void* x, int64_t x_stride, const void* residual,
+                              int64_t residual_stride, int64_t rows, int64_t cols, int32_t dtype,
+                              double p, uint64_t seed, const int64_t* d_seed, uint64_t offset,
+                              void* y, int64_t y_stride, void* stream, uint32_t flags);
+
+/* The gradient: dx_i = bits_i >= q ? dy_i * 2^16 / (2^16 - q) : 0 (the residual's
+ * is dy).  dx may be dy.  Otherwise as dropout_forward. */
+SPOPT_API int dropout_backward(const void* dy, int64_t dy_stride, int64_t rows, int64_t cols,
+                               int32_t dtype, double p, uint64_t seed, const int64_t* d_seed,
+                               uint64_t offset, void* dx, int64_t dx_stride, void* stream,
+                               uint32_t flags);
 
 #ifdef __cplusplus
 }

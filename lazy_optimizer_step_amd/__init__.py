@@ -12,8 +12,8 @@ sparse_optimizer module page (COO/CSR gradients, sparse SGD, Lazy and
 DormancyDecay Adam with global-step bias correction) and, where it is silent,
 the DiskSparseAdam README (duplicates summed and sorted, validated inputs).
 
-Beside the table's step: layer norm and Muon (dense.py, include/dense_ops.h),
-which no page covers.
+Beside the table's step: layer norm, dropout, Muon and the loss over a table of
+classes (dense.py, loss.py, include/dense_ops.h), which no page covers.
 """
 from __future__ import annotations
 
@@ -37,7 +37,10 @@ __all__ = ["coo_from_lookups", "csr_from_coo", "csr_from_lookups", "csr_to_coo",
            "CsrGradient", "SparseAdam", "SparseSgd", "SparseOptError", "TRUSTED", "VALIDATE",
            "read_rows", "HostArray",
            "layer_norm_forward", "layer_norm_backward", "layer_norm_backward_workspace_size",
-           "LayerNorm", "newton_schulz", "newton_schulz_workspace_size", "muon_step", "Muon"]
+           "LayerNorm", "newton_schulz", "newton_schulz_workspace_size", "muon_step", "Muon",
+           "linear_cross_entropy_forward", "linear_cross_entropy_backward",
+           "linear_cross_entropy_workspace_size", "LinearCrossEntropy",
+           "dropout_forward", "dropout_backward", "Dropout"]
 
 
 def _stream(stream) -> int:
@@ -586,6 +589,8 @@ class SparseSgd:
 
 
 # The dense operators, which use the helpers above.
-from .dense import (LayerNorm, Muon, layer_norm_backward,  # noqa: E402
-                    layer_norm_backward_workspace_size, layer_norm_forward, muon_step,
-                    newton_schulz, newton_schulz_workspace_size)
+from .dense import (Dropout, LayerNorm, Muon, dropout_backward, dropout_forward,  # noqa: E402
+                    layer_norm_backward, layer_norm_backward_workspace_size, layer_norm_forward,
+                    muon_step, newton_schulz, newton_schulz_workspace_size)
+from .loss import (LinearCrossEntropy, linear_cross_entropy_backward,  # noqa: E402
+                   linear_cross_entropy_forward, linear_cross_entropy_workspace_size)

@@ -25,6 +25,7 @@ MODE_LAZY, MODE_DORMANCY = 0, 1
 WD_L2, WD_DECOUPLED = 0, 1
 FORMAT_COO, FORMAT_CSR = 0, 1
 DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
+REDUCE_NONE, REDUCE_SUM, REDUCE_MEAN = 0, 1, 2
 
 
 class AdamConfig(C.Structure):
@@ -131,9 +132,20 @@ def lib() -> C.CDLL:
         L.newton_schulz.argtypes = [P, I32, I64, I64, I64, C.POINTER(NsConfig), P, P, SZ, P, U32]
         L.muon_step.argtypes = [P, I32, P, P, I32, I64, I64, I64, C.POINTER(MuonConfig), P, SZ, P,
                                 U32]
+        U64 = C.c_uint64
+        L.linear_cross_entropy_workspace_size.argtypes = [I64, I64, I64, I32, I32, C.POINTER(SZ)]
+        L.linear_cross_entropy_forward.argtypes = [P, I64, P, I64, I64, I64, I64, I32, P, I64, F64,
+                                                   I32, P, P, P, SZ, P, U32]
+        L.linear_cross_entropy_backward.argtypes = [P, P, I64, P, I64, I64, I64, I64, I32, P, I64,
+                                                    F64, I32, P, P, I64, P, I64, P, SZ, P, U32]
+        L.dropout_forward.argtypes = [P, I64, P, I64, I64, I64, I32, F64, U64, P, U64, P, I64, P,
+                                      U32]
+        L.dropout_backward.argtypes = [P, I64, I64, I64, I32, F64, U64, P, U64, P, I64, P, U32]
         for f in (L.layer_norm_forward, L.layer_norm_backward_workspace_size,
                   L.layer_norm_backward, L.newton_schulz_workspace_size, L.newton_schulz,
-                  L.muon_step):
+                  L.muon_step, L.linear_cross_entropy_workspace_size,
+                  L.linear_cross_entropy_forward, L.linear_cross_entropy_backward,
+                  L.dropout_forward, L.dropout_backward):
             f.restype = C.c_int
         _lib = L
     return _lib
@@ -151,4 +163,6 @@ EXPORTED = ("sparse_opt_create", "sparse_opt_destroy", "sparse_opt_get_step", "s
             "sparse_opt_set_step_events", "read_rows",
             "sparse_opt_host_alloc", "sparse_opt_host_free", "sparse_opt_host_device_pointer",
             "layer_norm_forward", "layer_norm_backward_workspace_size", "layer_norm_backward",
-            "newton_schulz_workspace_size", "newton_schulz", "muon_step")
+            "newton_schulz_workspace_size", "newton_schulz", "muon_step",
+            "linear_cross_entropy_workspace_size", "linear_cross_entropy_forward",
+            "linear_cross_entropy_backward", "dropout_forward", "dropout_backward")

@@ -1,0 +1,1276 @@
+// cross_entropy.hip - softmax cross entropy of hidden states against every row
+// of a table of classes, forward and backward, without keeping the logits.
+//
+// With z = x W^T (rows x classes):
+//   forward   lse_i = log sum_j exp z_ij,  loss_i = lse_i - (1 - e) z_it - e mean_j z_ij
+//   backward  g_ij = c_i (exp(z_ij - lse_i) - (1 - e) [j = t] - e / classes),
+//             dx = g W,  dW = g^T x
+// Matrix products bound both: 2 and 6 operations for each row, class and
+// column.  The forward pass turns each tile of z into its rows' maximum and sum
+// of exponentials, in registers; a small kernel joins the tiles' pairs.  The
+// backward pass goes over the classes in pieces: z of a piece once more, g of
+// it in 16 bits into the workspace, and from there the piece's rows of dW and
+// its share of dx.  Nothing of rows x classes outlives a piece.
+//
+// Types.  16-bit operands go to the matrix cores as they are, sums are float32,
+// and g is rounded to the operands' type (in front of it 2^k that brings the
+// largest c_i to 2^13, which float16 needs for small probabilities).  A float32
+// operand a becomes two float16, hi = a 2^e rounded and lo = a 2^e - hi rounded,
+// e one for the whole operand that brings its largest value to 2^14: 22 bits of
+// each value (fewer of those below 2^-18 of the largest: off by 2^-40 of it at
+// most).  A product is hi hi + hi lo + lo hi, three matrix instructions in place
+// of one, which together still run at twice the rate of the float32 ones.
+#include <math.h>
+
+#include <type_traits>
+
+#include "dense.hpp"
+#include "matrix.hpp"
+
+namespace spopt {
+
+typedef __bf16 bhalf8 __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ float4v matrix_16x16x32(half8 a, half8 b, float4v c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ float4v matrix_16x16x32(bhalf8 a, bhalf8 b, float4v c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// What a call's kernels hand on to the next ones.
+struct CeScalars {
+    int ex, ew, ek;  // powers of two in front of the operands x, W (float32) and g
+};
+
+// An operand of a product: rows of 16-bit values.  Where the inner axis runs
+// along the rows, `last` is the last row; where it runs from row to row, the
+// last row and `cols` the columns that each row holds (a multiple of 8).  Split
+// rows hold 32 hi values, then their 32 lo, and so on.
+struct CeOperand {
+    const void* base;
+    int64_t ld, last, cols;
+};
+
+struct CeProduct {
+    CeOperand p, q;
+    int64_t m, n;     // the result's rows and columns
+    int64_t steps;    // of the inner axis, 64 values each (32 split)
+    int splits;       // parts of the inner axis
+    int64_t tiles_m, tiles_n;
+};
+
+// What is done with a tile of the logits.
+struct CeLogits {
+    const CeScalars* scalars;
+    const int64_t* targets;
+    int64_t first;       // class of the piece's first column
+    int64_t classes;     // of all pieces
+    float smoothing;
+    // forward
+    float2* parts;       // [tile of classes][row]: maximum, sum of exponentials
+    float* sums;         // [tile of classes][row]: sum of the logits (smoothing only)
+    float* at_target;    // [row]
+    int64_t first_tile;
+    // backward
+    const float* lse;
+    const float* coef;   // [row] c_i 2^k
+    void* g;             // [row][ldg]
+    int64_t ldg, rows_p, cols_p;  // g's extent, zeros beyond the matrix
+};
+
+// Where a product's result goes: sums in float32, [split][row][ld], added to
+// what is there or not; or (parts NULL) scaled and rounded to where it belongs.
+struct CeResult {
+    const CeScalars* scalars;
+    int of_w;            // the other operand is W (dx), else x (dW)
+    float* parts;
+    int64_t ld;
+    int add;
+    void* out;
+    int64_t out_ld;
+};
+
+enum : int { kCeLoss = 0, kCeGrad = 1, kCeDx = 2, kCeDw = 3 };
+
+// The product of one tile, in the order of matrix.hpp's helpers: operands go
+// through LDS 64 values of the inner axis at a time, loaded straight into it
+// while earlier stages are multiplied.  Operands whose inner axis lies along
+// their rows are laid out with chunk c of 8 values at c ^ (row & 7); the others
+// are turned as they are read.  Split operands bring 32 values of the inner
+// axis a stage, hi in its first half and lo in its second.
+template <class T, bool SPLIT, bool TP, bool TQ, class TL>
+struct CeTile {
+    static constexpr int BM = TL::BM, BN = TL::BN, WM = BM / TL::WGM, WN = BN / TL::WGN;
+    static constexpr int FM = WM / 16, FN = WN / 16, kWaves = TL::WGM * TL::WGN;
+    static constexpr int kRow = TQ ? 4 : 8;  // adjacent columns of a lane
+    static constexpr int kLoadsP = BM / 8 / kWaves, kLoadsQ = BN / 8 / kWaves;
+    static constexpr int kInner = SPLIT ? 32 : 64;
+    typedef T vec8 __attribute__((ext_vector_type(8)));
+    typedef T vec4 __attribute__((ext_vector_type(4)));
+    static_assert(BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0, "rows share out evenly");
+    static_assert(TQ || FN % 2 == 0, "eight adjacent columns take two parts");
+
+    // A side's loads: a lane's places in the operand.
+    template <bool TURN, int B, int LOADS>
+    struct Feed {
+        const T* src[LOADS];
+        int row[TURN ? LOADS : 1];
+        int64_t ld, last;
+        __device__ __forceinline__ void init(const CeOperand& o, int64_t first, int lane, int wv,
+                                             bool pair) {
+            const T* base = (const T*)o.base;
+            ld = o.ld;
+            last = o.last;
+#pragma unroll
+            for (int l = 0; l < LOADS; ++l) {
+                if constexpr (TURN) {
+                    const int at = (l * kWaves + wv) * 64 + lane;
+                    const int v = at / (B / 8), slot = at % (B / 8);
+                    int64_t c = first + (((slot >> 1) ^ turn_q<B>(v)) * 2 + (slot & 1)) * 8;
+                    if (c > o.cols - 8) c = o.cols - 8;
+                    if (SPLIT) c = (c / 32) * 64 + c % 32 + (v >> 5) * 32;
+                    row[l] = SPLIT ? v & 31 : v;
+                    src[l] = base + c;
+                } else {
+                    const int at = (l * kWaves + wv) * 8 + (lane >> 3);
+                    int64_t r = first + at;
+                    if (pair) {
+                        const int in = at & 31;
+                        r = first + at - in + ((in & 12) >> 2) * 8 + (in >> 4) * 4 + (in & 3);
+                    }
+                    if (r > last) r = last;
+                    src[l] = base + r * ld + ((lane & 7) ^ (lane >> 3)) * 8;
+                }
+            }
+        }
+        __device__ __forceinline__ void bring(int64_t k, T* to, int wv) const {
+#pragma unroll
+            for (int l = 0; l < LOADS; ++l) {
+                const T* from;
+                if constexpr (TURN) {
+                    int64_t r = k * kInner + row[l];
+                    if (r > last) r = last;
+                    from = src[l] + r * ld;
+                } else {
+                    from = src[l] + k * 64;
+                }
+                load_lds16(from, to + (l * kWaves + wv) * 512);
+            }
+        }
+    };
+
+    int lane, wv, wi, wj;
+    float4v acc[FM][FN];
+
+    // Operand `f` of half kk from a side's stage in LDS.
+    template <bool TURN, int B>
+    __device__ __forceinline__ vec8 operand(const T* l, int first, int kk) const {
+        if constexpr (TURN) {
+            const int row = (lane >> 4) * 8 + ((lane & 15) >> 2);
+            const T* a = l + (kk * 32 + row) * B + ((first / 16) ^ turn_q<B>(row)) * 16 +
+                         (lane & 3) * 4;
+            const vec4 lo = __builtin_bit_cast(vec4, read_turned((const _Float16*)a));
+            const vec4 hi = __builtin_bit_cast(vec4, read_turned((const _Float16*)(a + 4 * B)));
+            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        } else {
+            return *(const vec8*)(l + (first + (lane & 15)) * kTile +
+                                  ((kk * 4 + (lane >> 4)) ^ (lane & 7)) * 8);
+        }
+    }
+
+    __device__ __forceinline__ void multiply(const vec8 (&fa)[FM], const vec8 (&fb)[FN]) {
+#pragma unroll
+        for (int x = 0; x < FM; ++x)
+#pragma unroll
+            for (int y = 0; y < FN; ++y) acc[x][y] = matrix_16x16x32(fb[y], fa[x], acc[x][y]);
+    }
+
+    __device__ __forceinline__ void init() {
+        lane = lane_id();
+        wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        wi = (wv / TL::WGN) * WM;
+        wj = (wv % TL::WGN) * WN;
+#pragma unroll
+        for (int x = 0; x < FM; ++x)
+#pragma unroll
+            for (int y = 0; y < FN; ++y) acc[x][y] = float4v{0.f, 0.f, 0.f, 0.f};
+    }
+
+    // Steps [k0, k1) of the inner axis, at least one.
+    __device__ __forceinline__ void run(T* lds, const CeProduct& c, int64_t i0, int64_t j0,
+                                        int64_t k0, int64_t k1) {
+        Feed<TP, BM, kLoadsP> fp;
+        Feed<TQ, BN, kLoadsQ> fq;
+        fp.init(c.p, i0, lane, wv, false);
+        fq.init(c.q, j0, lane, wv, !TQ);
+        constexpr int kLoads = kLoadsP + kLoadsQ;
+        // Past the end the last step is brought again, so that every wait counts
+        // the same loads; nothing reads it.
+        auto stage = [&](int buf, int64_t k) {
+            if (k >= k1) k = k1 - 1;
+            T* const to = lds + buf * TL::kStage;
+            fp.bring(k, to, wv);
+            fq.bring(k, to + BM * kTile, wv);
+        };
+        vec8 fa0[FM], fb0[FN], fa1[FM], fb1[FN];
+        auto operands = [&](int buf, int kk, vec8 (&fa)[FM], vec8 (&fb)[FN]) {
+            const T* lp = lds + buf * TL::kStage;
+            const T* lq = lp + BM * kTile;
+#pragma unroll
+            for (int y = 0; y < FN; ++y) fb[y] = operand<TQ, BN>(lq, wj + y * 16, kk);
+#pragma unroll
+            for (int x = 0; x < FM; ++x) fa[x] = operand<TP, BM>(lp, wi + x * 16, kk);
+        };
+        int buf = 0;
+#pragma unroll
+        for (int k = 0; k < TL::STAGES - 1; ++k) stage(k, k0 + k);
+        for (int64_t k = k0; k < k1; ++k) {
+            // This stage's loads have landed in every wave, and every wave has
+            // read the stage before, whose place the next loads take.
+            wait_stage<(TL::STAGES - 2) * kLoads>();
+            stage(buf == 0 ? TL::STAGES - 1 : buf - 1, k + TL::STAGES - 1);
+            operands(buf, 0, fa0, fb0);
+            multiply(fa0, fb0);
+            operands(buf, 1, fa1, fb1);
+            if constexpr (SPLIT) {
+                multiply(fa0, fb1);
+                multiply(fa1, fb0);
+            } else {
+                multiply(fa1, fb1);
+            }
+            buf = buf + 1 == TL::STAGES ? 0 : buf + 1;
+        }
+        wait_loads<0>();
+    }
+
+    // Row x and column (y, e) of this lane, within the tile.
+    __device__ __forceinline__ int row_of(int x) const { return wi + x * 16 + (lane & 15); }
+    __device__ __forceinline__ int col_of(int y) const {
+        return wj + (lane >> 4) * kRow + (kRow == 8 ? (y & ~1) * 16 + (y & 1) * 4 : y * 16);
+    }
+};
+
+// Tile `t` of a product, four rows of tiles at a time, column by column.
+__device__ __forceinline__ void ce_place(int64_t t, int64_t tm, int64_t tn, int64_t* ti,
+                                         int64_t* tj) {
+    const int64_t band = t / (4 * tn), in = t % (4 * tn);
+    const int64_t rows = tm - 4 * band < 4 ? tm - 4 * band : 4;
+    *ti = 4 * band + in % rows;
+    *tj = in / rows;
+}
+
+// The column of class `target` in a tile whose first is `first`; -1 where it lies
+// far from it.
+__device__ __forceinline__ int ce_column(int64_t target, int64_t first) {
+    const uint64_t j = (uint64_t)target - (uint64_t)first;
+    return j < 4096 ? (int)j : -1;
+}
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// exp(z - b), the difference formed before it is scaled.
+__device__ __forceinline__ float exp_less(float z, float b) {
+    return __builtin_amdgcn_exp2f((z - b) * kLog2e);
+}
+
+template <class T, bool SPLIT, int MODE, class TL>
+__global__ __launch_bounds__(TL::kThreads) void k_ce_logits(CeProduct c, CeLogits w) {
+    extern __shared__ __align__(16) char lds_raw[];
+    typedef CeTile<T, SPLIT, false, false, TL> Tile;
+    constexpr int FM = Tile::FM, FN = Tile::FN, BM = TL::BM, BN = TL::BN;
+    int64_t ti, tj;
+    ce_place(xcd_order(blockIdx.x, gridDim.x), c.tiles_m, c.tiles_n, &ti, &tj);
+    const int64_t i0 = ti * BM, j0 = tj * BN;
+    Tile tile;
+    tile.init();
+    tile.run((T*)lds_raw, c, i0, j0, 0, c.steps);
+    const int scale = SPLIT ? -(w.scalars->ex + w.scalars->ew) : 0;
+    const bool whole = j0 + BN <= c.n;
+    const float off = w.smoothing / (float)w.classes, on = 1.f - w.smoothing;
+
+    if constexpr (MODE == kCeLoss) {
+        float* const red = (float*)lds_raw;  // [WGN][3][BM]
+        __syncthreads();
+        const int wn = tile.wv % TL::WGN;
+#pragma unroll
+        for (int x = 0; x < FM; ++x) {
+            const int r = tile.row_of(x);
+            const int64_t i = i0 + r;
+            const int t = i < c.m ? ce_column(w.targets[i], w.first + j0) : -1;
+            float top = -INFINITY, z = 0.f, s = 0.f;
+#pragma unroll
+            for (int y = 0; y < FN; ++y)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float v = tile.acc[x][y][e];
+                    if (SPLIT) v = ldexpf(v, scale);
+                    const int j = tile.col_of(y) + e;
+                    if (whole || j0 + j < c.n) {
+                        z += v;
+                        if (j == t) w.at_target[i] = v;
+                    } else {
+                        v = -INFINITY;
+                    }
+                    tile.acc[x][y][e] = v;
+                    top = fmaxf(top, v);
+                }
+            top = fmaxf(top, __shfl_xor(top, 16, kWave));
+            top = fmaxf(top, __shfl_xor(top, 32, kWave));
+            const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+            for (int y = 0; y < FN; ++y)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s += exp_less(tile.acc[x][y][e], base);
+            s += __shfl_xor(s, 16, kWave);
+            s += __shfl_xor(s, 32, kWave);
+            z += __shfl_xor(z, 16, kWave);
+            z += __shfl_xor(z, 32, kWave);
+            if (tile.lane < 16) {
+                red[(wn * 3 + 0) * BM + r] = top;
+                red[(wn * 3 + 1) * BM + r] = s;
+                red[(wn * 3 + 2) * BM + r] = z;
+            }
+        }
+        __syncthreads();
+        for (int r = threadIdx.x; r < BM; r += TL::kThreads) {
+            if (i0 + r >= c.m) break;
+            float top = -INFINITY, s = 0.f, z = 0.f;
+#pragma unroll
+            for (int k = 0; k < TL::WGN; ++k) top = fmaxf(top, red[k * 3 * BM + r]);
+            const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+            for (int k = 0; k < TL::WGN; ++k) {
+                s += red[(k * 3 + 1) * BM + r] * exp_less(red[k * 3 * BM + r], base);
+                z += red[(k * 3 + 2) * BM + r];
+            }
+            const int64_t at = (w.first_tile + tj) * c.m + i0 + r;
+            w.parts[at] = make_float2(top, s);
+            if (w.sums) w.sums[at] = z;
+        }
+    } else {
+        T* const g = (T*)w.g;
+#pragma unroll
+        for (int x = 0; x < FM; ++x) {
+            const int64_t i = i0 + tile.row_of(x);
+            if (i >= w.rows_p) continue;
+            const bool row = i < c.m;
+            const int t = row ? ce_column(w.targets[i], w.first + j0) : -1;
+            const float coef = row ? w.coef[i] : 0.f, lse = row ? w.lse[i] : 0.f;
+#pragma unroll
+            for (int y = 0; y < FN; y += 2) {
+                const int j = tile.col_of(y);
+                if (j0 + j >= w.cols_p) continue;
+                float v[8], lo[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float z = tile.acc[x][y + e / 4][e & 3];
+                    if (SPLIT) z = ldexpf(z, scale);
+                    float p = exp_less(z, lse) - off;
+                    if (j + e == t) p -= on;
+                    p *= coef;
+                    // Rows that do not count may hold anything.
+                    v[e] = coef == 0.f || (!whole && j0 + j + e >= c.n) ? 0.f : p;
+                }
+                if constexpr (SPLIT) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) lo[e] = v[e] - (float)(T)v[e];
+                    T* to = g + i * w.ldg + (j0 + j) / 32 * 64 + (j0 + j) % 32;
+                    store_v<T, 8>(to, v);
+                    store_v<T, 8>(to + 32, lo);
+                } else {
+                    store_v<T, 8>(g + i * w.ldg + j0 + j, v);
+                }
+            }
+        }
+    }
+}
+
+template <class T, bool SPLIT, int MODE, class TL>
+__global__ __launch_bounds__(TL::kThreads) void k_ce_product(CeProduct c, CeResult w) {
+    extern __shared__ __align__(16) char lds_raw[];
+    typedef CeTile<T, SPLIT, MODE == kCeDw, true, TL> Tile;
+    typedef std::conditional_t<SPLIT, float, T> O;
+    constexpr int FM = Tile::FM, FN = Tile::FN, BM = TL::BM, BN = TL::BN;
+    const int64_t tiles = c.tiles_m * c.tiles_n;
+    const int64_t b = xcd_order(blockIdx.x, gridDim.x);
+    const int64_t split = b / tiles;
+    int64_t ti, tj;
+    ce_place(b % tiles, c.tiles_m, c.tiles_n, &ti, &tj);
+    const int64_t i0 = ti * BM, j0 = tj * BN;
+    const int64_t k0 = split * c.steps / c.splits, k1 = (split + 1) * c.steps / c.splits;
+    Tile tile;
+    tile.init();
+    if (k0 < k1) tile.run((T*)lds_raw, c, i0, j0, k0, k1);
+    if (w.parts != nullptr) {
+        float* const out = w.parts + split * c.m * w.ld;
+#pragma unroll
+        for (int x = 0; x < FM; ++x) {
+            const int64_t i = i0 + tile.row_of(x);
+            if (i >= c.m) continue;
+#pragma unroll
+            for (int y = 0; y < FN; ++y) {
+                const int64_t j = j0 + tile.col_of(y);
+                if (j >= w.ld) continue;
+                float4v* const to = (float4v*)(out + i * w.ld + j);
+                *to = w.add ? *to + tile.acc[x][y] : tile.acc[x][y];
+            }
+        }
+        return;
+    }
+    const int scale = -(w.scalars->ek + (SPLIT ? w.of_w ? w.scalars->ew : w.scalars->ex : 0));
+    O* const out = (O*)w.out;
+#pragma unroll
+    for (int x = 0; x < FM; ++x) {
+        const int64_t i = i0 + tile.row_of(x);
+        if (i >= c.m) continue;
+#pragma unroll
+        for (int y = 0; y < FN; ++y) {
+            const int64_t j = j0 + tile.col_of(y);
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = ldexpf(tile.acc[x][y][e], scale);
+            O* const to = out + i * w.out_ld + j;
+            if (j + 4 <= c.n) {
+                store_v<O, 4>(to, v);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (j + e < c.n) to[e] = (O)v[e];
+            }
+        }
+    }
+}
+
+// out = the splits' sums (zeros where there are none), scaled and rounded.  HBM
+// bounds it.
+template <class O>
+__global__ __launch_bounds__(256) void k_ce_gather(const float* parts, int splits, int64_t rows,
+                                                   int64_t ld, int64_t cols, const CeScalars* sc,
+                                                   int use_w, int use_x, O* out, int64_t out_ld) {
+    const int64_t quads = ld / 4, all = rows * quads;
+    const int scale =
+        splits == 0 ? 0 : -(sc->ek + (use_w ? sc->ew : 0) + (use_x ? sc->ex : 0));
+    for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < all;
+         q += (int64_t)gridDim.x * 256) {
+        const int64_t i = q / quads, j = q % quads * 4;
+        if (j >= cols) continue;
+        double s[4] = {};
+        for (int k = 0; k < splits; ++k) {
+            const float4v p = *(const float4v*)(parts + ((int64_t)k * rows + i) * ld + j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] += (double)p[e];
+        }
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = ldexpf((float)s[e], scale);
+        O* const to = out + i * out_ld + j;
+        if (j + 4 <= cols) {
+            store_v<O, 4>(to, v);
+        } else {
+            for (int e = 0; j + e < cols; ++e) to[e] = (O)v[e];
+        }
+    }
+}
+
+// ------------------------------------------------------------- operands ---
+
+constexpr int kAmaxParts = 512;
+
+// The largest finite magnitude that each block meets, as its bits.  Row 0 of
+// the grid takes x, but for the rows that are ignored, row 1 W.
+__global__ __launch_bounds__(256) void k_ce_amax(const float* x, int64_t x_ld, int64_t rows,
+                                                 const int64_t* targets, int64_t ignored,
+                                                 const float* w, int64_t w_ld, int64_t classes,
+                                                 int64_t cols, uint32_t* parts) {
+    __shared__ uint32_t lds[4];
+    const bool of_w = blockIdx.y == 1;
+    const float* a = of_w ? w : x;
+    const int64_t ld = of_w ? w_ld : x_ld, n = of_w ? classes : rows;
+    uint32_t top = 0;
+    auto take = [&](float v) {
+        const uint32_t u = __builtin_bit_cast(uint32_t, v) & 0x7fffffffu;
+        if (u < 0x7f800000u && u > top) top = u;
+    };
+    const int64_t chunks = (cols + 3) / 4, all = n * chunks;
+    for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < all;
+         q += (int64_t)gridDim.x * 256) {
+        const int64_t r = q / chunks, j = q % chunks * 4;
+        if (!of_w && targets[r] == ignored) continue;
+        const float* p = a + r * ld + j;
+        if (j + 4 <= cols) {
+            float v[4];
+            load_v<float, 4>(p, v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) take(v[e]);
+        } else {
+            for (int e = 0; j + e < cols; ++e) take(p[e]);
+        }
+    }
+#pragma unroll
+    for (int off = kWave / 2; off; off >>= 1) {
+        const uint32_t o = (uint32_t)__shfl_xor((int)top, off, kWave);
+        top = o > top ? o : top;
+    }
+    if (lane_id() == 0) lds[threadIdx.x >> 6] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int k = 1; k < 4; ++k) top = lds[k] > top ? lds[k] : top;
+        parts[blockIdx.y * kAmaxParts + blockIdx.x] = top;
+    }
+}
+
+// A copy of an operand as the products take it: rows_p rows of cols_p columns
+// (a multiple of 64), zeros beyond the matrix and in rows that do not count.
+// float32: scaled by 2^e and split; `amax` holds the blocks' shares of the
+// largest value, and block 0 leaves e in *exponent.
+template <class S, class T>
+__global__ __launch_bounds__(256) void k_ce_pack(const S* a, int64_t ld, int64_t rows,
+                                                 int64_t cols, int64_t rows_p, int64_t cols_p,
+                                                 const int64_t* targets, int64_t ignored,
+                                                 const uint32_t* amax, int n_amax, int* exponent,
+                                                 T* out) {
+    constexpr bool kSplit = std::is_same_v<S, float>;
+    int ex = 0;
+    if constexpr (kSplit) {
+        __shared__ uint32_t lds[4];
+        uint32_t top = 0;
+        for (int k = threadIdx.x; k < n_amax; k += 256) top = amax[k] > top ? amax[k] : top;
+#pragma unroll
+        for (int off = kWave / 2; off; off >>= 1) {
+            const uint32_t o = (uint32_t)__shfl_xor((int)top, off, kWave);
+            top = o > top ? o : top;
+        }
+        if (lane_id() == 0) lds[threadIdx.x >> 6] = top;
+        __syncthreads();
+        for (int k = 0; k < 4; ++k) top = lds[k] > top ? lds[k] : top;
+        if (top != 0) {
+            frexpf(__builtin_bit_cast(float, top), &ex);  // |a| < 2^ex
+            ex = 15 - ex;
+        }
+        if (blockIdx.x == 0 && threadIdx.x == 0) *exponent = ex;
+    }
+    const int64_t chunks = cols_p / 8, all = rows_p * chunks;
+    for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < all;
+         q += (int64_t)gridDim.x * 256) {
+        const int64_t r = q / chunks, j = q % chunks * 8;
+        float v[8] = {};
+        if (r < rows && j < cols && (targets == nullptr || targets[r] != ignored)) {
+            const S* p = a + r * ld + j;
+            if (j + 8 <= cols) {
+                load_v<S, 8>(p, v);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (j + e < cols) v[e] = (float)p[e];
+            }
+        }
+        if constexpr (kSplit) {
+            float lo[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[e] = ldexpf(v[e], ex);
+                lo[e] = v[e] - (float)(T)v[e];
+            }
+            T* to = out + r * 2 * cols_p + j / 32 * 64 + j % 32;
+            store_v<T, 8>(to, v);
+            store_v<T, 8>(to + 32, lo);
+        } else {
+            store_v<T, 8>(out + r * cols_p + j, v);
+        }
+    }
+}
+
+// ------------------------------------------------------ joins and sums ---
+
+__device__ __forceinline__ double ce_block_sum(double v, double* lds) {
+#pragma unroll
+    for (int off = kWave / 2; off; off >>= 1) v += __shfl_xor(v, off, kWave);
+    __syncthreads();
+    if (lane_id() == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    double s = 0.;
+    for (int i = 0; i < (int)(blockDim.x >> 6); ++i) s += lds[i];
+    return s;
+}
+
+enum : int { kCeNone = SPOPT_REDUCE_NONE, kCeSum = SPOPT_REDUCE_SUM, kCeMean = SPOPT_REDUCE_MEAN };
+
+// lse and loss of each row from its tiles' pairs: `per` rows (a power of two, up
+// to 64) of a block's 1024 threads, the tiles shared out to 1024 / per of them.
+// A block that has all rows sums their losses itself.
+__global__ __launch_bounds__(1024) void k_ce_join(const float2* parts, const float* sums,
+                                                  const float* at_target, const int64_t* targets,
+                                                  int64_t ignored, int64_t rows, int64_t tiles,
+                                                  int64_t classes, float smoothing, int per,
+                                                  int reduction, float* row_loss, float* loss,
+                                                  float* lse) {
+    __shared__ float tops[1024];
+    __shared__ double both[2][1024];
+    const int t = threadIdx.x, slices = 1024 / per;
+    const int64_t i = (int64_t)blockIdx.x * per + t % per;
+    float top = -INFINITY;
+    double s = 0., z = 0.;
+    auto add = [&](float m, double v) {
+        const float next = fmaxf(top, m);
+        if (top != next) s *= (double)__expf(top - next);
+        s += m == next ? v : v * (double)__expf(m - next);
+        top = next;
+    };
+    if (i < rows) {
+        int64_t k = t / per;
+        for (; k + 3 * slices < tiles; k += 4 * slices) {
+            float2 p[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) p[u] = parts[(k + u * slices) * rows + i];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) add(p[u].x, p[u].y);
+        }
+        for (; k < tiles; k += slices) {
+            const float2 p = parts[k * rows + i];
+            add(p.x, p.y);
+        }
+        if (sums)
+            for (k = t / per; k < tiles; k += slices) z += (double)sums[k * rows + i];
+    }
+    for (int off = slices / 2; off; off >>= 1) {
+        tops[t] = top;
+        both[0][t] = s;
+        both[1][t] = z;
+        __syncthreads();
+        if (t < off * per) {
+            add(tops[t + off * per], both[0][t + off * per]);
+            z += both[1][t + off * per];
+        }
+        __syncthreads();
+    }
+    double own = 0.;
+    bool valid = false;
+    if (t < per && i < rows) {
+        const double l = (double)top + log(s);
+        const int64_t goal = targets[i];
+        valid = goal != ignored;
+        if (valid) {
+            own = goal < 0 || goal >= classes
+                      ? (double)NAN
+                      : l - (1. - (double)smoothing) * (double)at_target[i] -
+                            (double)smoothing * (z / (double)classes);
+        }
+        lse[i] = valid ? (float)l : 0.f;
+        if (reduction == kCeNone)
+            loss[i] = (float)own;
+        else
+            row_loss[i] = (float)own;
+    }
+    if (reduction == kCeNone || gridDim.x != 1) return;
+    const double sum = ce_block_sum(own, both[0]);
+    const double count = ce_block_sum(valid ? 1. : 0., both[1]);
+    if (t == 0) *loss = (float)(reduction == kCeMean ? sum / fmax(count, 1.) : sum);
+}
+
+// The rows' losses as one, by one block.
+__global__ __launch_bounds__(1024) void k_ce_reduce(const float* row_loss, const int64_t* targets,
+                                                    int64_t ignored, int64_t rows, int reduction,
+                                                    float* loss) {
+    __shared__ double lds[16];
+    double s = 0., n = 0.;
+    for (int64_t i = threadIdx.x; i < rows; i += 1024) {
+        s += (double)row_loss[i];
+        n += targets[i] != ignored ? 1. : 0.;
+    }
+    s = ce_block_sum(s, lds);
+    n = ce_block_sum(n, lds);
+    if (threadIdx.x == 0) *loss = (float)(reduction == kCeMean ? s / fmax(n, 1.) : s);
+}
+
+// Each row's factor in front of its gradient, times the power of two that
+// brings the largest to [2^13, 2^14); zero for rows that are ignored and beyond
+// the last, NaN for a target outside the classes.  One block.
+__global__ __launch_bounds__(1024) void k_ce_coef(const float* dloss, const int64_t* targets,
+                                                  int64_t ignored, int64_t rows, int64_t rows_p,
+                                                  int64_t classes, int reduction, float* coef,
+                                                  CeScalars* scalars) {
+    __shared__ double lds[16];
+    __shared__ float top_of[16];
+    const int t = threadIdx.x;
+    double n = 0.;
+    float top = 0.f;
+    for (int64_t i = t; i < rows; i += 1024) {
+        if (targets[i] == ignored) continue;
+        n += 1.;
+        if (reduction == kCeNone && finite_f(dloss[i])) top = fmaxf(top, fabsf(dloss[i]));
+    }
+    n = ce_block_sum(n, lds);
+#pragma unroll
+    for (int off = kWave / 2; off; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, kWave));
+    if (lane_id() == 0) top_of[t >> 6] = top;
+    __syncthreads();
+    for (int k = 0; k < 16; ++k) top = fmaxf(top, top_of[k]);
+    const float one = reduction == kCeNone  ? 0.f
+                      : reduction == kCeSum ? dloss[0]
+                                            : (float)((double)dloss[0] / fmax(n, 1.));
+    if (reduction != kCeNone) top = fabsf(one);
+    int ek = 0;
+    if (top > 0.f && finite_f(top)) {
+        frexpf(top, &ek);
+        ek = 14 - ek;
+    }
+    if (t == 0) scalars->ek = ek;
+    for (int64_t i = t; i < rows_p; i += 1024) {
+        float c = 0.f;
+        if (i < rows && targets[i] != ignored) {
+            c = ldexpf(reduction == kCeNone ? dloss[i] : one, ek);
+            if (targets[i] < 0 || targets[i] >= classes) c = NAN;
+        }
+        coef[i] = c;
+    }
+}
+
+// Sets kStatusRange for a target that is neither ignored nor a class, and
+// kStatusNonFinite where a row that counts holds a NaN or an infinity.
+template <class T>
+__global__ __launch_bounds__(256) void k_ce_check(const T* x, int64_t ld, int64_t rows,
+                                                  int64_t cols, const int64_t* targets,
+                                                  int64_t ignored, int64_t classes,
+                                                  uint32_t* status) {
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const int64_t t = targets[r];
+        if (t == ignored) continue;
+        uint32_t bad = t < 0 || t >= classes ? kStatusRange : 0u;
+        for (int64_t c = threadIdx.x; c < cols; c += 256)
+            if (!finite_f((float)x[r * ld + c])) bad |= kStatusNonFinite;
+        if (bad) atomicOr(status, bad);
+    }
+}
+
+// ------------------------------------------------------------------ host ---
+
+typedef Tiling<64, 64, 2, 2, 2> CeS;
+typedef Tiling<128, 128, 2, 4, 2> CeM;
+typedef Tiling<256, 256, 2, 4, 2> CeL;
+
+// How a product is tiled, and into how many parts its inner axis is cut.
+struct CePlan {
+    int tile;    // 64, 128 or 256
+    int splits;
+};
+
+// An inner step takes a tile of 64, 128 and 256 about 0.2, 0.5 and 1.8 us of its
+// CU.  Cut products write and read their parts once more, 5 bytes a picosecond.
+static CePlan ce_plan(int64_t m, int64_t n, int64_t steps, bool cut) {
+    CePlan best{64, 1};
+    double least = INFINITY;
+    const struct { int b; double us; } kind[3] = {{64, 0.2}, {128, 0.5}, {256, 1.8}};
+    for (const auto& k : kind) {
+        const int64_t tiles = ceil_div(m, k.b) * ceil_div(n, k.b);
+        for (int s = 1; s <= (cut ? 32 : 1); s *= 2) {
+            if (s > 1 && steps < 4 * s) break;
+            if (tiles * s > (1 << 22) && !(k.b == 256 && s == 1)) continue;
+            const double us = (double)ceil_div(tiles * s, 256) * (double)(ceil_div(steps, s) + 2) *
+                                  k.us +
+                              (s > 1 ? 3. + (double)s * (double)m * (double)n * 8. / 5e6 : 0.);
+            if (us < least) {
+                least = us;
+                best = CePlan{k.b, s};
+            }
+        }
+    }
+    return best;
+}
+
+struct CeShape {
+    int64_t rows, cols, classes;
+    int32_t dtype;
+    bool split;
+    int64_t cols_p;     // columns of a packed operand
+    int64_t rows_p;     // rows of g and of x's copy
+    int64_t value;      // 16-bit values that a value takes in a packed operand
+};
+
+static CeShape ce_shape(int64_t rows, int64_t cols, int64_t classes, int32_t dtype) {
+    CeShape s{rows, cols, classes, dtype, dtype == SPOPT_DTYPE_F32, 0, 0, 1};
+    s.cols_p = ceil_div(cols, 64) * 64;
+    s.rows_p = ceil_div(rows, 64) * 64;
+    s.value = s.split ? 2 : 1;
+    return s;
+}
+
+// Classes at a time.  Forward: copies of W's rows of up to 256 MiB, and grids of
+// up to 2^22 tiles.  Backward: g of up to 512 MiB, for at least 2048 classes.
+static int64_t ce_piece(const CeShape& s, bool backward) {
+    int64_t most = ((int64_t)1 << 28) / (s.cols_p * s.value * 2);
+    if (backward) {
+        const int64_t g = ((int64_t)1 << 29) / (s.rows_p * s.value * 2);
+        most = most < g ? most : g;
+    }
+    if (most < 2048) most = 2048;
+    const int64_t tiles = ((int64_t)1 << 22) / ceil_div(s.rows, 256);
+    if (most > tiles * 256) most = tiles * 256;
+    most = most / 256 * 256;
+    const int64_t all = ceil_div(s.classes, 256) * 256;
+    if (most >= all) return all;
+    return ceil_div(ceil_div(all, ceil_div(all, most)), 256) * 256;  // pieces alike
+}
+
+struct CeBuffers {
+    CeScalars* scalars;
+    uint32_t* amax;
+    void* x;            // x's copy
+    void* w;            // a piece of W's copy
+    // forward
+    float2* parts;
+    float* sums;
+    float* at_target;
+    float* row_loss;
+    // backward
+    float* coef;
+    void* g;
+    float* dx_parts;
+    float* dw_parts;
+};
+
+struct CeRun {
+    CeShape s;
+    int64_t piece;
+    CePlan logits, dx, dw;
+    int64_t tiles;       // of classes, in the forward pass
+};
+
+static CeRun ce_run(const CeShape& s, bool backward) {
+    CeRun r{};
+    r.s = s;
+    r.piece = ce_piece(s, backward);
+    const int64_t inner = s.split ? 32 : 64;
+    const int64_t first = s.classes < r.piece ? s.classes : r.piece;
+    r.logits = ce_plan(s.rows, first, s.cols_p / inner, false);
+    r.tiles = 0;
+    for (int64_t v = 0; v < s.classes; v += r.piece) {
+        const int64_t n = s.classes - v < r.piece ? s.classes - v : r.piece;
+        r.tiles += ceil_div(n, r.logits.tile);
+    }
+    if (backward) {
+        r.dx = ce_plan(s.rows, s.cols, ceil_div(first, inner), true);
+        r.dw = ce_plan(first, s.cols, ceil_div(s.rows, inner), true);
+    }
+    return r;
+}
+
+static size_t ce_layout(const CeRun& r, bool backward, char* base, CeBuffers* b) {
+    const CeShape& s = r.s;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        char* p = base + at;
+        at += align_up(bytes, 256);
+        return (void*)p;
+    };
+    b->scalars = (CeScalars*)take(sizeof(CeScalars));
+    b->amax = (uint32_t*)take(2 * kAmaxParts * 4);
+    b->x = take((size_t)(s.rows_p * s.cols_p * s.value) * 2);
+    b->w = take((size_t)(r.piece * s.cols_p * s.value) * 2);
+    if (!backward) {
+        b->parts = (float2*)take((size_t)(r.tiles * s.rows) * 8);
+        b->sums = (float*)take((size_t)(r.tiles * s.rows) * 4);
+        b->at_target = (float*)take((size_t)s.rows * 4);
+        b->row_loss = (float*)take((size_t)s.rows * 4);
+        return at;
+    }
+    b->coef = (float*)take((size_t)s.rows_p * 4);
+    b->g = take((size_t)(s.rows_p * r.piece * s.value) * 2);
+    b->dx_parts = (float*)take((size_t)(r.dx.splits * s.rows * s.cols_p) * 4);
+    b->dw_parts = (float*)take(
+        r.dw.splits > 1 ? (size_t)(r.dw.splits * r.piece * s.cols_p) * 4 : 0);
+    return at;
+}
+
+static int ce_check_size(const char* what, int64_t rows, int64_t cols, int64_t classes,
+                         int32_t dtype) {
+    if (dtype != SPOPT_DTYPE_F32 && dtype != SPOPT_DTYPE_BF16 && dtype != SPOPT_DTYPE_F16)
+        return fail(SPOPT_EINVAL, "%s: unknown element type %d", what, dtype);
+    constexpr int64_t kMost = (int64_t)1 << 38;
+    if (rows < 0 || cols < 1 || classes < 1 || rows > (1 << 28) || cols > (1 << 20) ||
+        classes > (1 << 30) || rows > kMost / cols || classes > kMost / cols)
+        return fail(SPOPT_EINVAL, "%s: bad size %lld x %lld for %lld classes", what,
+                    (long long)rows, (long long)cols, (long long)classes);
+    return SPOPT_OK;
+}
+
+template <class F>
+static void ce_types(int32_t dtype, F&& f) {
+    if (dtype == SPOPT_DTYPE_F32)
+        f(_Float16{}, std::true_type{});
+    else if (dtype == SPOPT_DTYPE_F16)
+        f(_Float16{}, std::false_type{});
+    else
+        f(__bf16{}, std::false_type{});
+}
+
+template <class F>
+static void ce_tilings(int tile, F&& f) {
+    if (tile == 64)
+        f(CeS{});
+    else if (tile == 128)
+        f(CeM{});
+    else
+        f(CeL{});
+}
+
+template <class K, class TL, class... A>
+static int ce_launch(K kernel, TL, int64_t blocks, hipStream_t s, const A&... a) {
+    constexpr int bytes = TL::STAGES * TL::kStage * 2;
+    if constexpr (bytes > 64 * 1024) {
+        SPOPT_HIP(hipFuncSetAttribute((const void*)kernel,
+                                      hipFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    }
+    kernel<<<(unsigned)blocks, TL::kThreads, bytes, s>>>(a...);
+    SPOPT_LAUNCHED();
+    return SPOPT_OK;
+}
+
+template <int MODE>
+static int ce_logits(const CeRun& r, CeProduct c, const CeLogits& w, hipStream_t s) {
+    int rc = SPOPT_OK;
+    c.splits = 1;
+    c.tiles_m = ceil_div(c.m, r.logits.tile);
+    // g's columns beyond the piece's last class are written too, as zeros.
+    c.tiles_n = ceil_div(MODE == kCeGrad ? w.cols_p : c.n, r.logits.tile);
+    ce_types(r.s.dtype, [&](auto t, auto split) {
+        ce_tilings(r.logits.tile, [&](auto tl) {
+            rc = ce_launch(k_ce_logits<decltype(t), decltype(split)::value, MODE, decltype(tl)>,
+                           tl, c.tiles_m * c.tiles_n, s, c, w);
+        });
+    });
+    return rc;
+}
+
+template <int MODE>
+static int ce_product(const CeRun& r, const CePlan& plan, CeProduct c, const CeResult& w,
+                      hipStream_t s) {
+    int rc = SPOPT_OK;
+    c.splits = plan.splits;
+    c.tiles_m = ceil_div(c.m, plan.tile);
+    c.tiles_n = ceil_div(c.n, plan.tile);
+    ce_types(r.s.dtype, [&](auto t, auto split) {
+        ce_tilings(plan.tile, [&](auto tl) {
+            rc = ce_launch(k_ce_product<decltype(t), decltype(split)::value, MODE, decltype(tl)>,
+                           tl, c.tiles_m * c.tiles_n * c.splits, s, c, w);
+        });
+    });
+    return rc;
+}
+
+static unsigned ce_grid(int64_t items) {
+    const int64_t b = ceil_div(items, 256);
+    return (unsigned)(b < 1 ? 1 : b < 8192 ? b : 8192);
+}
+
+// An operand as the products take it: in place where it can be read 16 bytes at
+// a time without a remainder, else a copy in `to`.
+static int ce_operand(const CeShape& s, const void* a, int64_t ld, int64_t rows, int64_t rows_p,
+                      bool copy, const int64_t* targets, int64_t ignored, const uint32_t* amax,
+                      int n_amax, int* exponent, void* to, CeOperand* o, hipStream_t stream) {
+    if (!copy && !s.split && s.cols % 64 == 0 && ld % 8 == 0 && aligned16(a)) {
+        *o = CeOperand{a, ld, rows - 1, s.cols_p};
+        return SPOPT_OK;
+    }
+    const unsigned grid = ce_grid(rows_p * s.cols_p / 8);
+    if (s.split)
+        k_ce_pack<float, _Float16><<<grid, 256, 0, stream>>>(
+            (const float*)a, ld, rows, s.cols, rows_p, s.cols_p, targets, ignored, amax, n_amax,
+            exponent, (_Float16*)to);
+    else if (s.dtype == SPOPT_DTYPE_F16)
+        k_ce_pack<_Float16, _Float16><<<grid, 256, 0, stream>>>(
+            (const _Float16*)a, ld, rows, s.cols, rows_p, s.cols_p, targets, ignored, nullptr, 0,
+            nullptr, (_Float16*)to);
+    else
+        k_ce_pack<__bf16, __bf16><<<grid, 256, 0, stream>>>(
+            (const __bf16*)a, ld, rows, s.cols, rows_p, s.cols_p, targets, ignored, nullptr, 0,
+            nullptr, (__bf16*)to);
+    SPOPT_LAUNCHED();
+    *o = CeOperand{to, s.cols_p * s.value, rows_p - 1, s.cols_p};
+    return SPOPT_OK;
+}
+
+static int ce_amax(const CeShape& s, const void* x, int64_t x_ld, const int64_t* targets,
+                   int64_t ignored, const void* w, int64_t w_ld, const CeBuffers& b, int* parts,
+                   hipStream_t stream) {
+    *parts = 0;
+    if (!s.split) return SPOPT_OK;
+    const int64_t values = (s.classes > s.rows ? s.classes : s.rows) * s.cols;
+    int64_t n = ceil_div(values, 256 * 16);
+    if (n > kAmaxParts) n = kAmaxParts;
+    k_ce_amax<<<dim3((unsigned)n, 2), 256, 0, stream>>>((const float*)x, x_ld, s.rows, targets,
+                                                        ignored, (const float*)w, w_ld, s.classes,
+                                                        s.cols, b.amax);
+    SPOPT_LAUNCHED();
+    *parts = (int)n;
+    return SPOPT_OK;
+}
+
+// What both passes check alike.
+static int ce_enter(const char* what, const CeShape& s, const void* x, int64_t x_ld,
+                    const void* w, int64_t w_ld, const int64_t* targets, double smoothing,
+                    int32_t reduction) {
+    if (!(smoothing >= 0.0 && smoothing <= 1.0))
+        return fail(SPOPT_EINVAL, "%s: label smoothing must lie in [0, 1]", what);
+    if (reduction != SPOPT_REDUCE_NONE && reduction != SPOPT_REDUCE_SUM &&
+        reduction != SPOPT_REDUCE_MEAN)
+        return fail(SPOPT_EINVAL, "%s: unknown reduction %d", what, reduction);
+    if (s.rows > 0 && (x == nullptr || targets == nullptr))
+        return fail(SPOPT_EINVAL, "%s: NULL x or targets", what);
+    if (w == nullptr) return fail(SPOPT_EINVAL, "%s: NULL weight", what);
+    if ((s.rows > 1 && x_ld < s.cols) || (s.classes > 1 && w_ld < s.cols))
+        return fail(SPOPT_EINVAL, "%s: a row stride below cols", what);
+    return SPOPT_OK;
+}
+
+static int ce_validate(const char* what, const CeShape& s, const void* x, int64_t x_ld,
+                       const void* w, int64_t w_ld, const int64_t* targets, int64_t ignored,
+                       hipStream_t stream) {
+    return validate_on_device(stream, false, what, [&](uint32_t* status) {
+        const unsigned grid = (unsigned)(s.rows < 4096 ? s.rows : 4096);
+        auto check = [&](auto t) {
+            using S = decltype(t);
+            k_ce_check<S><<<grid, 256, 0, stream>>>((const S*)x, x_ld, s.rows, s.cols, targets,
+                                                    ignored, s.classes, status);
+        };
+        if (s.dtype == SPOPT_DTYPE_F32)
+            check(float{});
+        else if (s.dtype == SPOPT_DTYPE_F16)
+            check(_Float16{});
+        else
+            check(__bf16{});
+        SPOPT_LAUNCHED();
+        return launch_check_finite(w, s.dtype, s.classes, s.cols, w_ld, status, stream);
+    });
+}
+
+static int ce_workspace(const char* what, const void* workspace, size_t have, size_t need) {
+    if (need != 0 && (workspace == nullptr || !aligned16(workspace) || have < need))
+        return fail(SPOPT_EWORKSPACE, "%s: workspace of %zu bytes, needs %zu", what, have, need);
+    return SPOPT_OK;
+}
+
+}  // namespace spopt
+
+using namespace spopt;
+
+extern "C" int linear_cross_entropy_workspace_size(int64_t rows, int64_t cols, int64_t classes,
+                                                   int32_t dtype, int32_t backward,
+                                                   size_t* bytes) {
+    const char* what = "linear_cross_entropy_workspace_size";
+    if (bytes == nullptr) return fail(SPOPT_EINVAL, "%s: NULL output", what);
+    int rc = ce_check_size(what, rows, cols, classes, dtype);
+    if (rc) return rc;
+    *bytes = 0;
+    if (rows == 0) return SPOPT_OK;
+    CeBuffers b;
+    *bytes = ce_layout(ce_run(ce_shape(rows, cols, classes, dtype), backward != 0), backward != 0,
+                       nullptr, &b);
+    return SPOPT_OK;
+}
+
+extern "C" int linear_cross_entropy_forward(const void* x, int64_t x_stride, const void* weight,
+                                            int64_t weight_stride, int64_t rows, int64_t cols,
+                                            int64_t classes, int32_t dtype,
+                                            const int64_t* targets, int64_t ignore_index,
+                                            double label_smoothing, int32_t reduction, float* loss,
+                                            float* lse, void* workspace, size_t workspace_bytes,
+                                            void* stream, uint32_t flags) {
+    const char* what = "linear_cross_entropy_forward";
+    hipStream_t s = (hipStream_t)stream;
+    int rc = ce_check_size(what, rows, cols, classes, dtype);
+    if (rc) return rc;
+    const CeShape sh = ce_shape(rows, cols, classes, dtype);
+    rc = ce_enter(what, sh, x, x_stride, weight, weight_stride, targets, label_smoothing,
+                  reduction);
+    if (rc) return rc;
+    if ((loss == nullptr && (rows > 0 || reduction != SPOPT_REDUCE_NONE)) ||
+        (lse == nullptr && rows > 0))
+        return fail(SPOPT_EINVAL, "%s: NULL loss or lse", what);
+    if (rows == 0) {
+        if (reduction != SPOPT_REDUCE_NONE)
+            k_ce_reduce<<<1, 1024, 0, s>>>(nullptr, nullptr, ignore_index, 0, reduction, loss);
+        SPOPT_LAUNCHED();
+        return SPOPT_OK;
+    }
+    const CeRun r = ce_run(sh, false);
+    CeBuffers b;
+    rc = ce_workspace(what, workspace, workspace_bytes, ce_layout(r, false, (char*)workspace, &b));
+    if (rc) return rc;
+    if (flags & SPOPT_VALIDATE) {
+        rc = ce_validate(what, sh, x, x_stride, weight, weight_stride, targets, ignore_index, s);
+        if (rc) return rc;
+    }
+    int amax = 0;
+    rc = ce_amax(sh, x, x_stride, targets, ignore_index, weight, weight_stride, b, &amax, s);
+    if (rc) return rc;
+    CeProduct c{};
+    c.m = rows;
+    c.steps = sh.cols_p / (sh.split ? 32 : 64);
+    rc = ce_operand(sh, x, x_stride, rows, rows, false, targets, ignore_index, b.amax, amax,
+                    &b.scalars->ex, b.x, &c.p, s);
+    if (rc) return rc;
+    CeLogits w{};
+    w.scalars = b.scalars;
+    w.targets = targets;
+    w.classes = classes;
+    w.smoothing = (float)label_smoothing;
+    w.parts = b.parts;
+    w.sums = label_smoothing != 0.0 ? b.sums : nullptr;
+    w.at_target = b.at_target;
+    for (int64_t v = 0; v < classes; v += r.piece) {
+        c.n = classes - v < r.piece ? classes - v : r.piece;
+        w.first = v;
+        rc = ce_operand(sh, (const char*)weight + (size_t)(v * weight_stride) * dtype_bytes(dtype),
+                        weight_stride, c.n, c.n, false, nullptr, 0, b.amax + kAmaxParts, amax,
+                        &b.scalars->ew, b.w, &c.q, s);
+        if (!rc) rc = ce_logits<kCeLoss>(r, c, w, s);
+        if (rc) return rc;
+        w.first_tile += ceil_div(c.n, r.logits.tile);
+    }
+    int per = 64;
+    while (per > 1 && ceil_div(rows, per) < 128 && rows <= per / 2) per /= 2;
+    k_ce_join<<<(unsigned)ceil_div(rows, per), 1024, 0, s>>>(
+        b.parts, w.sums, b.at_target, targets, ignore_index, rows, r.tiles, classes,
+        w.smoothing, per, reduction, b.row_loss, loss, lse);
+    SPOPT_LAUNCHED();
+    if (reduction != SPOPT_REDUCE_NONE && rows > per) {
+        k_ce_reduce<<<1, 1024, 0, s>>>(b.row_loss, targets, ignore_index, rows, reduction, loss);
+        SPOPT_LAUNCHED();
+    }
+    return SPOPT_OK;
+}
+
+extern "C" int linear_cross_entropy_backward(
+    const float* dloss, const void* x, int64_t x_stride, const void* weight, int64_t weight_stride,
+    int64_t rows, int64_t cols, int64_t classes, int32_t dtype, const int64_t* targets,
+    int64_t ignore_index, double label_smoothing, int32_t reduction, const float* lse, void* dx,
+    int64_t dx_stride, void* dweight, int64_t dweight_stride, void* workspace,
+    size_t workspace_bytes, void* stream, uint32_t flags) {
+    const char* what = "linear_cross_entropy_backward";
+    hipStream_t s = (hipStream_t)stream;
+    int rc = ce_check_size(what, rows, cols, classes, dtype);
+    if (rc) return rc;
+    const CeShape sh = ce_shape(rows, cols, classes, dtype);
+    rc = ce_enter(what, sh, x, x_stride, weight, weight_stride, targets, label_smoothing,
+                  reduction);
+    if (rc) return rc;
+    if (rows > 0 && (dloss == nullptr || lse == nullptr))
+        return fail(SPOPT_EINVAL, "%s: NULL dloss or lse", what);
+    if ((dx != nullptr && rows > 1 && dx_stride < cols) ||
+        (dweight != nullptr && classes > 1 && dweight_stride < cols))
+        return fail(SPOPT_EINVAL, "%s: a row stride below cols", what);
+    if (dx == nullptr && dweight == nullptr) return SPOPT_OK;
+    // The splits' sums of an operand's gradient, to where it belongs.
+    auto gather = [&](const float* parts, const CeScalars* sc, int splits, int64_t n, bool of_w,
+                      void* out, int64_t ld) {
+        const unsigned grid = ce_grid(n * (sh.cols_p / 4));
+        const int uw = sh.split && of_w, ux = sh.split && !of_w;
+        if (dtype == SPOPT_DTYPE_F32)
+            k_ce_gather<<<grid, 256, 0, s>>>(parts, splits, n, sh.cols_p, cols, sc, uw, ux,
+                                             (float*)out, ld);
+        else if (dtype == SPOPT_DTYPE_F16)
+            k_ce_gather<<<grid, 256, 0, s>>>(parts, splits, n, sh.cols_p, cols, sc, uw, ux,
+                                             (_Float16*)out, ld);
+        else
+            k_ce_gather<<<grid, 256, 0, s>>>(parts, splits, n, sh.cols_p, cols, sc, uw, ux,
+                                             (__bf16*)out, ld);
+    };
+    if (rows == 0) {
+        if (dweight != nullptr)
+            gather(nullptr, nullptr, 0, classes, false, dweight, dweight_stride);
+        SPOPT_LAUNCHED();
+        return SPOPT_OK;
+    }
+    const CeRun r = ce_run(sh, true);
+    CeBuffers b;
+    rc = ce_workspace(what, workspace, workspace_bytes, ce_layout(r, true, (char*)workspace, &b));
+    if (rc) return rc;
+    if (flags & SPOPT_VALIDATE) {
+        rc = ce_validate(what, sh, x, x_stride, weight, weight_stride, targets, ignore_index, s);
+        if (rc) return rc;
+    }
+    int amax = 0;
+    rc = ce_amax(sh, x, x_stride, targets, ignore_index, weight, weight_stride, b, &amax, s);
+    if (rc) return rc;
+    k_ce_coef<<<1, 1024, 0, s>>>(dloss, targets, ignore_index, rows, sh.rows_p, classes, reduction,
+                                 b.coef, b.scalars);
+    SPOPT_LAUNCHED();
+    // x is copied for its rows that are ignored: they may hold anything, and meet
+    // g's zeros in dW.
+    CeOperand xo{}, wo{}, g{};
+    rc = ce_operand(sh, x, x_stride, rows, sh.rows_p, true, targets, ignore_index, b.amax, amax,
+                    &b.scalars->ex, b.x, &xo, s);
+    if (rc) return rc;
+    const int64_t inner = sh.split ? 32 : 64;
+    for (int64_t v = 0; v < classes; v += r.piece) {
+        const int64_t n = classes - v < r.piece ? classes - v : r.piece;
+        const int64_t n_p = ceil_div(n, 64) * 64, ldg = n_p * sh.value;
+        rc = ce_operand(sh, (const char*)weight + (size_t)(v * weight_stride) * dtype_bytes(dtype),
+                        weight_stride, n, n, false, nullptr, 0, b.amax + kAmaxParts, amax,
+                        &b.scalars->ew, b.w, &wo, s);
+        if (rc) return rc;
+        CeProduct c{};
+        c.p = xo;
+        c.q = wo;
+        c.m = rows;
+        c.n = n;
+        c.steps = sh.cols_p / inner;
+        CeLogits w{};
+        w.scalars = b.scalars;
+        w.targets = targets;
+        w.first = v;
+        w.classes = classes;
+        w.smoothing = (float)label_smoothing;
+        w.lse = lse;
+        w.coef = b.coef;
+        w.g = b.g;
+        w.ldg = ldg;
+        w.rows_p = sh.rows_p;
+        w.cols_p = n_p;
+        rc = ce_logits<kCeGrad>(r, c, w, s);
+        if (rc) return rc;
+        g = CeOperand{b.g, ldg, sh.rows_p - 1, n_p};
+        CeResult o{};
+        o.scalars = b.scalars;
+        if (dx != nullptr) {
+            c.p = g;
+            c.q = wo;
+            c.m = rows;
+            c.n = cols;
+            c.steps = n_p / inner;
+            o.of_w = 1;
+            o.out = dx;
+            o.out_ld = dx_stride;
+            o.ld = sh.cols_p;
+            o.add = v > 0;
+            o.parts = r.dx.splits == 1 && r.piece >= classes ? nullptr : b.dx_parts;
+            rc = ce_product<kCeDx>(r, r.dx, c, o, s);
+            if (rc) return rc;
+        }
+        if (dweight != nullptr) {
+            c.p = g;
+            c.q = xo;
+            c.m = n;
+            c.n = cols;
+            c.steps = sh.rows_p / inner;
+            o.of_w = 0;
+            o.out = (char*)dweight + (size_t)(v * dweight_stride) * dtype_bytes(dtype);
+            o.out_ld = dweight_stride;
+            o.ld = sh.cols_p;
+            o.add = 0;
+            o.parts = r.dw.splits == 1 ? nullptr : b.dw_parts;
+            rc = ce_product<kCeDw>(r, r.dw, c, o, s);
+            if (rc) return rc;
+            if (r.dw.splits > 1) {
+                gather(b.dw_parts, b.scalars, r.dw.splits, n, false, o.out, dweight_stride);
+                SPOPT_LAUNCHED();
+            }
+        }
+    }
+    if (dx != nullptr && (r.dx.splits > 1 || r.piece < classes)) {
+        gather(b.dx_parts, b.scalars, r.dx.splits, rows, true, dx, dx_stride);
+        SPOPT_LAUNCHED();
+    }
+    return SPOPT_OK;
+}

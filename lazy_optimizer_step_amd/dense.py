@@ -1,11 +1,12 @@
-"""The dense operators beside a table's sparse step: layer norm, the Newton-Schulz
+"""The dense operators beside a table's sparse step: layer norm, dropout, the Newton-Schulz
 orthogonalisation and the Muon step (include/dense_ops.h).
 
-A training step of the whole runs ``read_rows`` (or ``SparseEmbedding``), layer
-norm and matrices forward, their gradients backward, ``step_lookups`` for the
-table's touched rows and ``muon_step`` for each matrix.  The functions carry the
-C ABI's names and only marshal arguments, as the package's other functions do;
-``LayerNorm`` and ``Muon`` are the module and the optimizer over them.
+A training step of the whole runs ``read_rows`` (or ``SparseEmbedding``), dropout,
+layer norm and matrices forward, the loss (loss.py), their gradients backward,
+``step_lookups`` for the table's touched rows and ``muon_step`` for each matrix.
+The functions carry the C ABI's names and only marshal arguments, as the
+package's other functions do; ``LayerNorm``, ``Dropout`` and ``Muon`` are the
+modules and the optimizer over them.
 """
 from __future__ import annotations
 
@@ -209,6 +210,120 @@ class LayerNorm(torch.nn.Module):
         if x.shape[-1] != self.dim:
             raise ValueError(f"x has {x.shape[-1]} columns, the norm {self.dim}")
         return _LayerNorm.apply(x, self.weight, self.bias, self.eps)
+
+
+# ---------------------------------------------------------------------------
+# Dropout
+# ---------------------------------------------------------------------------
+
+def _seed(seed, x):
+    """(seed, device address of one or None) of a seed given as an int or a device tensor."""
+    if isinstance(seed, torch.Tensor):
+        _need(seed, torch.int64, "seed")
+        if seed.numel() != 1:
+            raise ValueError(f"seed must hold one value, has shape {tuple(seed.shape)}")
+        if seed.device != x.device:
+            raise ValueError(f"seed is on {seed.device}, x on {x.device}")
+        return 0, seed.data_ptr()
+    return int(seed) & 0xFFFFFFFFFFFFFFFF, None
+
+
+def dropout_forward(x: torch.Tensor, p: float, seed, *, offset: int = 0, residual=None, out=None,
+                    stream=None, validate: bool = False) -> torch.Tensor:
+    """y = x / (1 - p) where it is kept, 0 where it is dropped, plus residual.  The mask is a
+    function of (seed, offset) and the value's index and is never stored; dense_ops.h states
+    it.  p counts in steps of 2^-16.  x: float32, bfloat16 or float16, its rows evenly spaced;
+    residual: as x, or None.  seed: an int, or a device int64 tensor of one value that the
+    kernel reads when it runs (a replayed graph then takes what it holds).  out may be x or
+    residual."""
+    rows, cols, xs = _rows(x, "x")
+    rs = ys = cols
+    if residual is not None:
+        _, _, rs = _rows(residual, "residual", x)
+    if out is not None:
+        _, _, ys = _rows(out, "out", x)
+    seed, d_seed = _seed(seed, x)
+    if out is None:
+        with _alloc_on(stream):
+            out = _like(x)
+    check(_lib.lib().dropout_forward(
+        x.data_ptr(), xs, _ptr(residual), rs, rows, cols, _DTYPES[x.dtype], p, seed, d_seed,
+        offset & 0xFFFFFFFFFFFFFFFF, out.data_ptr(), ys, _stream(stream), _flags(validate)))
+    return out
+
+
+def dropout_backward(dy: torch.Tensor, p: float, seed, *, offset: int = 0, out=None, stream=None,
+                     validate: bool = False) -> torch.Tensor:
+    """dx of dropout_forward with the same p, seed and offset (the residual's gradient is dy).
+    out may be dy."""
+    rows, cols, ds = _rows(dy, "dy")
+    os_ = cols
+    if out is not None:
+        _, _, os_ = _rows(out, "out", dy)
+    seed, d_seed = _seed(seed, dy)
+    if out is None:
+        with _alloc_on(stream):
+            out = _like(dy)
+    check(_lib.lib().dropout_backward(
+        dy.data_ptr(), ds, rows, cols, _DTYPES[dy.dtype], p, seed, d_seed,
+        offset & 0xFFFFFFFFFFFFFFFF, out.data_ptr(), os_, _stream(stream), _flags(validate)))
+    return out
+
+
+def _spaced(t):
+    """t, or a copy of it where its rows are not evenly spaced."""
+    try:
+        _rows(t, "t")
+        return t
+    except ValueError:
+        return t.contiguous()
+
+
+class _Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, p, seed, offset):
+        if isinstance(seed, torch.Tensor):
+            # What the caller writes there next belongs to the next mask.
+            seed = seed.clone()
+        ctx.p, ctx.seed, ctx.offset = p, seed, offset
+        return dropout_forward(_spaced(x), p, seed, offset=offset,
+                               residual=None if residual is None else _spaced(residual))
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        dx = None
+        if ctx.needs_input_grad[0]:
+            dx = dropout_backward(_spaced(dy), ctx.p, ctx.seed, offset=ctx.offset)
+        return dx, dy if ctx.needs_input_grad[1] else None, None, None, None
+
+
+class Dropout(torch.nn.Module):
+    """Dropout of probability ``p`` in training, forward and backward in the library's kernels;
+    ``forward(x, residual)`` adds the residual stream in the same pass.
+
+    Each training pass takes the next offset under ``seed``: two modules need two seeds.  The
+    seed is an int, or a device int64 tensor of one value, read when the kernel runs: a pass
+    captured into a graph replays its offset, so change the tensor between replays.  ``offset``
+    is part of the state dict."""
+
+    def __init__(self, p: float, seed=0):
+        super().__init__()
+        if not 0.0 <= p <= 1.0:
+            raise ValueError(f"p must lie in [0, 1], got {p}")
+        self.p, self.seed, self.offset = p, seed, 0
+
+    def get_extra_state(self):
+        return {"offset": self.offset}
+
+    def set_extra_state(self, state):
+        self.offset = state["offset"]
+
+    def forward(self, x: torch.Tensor, residual=None) -> torch.Tensor:
+        if not self.training:
+            return x if residual is None else x + residual
+        offset, self.offset = self.offset, self.offset + 1
+        return _Dropout.apply(x, residual, self.p, self.seed, offset)
 
 
 # ---------------------------------------------------------------------------
