@@ -133,6 +133,13 @@ def _need(t, dtype, name, numel=None):
     return t
 
 
+def _here(t, name) -> None:
+    """Kernels run on the current device: a tensor of another is refused."""
+    if t.is_cuda and t.device.index != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {t.device}, the current device is "
+                         f"cuda:{torch._C._cuda_getDevice()}")
+
+
 def _flags(validate: bool) -> int:
     return VALIDATE if validate else TRUSTED
 

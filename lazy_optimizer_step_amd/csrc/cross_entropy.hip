@@ -1088,8 +1088,8 @@ extern "C" int linear_cross_entropy_forward(const void* x, int64_t x_stride, con
         (lse == nullptr && rows > 0))
         return fail(SPOPT_EINVAL, "%s: NULL loss or lse", what);
     if (rows == 0) {
-        if (reduction != SPOPT_REDUCE_NONE)
-            k_ce_reduce<<<1, 1024, 0, s>>>(nullptr, nullptr, ignore_index, 0, reduction, loss);
+        if (reduction == SPOPT_REDUCE_NONE) return SPOPT_OK;
+        k_ce_reduce<<<1, 1024, 0, s>>>(nullptr, nullptr, ignore_index, 0, reduction, loss);
         SPOPT_LAUNCHED();
         return SPOPT_OK;
     }
@@ -1177,8 +1177,8 @@ extern "C" int linear_cross_entropy_backward(
                                              (__bf16*)out, ld);
     };
     if (rows == 0) {
-        if (dweight != nullptr)
-            gather(nullptr, nullptr, 0, classes, false, dweight, dweight_stride);
+        if (dweight == nullptr) return SPOPT_OK;
+        gather(nullptr, nullptr, 0, classes, false, dweight, dweight_stride);
         SPOPT_LAUNCHED();
         return SPOPT_OK;
     }

@@ -16,7 +16,7 @@ import math
 
 import torch
 
-from . import _alloc_on, _flags, _lib, _need, _ptr, _stream, check
+from . import _alloc_on, _flags, _here, _lib, _need, _ptr, _stream, check
 
 NS_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
 
@@ -237,6 +237,7 @@ def dropout_forward(x: torch.Tensor, p: float, seed, *, offset: int = 0, residua
     kernel reads when it runs (a replayed graph then takes what it holds).  out may be x or
     residual."""
     rows, cols, xs = _rows(x, "x")
+    _here(x, "x")
     rs = ys = cols
     if residual is not None:
         _, _, rs = _rows(residual, "residual", x)
@@ -257,6 +258,7 @@ def dropout_backward(dy: torch.Tensor, p: float, seed, *, offset: int = 0, out=N
     """dx of dropout_forward with the same p, seed and offset (the residual's gradient is dy).
     out may be dy."""
     rows, cols, ds = _rows(dy, "dy")
+    _here(dy, "dy")
     os_ = cols
     if out is not None:
         _, _, os_ = _rows(out, "out", dy)

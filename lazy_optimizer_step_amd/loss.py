@@ -13,7 +13,7 @@ import functools
 
 import torch
 
-from . import _alloc_on, _flags, _lib, _need, _ptr, _stream, check
+from . import _alloc_on, _flags, _here, _lib, _need, _ptr, _stream, check
 from .dense import _DTYPES, _like, _rows, _spaced
 
 _REDUCTIONS = {"none": _lib.REDUCE_NONE, "sum": _lib.REDUCE_SUM, "mean": _lib.REDUCE_MEAN}
@@ -48,6 +48,7 @@ def _table(weight, name, x, cols):
 
 def _inputs(x, weight, targets, reduction):
     rows, cols, xs = _rows(x, "x")
+    _here(x, "x")
     classes, ws = _table(weight, "weight", x, cols)
     _need(targets, torch.int64, "targets")
     if targets.device != x.device:
