@@ -20,28 +20,9 @@
 // each value (fewer of those below 2^-18 of the largest: off by 2^-40 of it at
 // most).  A product is hi hi + hi lo + lo hi, three matrix instructions in place
 // of one, which together still run at twice the rate of the float32 ones.
-#include <math.h>
-
-#include <type_traits>
-
-#include "dense.hpp"
-#include "matrix.hpp"
+#include "cross_entropy.hpp"
 
 namespace spopt {
-
-typedef __bf16 bhalf8 __attribute__((ext_vector_type(8)));
-
-__device__ __forceinline__ float4v matrix_16x16x32(half8 a, half8 b, float4v c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-}
-__device__ __forceinline__ float4v matrix_16x16x32(bhalf8 a, bhalf8 b, float4v c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
-
-// What a call's kernels hand on to the next ones.
-struct CeScalars {
-    int ex, ew, ek;  // powers of two in front of the operands x, W (float32) and g
-};
 
 // An operand of a product: rows of 16-bit values.  Where the inner axis runs
 // along the rows, `last` is the last row; where it runs from row to row, the
@@ -59,39 +40,6 @@ struct CeProduct {
     int splits;       // parts of the inner axis
     int64_t tiles_m, tiles_n;
 };
-
-// What is done with a tile of the logits.
-struct CeLogits {
-    const CeScalars* scalars;
-    const int64_t* targets;
-    int64_t first;       // class of the piece's first column
-    int64_t classes;     // of all pieces
-    float smoothing;
-    // forward
-    float2* parts;       // [tile of classes][row]: maximum, sum of exponentials
-    float* sums;         // [tile of classes][row]: sum of the logits (smoothing only)
-    float* at_target;    // [row]
-    int64_t first_tile;
-    // backward
-    const float* lse;
-    const float* coef;   // [row] c_i 2^k
-    void* g;             // [row][ldg]
-    int64_t ldg, rows_p, cols_p;  // g's extent, zeros beyond the matrix
-};
-
-// Where a product's result goes: sums in float32, [split][row][ld], added to
-// what is there or not; or (parts NULL) scaled and rounded to where it belongs.
-struct CeResult {
-    const CeScalars* scalars;
-    int of_w;            // the other operand is W (dx), else x (dW)
-    float* parts;
-    int64_t ld;
-    int add;
-    void* out;
-    int64_t out_ld;
-};
-
-enum : int { kCeLoss = 0, kCeGrad = 1, kCeDx = 2, kCeDw = 3 };
 
 // The product of one tile, in the order of matrix.hpp's helpers: operands go
 // through LDS 64 values of the inner axis at a time, loaded straight into it
@@ -251,195 +199,47 @@ struct CeTile {
     }
 };
 
-// Tile `t` of a product, four rows of tiles at a time, column by column.
-__device__ __forceinline__ void ce_place(int64_t t, int64_t tm, int64_t tn, int64_t* ti,
-                                         int64_t* tj) {
-    const int64_t band = t / (4 * tn), in = t % (4 * tn);
-    const int64_t rows = tm - 4 * band < 4 ? tm - 4 * band : 4;
-    *ti = 4 * band + in % rows;
-    *tj = in / rows;
-}
-
-// The column of class `target` in a tile whose first is `first`; -1 where it lies
-// far from it.
-__device__ __forceinline__ int ce_column(int64_t target, int64_t first) {
-    const uint64_t j = (uint64_t)target - (uint64_t)first;
-    return j < 4096 ? (int)j : -1;
-}
-
-constexpr float kLog2e = 1.44269504088896340736f;
-
-// exp(z - b), the difference formed before it is scaled.
-__device__ __forceinline__ float exp_less(float z, float b) {
-    return __builtin_amdgcn_exp2f((z - b) * kLog2e);
-}
-
 template <class T, bool SPLIT, int MODE, class TL>
 __global__ __launch_bounds__(TL::kThreads) void k_ce_logits(CeProduct c, CeLogits w) {
     extern __shared__ __align__(16) char lds_raw[];
     typedef CeTile<T, SPLIT, false, false, TL> Tile;
-    constexpr int FM = Tile::FM, FN = Tile::FN, BM = TL::BM, BN = TL::BN;
+    constexpr int BM = TL::BM, BN = TL::BN;
     int64_t ti, tj;
     ce_place(xcd_order(blockIdx.x, gridDim.x), c.tiles_m, c.tiles_n, &ti, &tj);
     const int64_t i0 = ti * BM, j0 = tj * BN;
     Tile tile;
     tile.init();
     tile.run((T*)lds_raw, c, i0, j0, 0, c.steps);
-    const int scale = SPLIT ? -(w.scalars->ex + w.scalars->ew) : 0;
-    const bool whole = j0 + BN <= c.n;
-    const float off = w.smoothing / (float)w.classes, on = 1.f - w.smoothing;
-
-    if constexpr (MODE == kCeLoss) {
-        float* const red = (float*)lds_raw;  // [WGN][3][BM]
-        __syncthreads();
-        const int wn = tile.wv % TL::WGN;
-#pragma unroll
-        for (int x = 0; x < FM; ++x) {
-            const int r = tile.row_of(x);
-            const int64_t i = i0 + r;
-            const int t = i < c.m ? ce_column(w.targets[i], w.first + j0) : -1;
-            float top = -INFINITY, z = 0.f, s = 0.f;
-#pragma unroll
-            for (int y = 0; y < FN; ++y)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float v = tile.acc[x][y][e];
-                    if (SPLIT) v = ldexpf(v, scale);
-                    const int j = tile.col_of(y) + e;
-                    if (whole || j0 + j < c.n) {
-                        z += v;
-                        if (j == t) w.at_target[i] = v;
-                    } else {
-                        v = -INFINITY;
-                    }
-                    tile.acc[x][y][e] = v;
-                    top = fmaxf(top, v);
-                }
-            top = fmaxf(top, __shfl_xor(top, 16, kWave));
-            top = fmaxf(top, __shfl_xor(top, 32, kWave));
-            const float base = top == -INFINITY ? 0.f : top;
-#pragma unroll
-            for (int y = 0; y < FN; ++y)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s += exp_less(tile.acc[x][y][e], base);
-            s += __shfl_xor(s, 16, kWave);
-            s += __shfl_xor(s, 32, kWave);
-            z += __shfl_xor(z, 16, kWave);
-            z += __shfl_xor(z, 32, kWave);
-            if (tile.lane < 16) {
-                red[(wn * 3 + 0) * BM + r] = top;
-                red[(wn * 3 + 1) * BM + r] = s;
-                red[(wn * 3 + 2) * BM + r] = z;
-            }
-        }
-        __syncthreads();
-        for (int r = threadIdx.x; r < BM; r += TL::kThreads) {
-            if (i0 + r >= c.m) break;
-            float top = -INFINITY, s = 0.f, z = 0.f;
-#pragma unroll
-            for (int k = 0; k < TL::WGN; ++k) top = fmaxf(top, red[k * 3 * BM + r]);
-            const float base = top == -INFINITY ? 0.f : top;
-#pragma unroll
-            for (int k = 0; k < TL::WGN; ++k) {
-                s += red[(k * 3 + 1) * BM + r] * exp_less(red[k * 3 * BM + r], base);
-                z += red[(k * 3 + 2) * BM + r];
-            }
-            const int64_t at = (w.first_tile + tj) * c.m + i0 + r;
-            w.parts[at] = make_float2(top, s);
-            if (w.sums) w.sums[at] = z;
-        }
-    } else {
-        T* const g = (T*)w.g;
-#pragma unroll
-        for (int x = 0; x < FM; ++x) {
-            const int64_t i = i0 + tile.row_of(x);
-            if (i >= w.rows_p) continue;
-            const bool row = i < c.m;
-            const int t = row ? ce_column(w.targets[i], w.first + j0) : -1;
-            const float coef = row ? w.coef[i] : 0.f, lse = row ? w.lse[i] : 0.f;
-#pragma unroll
-            for (int y = 0; y < FN; y += 2) {
-                const int j = tile.col_of(y);
-                if (j0 + j >= w.cols_p) continue;
-                float v[8], lo[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float z = tile.acc[x][y + e / 4][e & 3];
-                    if (SPLIT) z = ldexpf(z, scale);
-                    float p = exp_less(z, lse) - off;
-                    if (j + e == t) p -= on;
-                    p *= coef;
-                    // Rows that do not count may hold anything.
-                    v[e] = coef == 0.f || (!whole && j0 + j + e >= c.n) ? 0.f : p;
-                }
-                if constexpr (SPLIT) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) lo[e] = v[e] - (float)(T)v[e];
-                    T* to = g + i * w.ldg + (j0 + j) / 32 * 64 + (j0 + j) % 32;
-                    store_v<T, 8>(to, v);
-                    store_v<T, 8>(to + 32, lo);
-                } else {
-                    store_v<T, 8>(g + i * w.ldg + j0 + j, v);
-                }
-            }
-        }
-    }
+    const int e = SPLIT ? -(w.scalars->ex + w.scalars->ew) : 0;
+    auto scale = [&](float v) { return SPLIT ? ldexpf(v, e) : v; };
+    if constexpr (MODE == kCeLoss)
+        ce_loss_tile<BM, BN, TL::WGN>(tile, (float*)lds_raw, i0, j0, tj, c.m, c.n, w, scale);
+    else
+        ce_grad_tile<T, SPLIT, BN>(tile, i0, j0, c.m, c.n, w, scale,
+                                   [&](int64_t i) { return w.coef[i]; });
 }
 
 template <class T, bool SPLIT, int MODE, class TL>
-__global__ __launch_bounds__(TL::kThreads) void k_ce_product(CeProduct c, CeResult w) {
+__global__ __launch_bounds__(TL::kThreads) void k_ce_product(CeProduct c, CeResult w,
+                                                             const CeScalars* sc) {
     extern __shared__ __align__(16) char lds_raw[];
     typedef CeTile<T, SPLIT, MODE == kCeDw, true, TL> Tile;
     typedef std::conditional_t<SPLIT, float, T> O;
-    constexpr int FM = Tile::FM, FN = Tile::FN, BM = TL::BM, BN = TL::BN;
     const int64_t tiles = c.tiles_m * c.tiles_n;
     const int64_t b = xcd_order(blockIdx.x, gridDim.x);
     const int64_t split = b / tiles;
     int64_t ti, tj;
     ce_place(b % tiles, c.tiles_m, c.tiles_n, &ti, &tj);
-    const int64_t i0 = ti * BM, j0 = tj * BN;
+    const int64_t i0 = ti * TL::BM, j0 = tj * TL::BN;
     const int64_t k0 = split * c.steps / c.splits, k1 = (split + 1) * c.steps / c.splits;
     Tile tile;
     tile.init();
     if (k0 < k1) tile.run((T*)lds_raw, c, i0, j0, k0, k1);
-    if (w.parts != nullptr) {
-        float* const out = w.parts + split * c.m * w.ld;
-#pragma unroll
-        for (int x = 0; x < FM; ++x) {
-            const int64_t i = i0 + tile.row_of(x);
-            if (i >= c.m) continue;
-#pragma unroll
-            for (int y = 0; y < FN; ++y) {
-                const int64_t j = j0 + tile.col_of(y);
-                if (j >= w.ld) continue;
-                float4v* const to = (float4v*)(out + i * w.ld + j);
-                *to = w.add ? *to + tile.acc[x][y] : tile.acc[x][y];
-            }
-        }
-        return;
-    }
-    const int scale = -(w.scalars->ek + (SPLIT ? w.of_w ? w.scalars->ew : w.scalars->ex : 0));
-    O* const out = (O*)w.out;
-#pragma unroll
-    for (int x = 0; x < FM; ++x) {
-        const int64_t i = i0 + tile.row_of(x);
-        if (i >= c.m) continue;
-#pragma unroll
-        for (int y = 0; y < FN; ++y) {
-            const int64_t j = j0 + tile.col_of(y);
-            float v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = ldexpf(tile.acc[x][y][e], scale);
-            O* const to = out + i * w.out_ld + j;
-            if (j + 4 <= c.n) {
-                store_v<O, 4>(to, v);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (j + e < c.n) to[e] = (O)v[e];
-            }
-        }
-    }
+    const int e = sc->ek + (SPLIT ? MODE == kCeDx ? sc->ew : sc->ex : 0);
+    const float mu = sc->mu;
+    ce_store_tile<O>(tile, i0, j0, c.m, c.n, w,
+                     w.parts == nullptr ? nullptr : w.parts + split * c.m * w.ld,
+                     [&](float v) { return ce_unscale(v, mu, e); });
 }
 
 // out = the splits' sums (zeros where there are none), scaled and rounded.  HBM
@@ -449,8 +249,8 @@ __global__ __launch_bounds__(256) void k_ce_gather(const float* parts, int split
                                                    int64_t ld, int64_t cols, const CeScalars* sc,
                                                    int use_w, int use_x, O* out, int64_t out_ld) {
     const int64_t quads = ld / 4, all = rows * quads;
-    const int scale =
-        splits == 0 ? 0 : -(sc->ek + (use_w ? sc->ew : 0) + (use_x ? sc->ex : 0));
+    const float mu = splits == 0 ? 0.f : sc->mu;
+    const int scale = splits == 0 ? 0 : sc->ek + (use_w ? sc->ew : 0) + (use_x ? sc->ex : 0);
     for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < all;
          q += (int64_t)gridDim.x * 256) {
         const int64_t i = q / quads, j = q % quads * 4;
@@ -463,7 +263,7 @@ __global__ __launch_bounds__(256) void k_ce_gather(const float* parts, int split
         }
         float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = ldexpf((float)s[e], scale);
+        for (int e = 0; e < 4; ++e) v[e] = ce_unscale((float)s[e], mu, scale);
         O* const to = out + i * out_ld + j;
         if (j + 4 <= cols) {
             store_v<O, 4>(to, v);
@@ -583,89 +383,85 @@ __global__ __launch_bounds__(256) void k_ce_pack(const S* a, int64_t ld, int64_t
 
 // ------------------------------------------------------ joins and sums ---
 
-__device__ __forceinline__ double ce_block_sum(double v, double* lds) {
-#pragma unroll
-    for (int off = kWave / 2; off; off >>= 1) v += __shfl_xor(v, off, kWave);
-    __syncthreads();
-    if (lane_id() == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    double s = 0.;
-    for (int i = 0; i < (int)(blockDim.x >> 6); ++i) s += lds[i];
-    return s;
-}
-
-enum : int { kCeNone = SPOPT_REDUCE_NONE, kCeSum = SPOPT_REDUCE_SUM, kCeMean = SPOPT_REDUCE_MEAN };
-
 // lse and loss of each row from its tiles' pairs: `per` rows (a power of two, up
-// to 64) of a block's 1024 threads, the tiles shared out to 1024 / per of them.
-// A block that has all rows sums their losses itself.
+// to 64, or 1024) at a time by a block's 1024 threads, the tiles shared out to
+// 1024 / per of them.  A block alone sums the rows' losses itself.
 __global__ __launch_bounds__(1024) void k_ce_join(const float2* parts, const float* sums,
                                                   const float* at_target, const int64_t* targets,
                                                   int64_t ignored, int64_t rows, int64_t tiles,
                                                   int64_t classes, float smoothing, int per,
                                                   int reduction, float* row_loss, float* loss,
                                                   float* lse) {
-    __shared__ float tops[1024];
-    __shared__ double both[2][1024];
-    const int t = threadIdx.x, slices = 1024 / per;
-    const int64_t i = (int64_t)blockIdx.x * per + t % per;
-    float top = -INFINITY;
-    double s = 0., z = 0.;
-    auto add = [&](float m, double v) {
-        const float next = fmaxf(top, m);
-        if (top != next) s *= (double)__expf(top - next);
-        s += m == next ? v : v * (double)__expf(m - next);
-        top = next;
-    };
-    if (i < rows) {
-        int64_t k = t / per;
-        for (; k + 3 * slices < tiles; k += 4 * slices) {
-            float2 p[4];
+    __shared__ float tops[16][64];
+    __shared__ double both[2][16][64];
+    const int t = threadIdx.x, slices = 1024 / per, lane = lane_id(), wv = t >> 6;
+    double total = 0., count = 0.;
+    for (int64_t first = (int64_t)blockIdx.x * per; first < rows; first += (int64_t)gridDim.x * per) {
+        const int64_t i = first + t % per;
+        float top = -INFINITY;
+        double s = 0., z = 0.;
+        auto add = [&](float m, double v) {
+            const float next = fmaxf(top, m);
+            if (top != next) s *= (double)exp_less(top, next);
+            s += m == next ? v : v * (double)exp_less(m, next);
+            top = next;
+        };
+        if (i < rows) {
+            int64_t k = t / per;
+            for (; k + 3 * slices < tiles; k += 4 * slices) {
+                float2 p[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) p[u] = parts[(k + u * slices) * rows + i];
+                for (int u = 0; u < 4; ++u) p[u] = parts[(k + u * slices) * rows + i];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) add(p[u].x, p[u].y);
+                for (int u = 0; u < 4; ++u) add(p[u].x, p[u].y);
+            }
+            for (; k < tiles; k += slices) {
+                const float2 p = parts[k * rows + i];
+                add(p.x, p.y);
+            }
+            if (sums)
+                for (k = t / per; k < tiles; k += slices) z += (double)sums[k * rows + i];
         }
-        for (; k < tiles; k += slices) {
-            const float2 p = parts[k * rows + i];
-            add(p.x, p.y);
+        for (int off = per; off < kWave; off <<= 1) {
+            const float m = __shfl_xor(top, off, kWave);
+            const double v = __shfl_xor(s, off, kWave);
+            add(m, v);
+            z += __shfl_xor(z, off, kWave);
         }
-        if (sums)
-            for (k = t / per; k < tiles; k += slices) z += (double)sums[k * rows + i];
-    }
-    for (int off = slices / 2; off; off >>= 1) {
-        tops[t] = top;
-        both[0][t] = s;
-        both[1][t] = z;
-        __syncthreads();
-        if (t < off * per) {
-            add(tops[t + off * per], both[0][t + off * per]);
-            z += both[1][t + off * per];
+        if (per != 1024) __syncthreads();
+        if (lane < per && per != 1024) {
+            tops[wv][lane] = top;
+            both[0][wv][lane] = s;
+            both[1][wv][lane] = z;
         }
-        __syncthreads();
-    }
-    double own = 0.;
-    bool valid = false;
-    if (t < per && i < rows) {
-        const double l = (double)top + log(s);
+        if (per != 1024) __syncthreads();
+        if (t >= per || i >= rows) continue;
+        for (int k = 1; k < 16 && per != 1024; ++k) {
+            add(tops[k][t], both[0][k][t]);
+            z += both[1][k][t];
+        }
         const int64_t goal = targets[i];
-        valid = goal != ignored;
+        const bool valid = goal != ignored;
+        const double l = (double)top + log(s);
+        double own = 0.;
         if (valid) {
             own = goal < 0 || goal >= classes
                       ? (double)NAN
                       : l - (1. - (double)smoothing) * (double)at_target[i] -
                             (double)smoothing * (z / (double)classes);
+            total += own;
+            count += 1.;
         }
         lse[i] = valid ? (float)l : 0.f;
         if (reduction == kCeNone)
             loss[i] = (float)own;
-        else
+        else if (gridDim.x != 1)
             row_loss[i] = (float)own;
     }
     if (reduction == kCeNone || gridDim.x != 1) return;
-    const double sum = ce_block_sum(own, both[0]);
-    const double count = ce_block_sum(valid ? 1. : 0., both[1]);
-    if (t == 0) *loss = (float)(reduction == kCeMean ? sum / fmax(count, 1.) : sum);
+    total = ce_block_sum(total, both[0][0]);
+    count = ce_block_sum(count, both[1][0]);
+    if (t == 0) *loss = (float)(reduction == kCeMean ? total / fmax(count, 1.) : total);
 }
 
 // The rows' losses as one, by one block.
@@ -683,47 +479,19 @@ __global__ __launch_bounds__(1024) void k_ce_reduce(const float* row_loss, const
     if (threadIdx.x == 0) *loss = (float)(reduction == kCeMean ? s / fmax(n, 1.) : s);
 }
 
-// Each row's factor in front of its gradient, times the power of two that
-// brings the largest to [2^13, 2^14); zero for rows that are ignored and beyond
-// the last, NaN for a target outside the classes.  One block.
-__global__ __launch_bounds__(1024) void k_ce_coef(const float* dloss, const int64_t* targets,
-                                                  int64_t ignored, int64_t rows, int64_t rows_p,
-                                                  int64_t classes, int reduction, float* coef,
+// Each row's factor, 0 beyond the last.  One block.
+__global__ __launch_bounds__(1024) void k_ce_coef(CeRows rows, int64_t rows_p, float* coef,
                                                   CeScalars* scalars) {
     __shared__ double lds[16];
     __shared__ float top_of[16];
-    const int t = threadIdx.x;
-    double n = 0.;
-    float top = 0.f;
-    for (int64_t i = t; i < rows; i += 1024) {
-        if (targets[i] == ignored) continue;
-        n += 1.;
-        if (reduction == kCeNone && finite_f(dloss[i])) top = fmaxf(top, fabsf(dloss[i]));
+    CeFactor f;
+    f.init(rows, false, lds, top_of);
+    if (threadIdx.x == 0) {
+        scalars->ek = f.ek;
+        scalars->mu = f.mu;
     }
-    n = ce_block_sum(n, lds);
-#pragma unroll
-    for (int off = kWave / 2; off; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, kWave));
-    if (lane_id() == 0) top_of[t >> 6] = top;
-    __syncthreads();
-    for (int k = 0; k < 16; ++k) top = fmaxf(top, top_of[k]);
-    const float one = reduction == kCeNone  ? 0.f
-                      : reduction == kCeSum ? dloss[0]
-                                            : (float)((double)dloss[0] / fmax(n, 1.));
-    if (reduction != kCeNone) top = fabsf(one);
-    int ek = 0;
-    if (top > 0.f && finite_f(top)) {
-        frexpf(top, &ek);
-        ek = 14 - ek;
-    }
-    if (t == 0) scalars->ek = ek;
-    for (int64_t i = t; i < rows_p; i += 1024) {
-        float c = 0.f;
-        if (i < rows && targets[i] != ignored) {
-            c = ldexpf(reduction == kCeNone ? dloss[i] : one, ek);
-            if (targets[i] < 0 || targets[i] >= classes) c = NAN;
-        }
-        coef[i] = c;
-    }
+    for (int64_t i = threadIdx.x; i < rows_p; i += 1024)
+        coef[i] = i < rows.rows ? f.of(rows, i) : 0.f;
 }
 
 // Sets kStatusRange for a target that is neither ignored nor a class, and
@@ -751,15 +519,16 @@ typedef Tiling<256, 256, 2, 4, 2> CeL;
 
 // How a product is tiled, and into how many parts its inner axis is cut.
 struct CePlan {
-    int tile;    // 64, 128 or 256
+    int tile;    // its rows: 64, 128 or 256; 16 or 64 of the direct kernels
     int splits;
+    double us;   // what it is expected to take
 };
 
 // An inner step takes a tile of 64, 128 and 256 about 0.2, 0.5 and 1.8 us of its
-// CU.  Cut products write and read their parts once more, 5 bytes a picosecond.
-static CePlan ce_plan(int64_t m, int64_t n, int64_t steps, bool cut) {
-    CePlan best{64, 1};
-    double least = INFINITY;
+// CU, of split operands half as much again.  Cut products write and read their
+// parts once more, 5 bytes a picosecond.
+static CePlan ce_plan(int64_t m, int64_t n, int64_t steps, bool cut, bool split) {
+    CePlan best{64, 1, INFINITY};
     const struct { int b; double us; } kind[3] = {{64, 0.2}, {128, 0.5}, {256, 1.8}};
     for (const auto& k : kind) {
         const int64_t tiles = ceil_div(m, k.b) * ceil_div(n, k.b);
@@ -767,12 +536,9 @@ static CePlan ce_plan(int64_t m, int64_t n, int64_t steps, bool cut) {
             if (s > 1 && steps < 4 * s) break;
             if (tiles * s > (1 << 22) && !(k.b == 256 && s == 1)) continue;
             const double us = (double)ceil_div(tiles * s, 256) * (double)(ceil_div(steps, s) + 2) *
-                                  k.us +
+                                  k.us * (split ? 1.5 : 1.) +
                               (s > 1 ? 3. + (double)s * (double)m * (double)n * 8. / 5e6 : 0.);
-            if (us < least) {
-                least = us;
-                best = CePlan{k.b, s};
-            }
+            if (us < best.us) best = CePlan{k.b, s, us};
         }
     }
     return best;
@@ -831,28 +597,75 @@ struct CeBuffers {
 
 struct CeRun {
     CeShape s;
+    bool direct;         // the kernels of cross_entropy_direct.hip
     int64_t piece;
     CePlan logits, dx, dw;
     int64_t tiles;       // of classes, in the forward pass
 };
 
+// As ce_plan, for the direct kernels: an inner step takes a tile of 16 and 64
+// rows about 0.25 and 0.3 us, of float32 0.4 and 0.7, and joining the parts of a
+// cut axis a launch.
+static CePlan ce_direct_plan(const CeShape& s, int64_t m, int64_t n, int64_t k, bool cut) {
+    const int64_t steps = ceil_div(k, s.split ? 32 : 64);
+    CePlan best{64, 1, INFINITY};
+    for (int tile = 16; tile <= 64; tile += 48)
+        for (int splits = 1; splits <= (cut ? 32 : 1); splits *= 2) {
+            const int64_t blocks = ceil_div(m, tile) * ceil_div(n, 64) * splits;
+            if (splits > 1 && blocks > 1024) break;
+            const double step = s.split ? tile == 16 ? 0.4 : 0.7 : tile == 16 ? 0.25 : 0.3;
+            const double us = (double)ceil_div(blocks, 256) *
+                                  ((double)ceil_div(steps, splits) * step + 1.) +
+                              (splits > 1 ? 5. : 0.);
+            if (us < best.us) best = CePlan{tile, splits, us};
+        }
+    return best;
+}
+
+// Which kernels, and their tiles.  Packed operands cost a launch for each copy and
+// each thing found out about them, 3.3 us each, and the copies' traffic (x's in
+// any backward pass; both operands' of float32, 12 bytes a value with the pass that
+// finds the largest; of 16 bits, 4 bytes a value of rows that have a remainder);
+// the direct kernels multiply more slowly, those of float32 far more.  Both sides
+// measured at 114 sizes, forward and backward: the estimates choose the slower one
+// at 7 of 228, by 1.04 to 1.2 times.  4 x 256 x 1000 float32: 18.7 against 28.9 us forward
+// and 25.9 against 39.1 backward; 500 x 256 x 100000 float32: 337 against 176 and
+// 934 against 446.
 static CeRun ce_run(const CeShape& s, bool backward) {
-    CeRun r{};
-    r.s = s;
-    r.piece = ce_piece(s, backward);
+    CeRun d{}, p{};
+    d.s = p.s = s;
+    d.direct = true;
+    d.piece = ceil_div(s.classes, 64) * 64;
+    d.tiles = ceil_div(s.classes, 64);
+    d.logits = ce_direct_plan(s, s.rows, s.classes, s.cols, false);
+    p.piece = ce_piece(s, backward);
     const int64_t inner = s.split ? 32 : 64;
-    const int64_t first = s.classes < r.piece ? s.classes : r.piece;
-    r.logits = ce_plan(s.rows, first, s.cols_p / inner, false);
-    r.tiles = 0;
-    for (int64_t v = 0; v < s.classes; v += r.piece) {
-        const int64_t n = s.classes - v < r.piece ? s.classes - v : r.piece;
-        r.tiles += ceil_div(n, r.logits.tile);
+    const int64_t first = s.classes < p.piece ? s.classes : p.piece;
+    const double pieces = (double)ceil_div(s.classes, p.piece);
+    p.logits = ce_plan(s.rows, first, s.cols_p / inner, false, s.split);
+    const bool copies = s.split || s.cols % 64 != 0;
+    double us_d = d.logits.us, us_p = p.logits.us * pieces;
+    us_p += copies ? (double)((s.rows + s.classes) * s.cols) * (s.split ? 12. : 4.) / 4.2e6 : 0.;
+    if (!backward) {
+        us_p += s.split ? 10. : copies ? 6.6 : 0.;
+    } else {
+        d.dx = ce_direct_plan(s, s.rows, s.cols, s.classes, true);
+        d.dw = ce_direct_plan(s, s.classes, s.cols, s.rows, true);
+        p.dx = ce_plan(s.rows, s.cols, ceil_div(first, inner), true, s.split);
+        p.dw = ce_plan(first, s.cols, ceil_div(s.rows, inner), true, s.split);
+        us_d += d.dx.us + d.dw.us;
+        us_p += (p.dx.us + p.dw.us) * pieces + (s.split ? 16. : copies ? 13. : 10.);
+        us_p += copies ? 0. : (double)(s.rows * s.cols) * 4. / 4.2e6;
     }
-    if (backward) {
-        r.dx = ce_plan(s.rows, s.cols, ceil_div(first, inner), true);
-        r.dw = ce_plan(first, s.cols, ceil_div(s.rows, inner), true);
+    // Grids and g have to fit at once.
+    const int64_t blocks = ceil_div(s.rows, 16) * ceil_div(s.classes, 64);
+    const bool fits = blocks < (1 << 22) && s.rows_p <= ((int64_t)1 << 29) / (d.piece * 2 * s.value);
+    if (fits && us_d <= 1.1 * us_p) return d;
+    for (int64_t v = 0; v < s.classes; v += p.piece) {
+        const int64_t n = s.classes - v < p.piece ? s.classes - v : p.piece;
+        p.tiles += ceil_div(n, p.logits.tile);
     }
-    return r;
+    return p;
 }
 
 static size_t ce_layout(const CeRun& r, bool backward, char* base, CeBuffers* b) {
@@ -864,9 +677,11 @@ static size_t ce_layout(const CeRun& r, bool backward, char* base, CeBuffers* b)
         return (void*)p;
     };
     b->scalars = (CeScalars*)take(sizeof(CeScalars));
-    b->amax = (uint32_t*)take(2 * kAmaxParts * 4);
-    b->x = take((size_t)(s.rows_p * s.cols_p * s.value) * 2);
-    b->w = take((size_t)(r.piece * s.cols_p * s.value) * 2);
+    if (!r.direct) {
+        b->amax = (uint32_t*)take(2 * kAmaxParts * 4);
+        b->x = take((size_t)(s.rows_p * s.cols_p * s.value) * 2);
+        b->w = take((size_t)(r.piece * s.cols_p * s.value) * 2);
+    }
     if (!backward) {
         b->parts = (float2*)take((size_t)(r.tiles * s.rows) * 8);
         b->sums = (float*)take((size_t)(r.tiles * s.rows) * 4);
@@ -874,7 +689,7 @@ static size_t ce_layout(const CeRun& r, bool backward, char* base, CeBuffers* b)
         b->row_loss = (float*)take((size_t)s.rows * 4);
         return at;
     }
-    b->coef = (float*)take((size_t)s.rows_p * 4);
+    if (!r.direct) b->coef = (float*)take((size_t)s.rows_p * 4);
     b->g = take((size_t)(s.rows_p * r.piece * s.value) * 2);
     b->dx_parts = (float*)take((size_t)(r.dx.splits * s.rows * s.cols_p) * 4);
     b->dw_parts = (float*)take(
@@ -944,7 +759,7 @@ static int ce_logits(const CeRun& r, CeProduct c, const CeLogits& w, hipStream_t
 
 template <int MODE>
 static int ce_product(const CeRun& r, const CePlan& plan, CeProduct c, const CeResult& w,
-                      hipStream_t s) {
+                      const CeScalars* sc, hipStream_t s) {
     int rc = SPOPT_OK;
     c.splits = plan.splits;
     c.tiles_m = ceil_div(c.m, plan.tile);
@@ -952,7 +767,7 @@ static int ce_product(const CeRun& r, const CePlan& plan, CeProduct c, const CeR
     ce_types(r.s.dtype, [&](auto t, auto split) {
         ce_tilings(plan.tile, [&](auto tl) {
             rc = ce_launch(k_ce_product<decltype(t), decltype(split)::value, MODE, decltype(tl)>,
-                           tl, c.tiles_m * c.tiles_n * c.splits, s, c, w);
+                           tl, c.tiles_m * c.tiles_n * c.splits, s, c, w, sc);
         });
     });
     return rc;
@@ -1101,15 +916,6 @@ extern "C" int linear_cross_entropy_forward(const void* x, int64_t x_stride, con
         rc = ce_validate(what, sh, x, x_stride, weight, weight_stride, targets, ignore_index, s);
         if (rc) return rc;
     }
-    int amax = 0;
-    rc = ce_amax(sh, x, x_stride, targets, ignore_index, weight, weight_stride, b, &amax, s);
-    if (rc) return rc;
-    CeProduct c{};
-    c.m = rows;
-    c.steps = sh.cols_p / (sh.split ? 32 : 64);
-    rc = ce_operand(sh, x, x_stride, rows, rows, false, targets, ignore_index, b.amax, amax,
-                    &b.scalars->ex, b.x, &c.p, s);
-    if (rc) return rc;
     CeLogits w{};
     w.scalars = b.scalars;
     w.targets = targets;
@@ -1118,7 +924,21 @@ extern "C" int linear_cross_entropy_forward(const void* x, int64_t x_stride, con
     w.parts = b.parts;
     w.sums = label_smoothing != 0.0 ? b.sums : nullptr;
     w.at_target = b.at_target;
-    for (int64_t v = 0; v < classes; v += r.piece) {
+    CeProduct c{};
+    int amax = 0;
+    if (r.direct) {
+        rc = ce_direct_loss(dtype, r.logits.tile, CeSide{x, x_stride, rows, cols, targets, ignore_index},
+                            CeSide{weight, weight_stride, classes, cols, nullptr, 0}, w, s);
+    } else {
+        rc = ce_amax(sh, x, x_stride, targets, ignore_index, weight, weight_stride, b, &amax, s);
+        c.m = rows;
+        c.steps = sh.cols_p / (sh.split ? 32 : 64);
+        if (!rc)
+            rc = ce_operand(sh, x, x_stride, rows, rows, false, targets, ignore_index, b.amax,
+                            amax, &b.scalars->ex, b.x, &c.p, s);
+    }
+    if (rc) return rc;
+    for (int64_t v = 0; v < classes && !r.direct; v += r.piece) {
         c.n = classes - v < r.piece ? classes - v : r.piece;
         w.first = v;
         rc = ce_operand(sh, (const char*)weight + (size_t)(v * weight_stride) * dtype_bytes(dtype),
@@ -1128,13 +948,17 @@ extern "C" int linear_cross_entropy_forward(const void* x, int64_t x_stride, con
         if (rc) return rc;
         w.first_tile += ceil_div(c.n, r.logits.tile);
     }
-    int per = 64;
-    while (per > 1 && ceil_div(rows, per) < 128 && rows <= per / 2) per /= 2;
-    k_ce_join<<<(unsigned)ceil_div(rows, per), 1024, 0, s>>>(
+    // Rows of few tiles one a thread; and where one block is enough (for up to
+    // 128 rows, or 2048 of few tiles), it spares the launch that sums the rows.
+    int per = rows > 64 && r.tiles <= 8 ? 1024 : 64;
+    while (per <= 64 && per > 1 && rows <= per / 2) per /= 2;
+    int64_t blocks = ceil_div(rows, per);
+    if (reduction != SPOPT_REDUCE_NONE && blocks == 2) blocks = 1;
+    k_ce_join<<<(unsigned)blocks, 1024, 0, s>>>(
         b.parts, w.sums, b.at_target, targets, ignore_index, rows, r.tiles, classes,
         w.smoothing, per, reduction, b.row_loss, loss, lse);
     SPOPT_LAUNCHED();
-    if (reduction != SPOPT_REDUCE_NONE && rows > per) {
+    if (reduction != SPOPT_REDUCE_NONE && blocks > 1) {
         k_ce_reduce<<<1, 1024, 0, s>>>(b.row_loss, targets, ignore_index, rows, reduction, loss);
         SPOPT_LAUNCHED();
     }
@@ -1162,10 +986,9 @@ extern "C" int linear_cross_entropy_backward(
         return fail(SPOPT_EINVAL, "%s: a row stride below cols", what);
     if (dx == nullptr && dweight == nullptr) return SPOPT_OK;
     // The splits' sums of an operand's gradient, to where it belongs.
-    auto gather = [&](const float* parts, const CeScalars* sc, int splits, int64_t n, bool of_w,
-                      void* out, int64_t ld) {
+    auto gather = [&](const float* parts, const CeScalars* sc, int splits, int64_t n, int uw,
+                      int ux, void* out, int64_t ld) {
         const unsigned grid = ce_grid(n * (sh.cols_p / 4));
-        const int uw = sh.split && of_w, ux = sh.split && !of_w;
         if (dtype == SPOPT_DTYPE_F32)
             k_ce_gather<<<grid, 256, 0, s>>>(parts, splits, n, sh.cols_p, cols, sc, uw, ux,
                                              (float*)out, ld);
@@ -1178,7 +1001,7 @@ extern "C" int linear_cross_entropy_backward(
     };
     if (rows == 0) {
         if (dweight == nullptr) return SPOPT_OK;
-        gather(nullptr, nullptr, 0, classes, false, dweight, dweight_stride);
+        gather(nullptr, nullptr, 0, classes, 0, 0, dweight, dweight_stride);
         SPOPT_LAUNCHED();
         return SPOPT_OK;
     }
@@ -1190,11 +1013,56 @@ extern "C" int linear_cross_entropy_backward(
         rc = ce_validate(what, sh, x, x_stride, weight, weight_stride, targets, ignore_index, s);
         if (rc) return rc;
     }
+    const CeRows factors{dloss, targets, ignore_index, rows, classes, reduction,
+                         (float)(1.0 - label_smoothing)};
+    CeLogits w{};
+    w.scalars = b.scalars;
+    w.targets = targets;
+    w.classes = classes;
+    w.smoothing = (float)label_smoothing;
+    w.lse = lse;
+    w.coef = b.coef;
+    w.g = b.g;
+    w.rows_p = sh.rows_p;
+    if (r.direct) {
+        w.ldg = w.cols_p = r.piece;
+        w.rows_p = rows;
+        const CeSide xs{x, x_stride, rows, cols, targets, ignore_index};
+        const CeSide ws{weight, weight_stride, classes, cols, nullptr, 0};
+        rc = ce_direct_grad(dtype, r.logits.tile, xs, ws, w, factors, b.scalars, s);
+        if (rc) return rc;
+        CeBoth both{};
+        both.g = CeSide{b.g, r.piece, rows, classes, nullptr, 0};
+        both.w = ws;
+        both.x = xs;
+        both.rows = rows;
+        both.cols = cols;
+        both.classes = classes;
+        both.dx_tile = r.dx.tile;
+        both.dw_tile = r.dw.tile;
+        both.dx_splits = r.dx.splits;
+        both.dw_splits = r.dw.splits;
+        both.scalars = b.scalars;
+        if (dx != nullptr)
+            both.dx_tiles = ceil_div(rows, r.dx.tile) * ceil_div(cols, 64);
+        if (dweight != nullptr)
+            both.dw_tiles = ceil_div(classes, r.dw.tile) * ceil_div(cols, 64);
+        both.dx = CeResult{r.dx.splits > 1 ? b.dx_parts : nullptr, sh.cols_p, 0, dx, dx_stride};
+        both.dw = CeResult{r.dw.splits > 1 ? b.dw_parts : nullptr, sh.cols_p, 0, dweight,
+                           dweight_stride};
+        rc = ce_direct_products(dtype, both, s);
+        if (rc) return rc;
+        if (dx != nullptr && r.dx.splits > 1)
+            gather(b.dx_parts, b.scalars, r.dx.splits, rows, 0, 0, dx, dx_stride);
+        if (dweight != nullptr && r.dw.splits > 1)
+            gather(b.dw_parts, b.scalars, r.dw.splits, classes, 0, 0, dweight, dweight_stride);
+        SPOPT_LAUNCHED();
+        return SPOPT_OK;
+    }
     int amax = 0;
     rc = ce_amax(sh, x, x_stride, targets, ignore_index, weight, weight_stride, b, &amax, s);
     if (rc) return rc;
-    k_ce_coef<<<1, 1024, 0, s>>>(dloss, targets, ignore_index, rows, sh.rows_p, classes, reduction,
-                                 b.coef, b.scalars);
+    k_ce_coef<<<1, 1024, 0, s>>>(factors, sh.rows_p, b.coef, b.scalars);
     SPOPT_LAUNCHED();
     // x is copied for its rows that are ignored: they may hold anything, and meet
     // g's zeros in dW.
@@ -1216,36 +1084,25 @@ extern "C" int linear_cross_entropy_backward(
         c.m = rows;
         c.n = n;
         c.steps = sh.cols_p / inner;
-        CeLogits w{};
-        w.scalars = b.scalars;
-        w.targets = targets;
         w.first = v;
-        w.classes = classes;
-        w.smoothing = (float)label_smoothing;
-        w.lse = lse;
-        w.coef = b.coef;
-        w.g = b.g;
         w.ldg = ldg;
-        w.rows_p = sh.rows_p;
         w.cols_p = n_p;
         rc = ce_logits<kCeGrad>(r, c, w, s);
         if (rc) return rc;
         g = CeOperand{b.g, ldg, sh.rows_p - 1, n_p};
         CeResult o{};
-        o.scalars = b.scalars;
         if (dx != nullptr) {
             c.p = g;
             c.q = wo;
             c.m = rows;
             c.n = cols;
             c.steps = n_p / inner;
-            o.of_w = 1;
             o.out = dx;
             o.out_ld = dx_stride;
             o.ld = sh.cols_p;
             o.add = v > 0;
             o.parts = r.dx.splits == 1 && r.piece >= classes ? nullptr : b.dx_parts;
-            rc = ce_product<kCeDx>(r, r.dx, c, o, s);
+            rc = ce_product<kCeDx>(r, r.dx, c, o, b.scalars, s);
             if (rc) return rc;
         }
         if (dweight != nullptr) {
@@ -1254,22 +1111,22 @@ extern "C" int linear_cross_entropy_backward(
             c.m = n;
             c.n = cols;
             c.steps = sh.rows_p / inner;
-            o.of_w = 0;
             o.out = (char*)dweight + (size_t)(v * dweight_stride) * dtype_bytes(dtype);
             o.out_ld = dweight_stride;
             o.ld = sh.cols_p;
             o.add = 0;
             o.parts = r.dw.splits == 1 ? nullptr : b.dw_parts;
-            rc = ce_product<kCeDw>(r, r.dw, c, o, s);
+            rc = ce_product<kCeDw>(r, r.dw, c, o, b.scalars, s);
             if (rc) return rc;
             if (r.dw.splits > 1) {
-                gather(b.dw_parts, b.scalars, r.dw.splits, n, false, o.out, dweight_stride);
+                gather(b.dw_parts, b.scalars, r.dw.splits, n, 0, sh.split, o.out,
+                       dweight_stride);
                 SPOPT_LAUNCHED();
             }
         }
     }
     if (dx != nullptr && (r.dx.splits > 1 || r.piece < classes)) {
-        gather(b.dx_parts, b.scalars, r.dx.splits, rows, true, dx, dx_stride);
+        gather(b.dx_parts, b.scalars, r.dx.splits, rows, sh.split, 0, dx, dx_stride);
         SPOPT_LAUNCHED();
     }
     return SPOPT_OK;

@@ -1,0 +1,310 @@
+// cross_entropy_direct.hip - the loss's kernels for small calls, which read the
+// caller's operands as they lie: any stride and alignment, float32 on the float32
+// matrix instructions.
+//
+// A launch costs the host 3.5 us, which is all that a small call takes.  These
+// take two launches forward (the logits' tiles, the join) and two backward (g;
+// both products), where packed operands take up to five and nine.  Operands go
+// through registers into LDS, three stages on their way, 64 x 64 tiles, one
+// layout in LDS with cross_entropy.hip's.
+#include "cross_entropy.hpp"
+
+namespace spopt {
+
+template <class T, bool TP, bool TQ, int BM_>
+struct CeDirect {
+    static constexpr int BM = BM_, BN = 64, WGN = BM == 64 ? 2 : 4;  // four waves
+    static constexpr int FM = BM / 16 * WGN / 4, FN = 4 / WGN;
+    static constexpr int kAhead = BM == 64 ? 4 : 6;       // stages on their way in registers
+    static constexpr int kRow = TQ || FN % 2 ? 4 : 8;     // adjacent columns of a lane
+    static constexpr int E = 16 / (int)sizeof(T);         // values of a chunk
+    static constexpr int kInner = 128 / (int)sizeof(T);   // values of the inner axis a stage
+    static constexpr int kSideP = BM * 128, kSideQ = BN * 128;  // bytes of a stage
+    static constexpr int kBytes = 2 * (kSideP + kSideQ);  // of LDS
+    typedef T chunk __attribute__((ext_vector_type(E)));
+    static_assert(BM == 64 || BM == 16, "two tiles");
+
+    // Row v of a turned side has its 16 columns from 16 u on at u ^ turn(v).
+    template <int B>
+    static __device__ __forceinline__ int turn(int v) {
+        return B == 16 ? 0 : sizeof(T) == 4 ? v >> 2 & 3 : turn_q<64>(v);
+    }
+
+    // A side's loads: 8 B chunks a stage.
+    template <bool TURN, int B>
+    struct Feed {
+        static constexpr int kLoads = B == 64 ? 2 : 1;
+        const T* base;
+        const int64_t* targets;
+        int64_t ld, rows, cols, ignored, row[kLoads], col;
+        int place[kLoads];
+        __device__ __forceinline__ void init(const CeSide& s, int64_t first, bool pair) {
+            base = (const T*)s.base;
+            targets = s.targets;
+            ld = s.ld;
+            rows = s.rows;
+            cols = s.cols;
+            ignored = s.ignored;
+            constexpr int kWide = 16 / E;  // chunks of 16 columns
+#pragma unroll
+            for (int l = 0; l < kLoads; ++l) {
+                const int at = ((int)threadIdx.x + 256 * l) % (8 * B);
+                if constexpr (TURN) {
+                    const int v = at / (B / E), c = at % (B / E);
+                    row[l] = v;
+                    col = first + c * E;
+                    place[l] = (v * (B / E) + ((c / kWide) ^ turn<B>(v)) * kWide + c % kWide) * 16;
+                } else {
+                    const int v = at / 8, c = at % 8, in = v & 31;
+                    row[l] = first + (pair ? v - in + ((in & 12) >> 2) * 8 + (in >> 4) * 4 + (in & 3)
+                                           : v);
+                    if (row[l] >= rows || (targets && targets[row[l]] == ignored)) row[l] = -1;
+                    col = c * E;
+                    place[l] = (v * 8 + (c ^ (v & 7))) * 16;
+                }
+            }
+        }
+        __device__ __forceinline__ chunk load(int64_t k, int l) const {
+            int64_t r = row[l], c = col;
+            bool in;
+            if constexpr (TURN) {
+                r += k * kInner;
+                in = r < rows && !(targets && targets[r] == ignored);
+            } else {
+                c += k * kInner;
+                in = r >= 0;
+            }
+            chunk v = {};
+            if (!in || c >= cols) return v;
+            const T* p = base + r * ld + c;
+            if (c + E <= cols) return *(const typename Pack<T, E>::type*)p;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (c + e < cols) v[e] = p[e];
+            return v;
+        }
+    };
+
+    int lane, wv, wi, wj;
+    float4v acc[FM][FN];
+
+    __device__ __forceinline__ void init() {
+        lane = lane_id();
+        wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        wi = wv / WGN * FM * 16;
+        wj = wv % WGN * FN * 16;
+#pragma unroll
+        for (int x = 0; x < FM; ++x)
+#pragma unroll
+            for (int y = 0; y < FN; ++y) acc[x][y] = float4v{0.f, 0.f, 0.f, 0.f};
+    }
+
+    // The operand of 16 rows (or columns) from `first` on: half kk of a stage.
+    template <bool TURN, int B>
+    __device__ __forceinline__ auto operand(const char* l, int first, int kk) const {
+        typedef T vec __attribute__((ext_vector_type(E)));
+        if constexpr (TURN && sizeof(T) == 4) {
+            const int v = (kk * 4 + (lane >> 4)) * 4;
+            const T* a = (const T*)l + v * B + ((first >> 4) ^ turn<B>(v)) * 16 + (lane & 15);
+            return vec{a[0], a[B], a[2 * B], a[3 * B]};
+        } else if constexpr (TURN) {
+            typedef T half __attribute__((ext_vector_type(4)));
+            const int v = (lane >> 4) * 8 + ((lane & 15) >> 2);
+            const T* a = (const T*)l + (kk * 32 + v) * B + ((first >> 4) ^ turn<B>(v)) * 16 +
+                         (lane & 3) * 4;
+            const half lo = __builtin_bit_cast(half, read_turned((const _Float16*)a));
+            const half hi = __builtin_bit_cast(half, read_turned((const _Float16*)(a + 4 * B)));
+            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        } else {
+            const int v = first + (lane & 15);
+            return *(const vec*)(l + (v * 8 + ((kk * 4 + (lane >> 4)) ^ (v & 7))) * 16);
+        }
+    }
+
+    // Steps [k0, k1) of the inner axis.
+    __device__ __forceinline__ void run(char* lds, const CeSide& p, const CeSide& q, int64_t i0,
+                                        int64_t j0, int64_t k0, int64_t k1) {
+        typedef Feed<TP, BM> FeedP;
+        typedef Feed<TQ, BN> FeedQ;
+        FeedP fp;
+        FeedQ fq;
+        fp.init(p, i0, false);
+        fq.init(q, j0, kRow == 8);
+        const bool with_p = BM == 64 || threadIdx.x < 8 * BM;
+        chunk cp[kAhead][FeedP::kLoads], cq[kAhead][FeedQ::kLoads];
+        auto bring = [&](int u, int64_t k) {
+#pragma unroll
+            for (int l = 0; l < FeedP::kLoads; ++l)
+                if (with_p) cp[u][l] = fp.load(k, l);
+#pragma unroll
+            for (int l = 0; l < FeedQ::kLoads; ++l) cq[u][l] = fq.load(k, l);
+        };
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (k0 + u < k1) bring(u, k0 + u);
+        int buf = 0;
+        for (int64_t k = k0; k < k1; k += kAhead) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (k + u >= k1) break;
+                char* const to = lds + buf * (kSideP + kSideQ);
+#pragma unroll
+                for (int l = 0; l < FeedP::kLoads; ++l)
+                    if (with_p) *(chunk*)(to + fp.place[l]) = cp[u][l];
+#pragma unroll
+                for (int l = 0; l < FeedQ::kLoads; ++l)
+                    *(chunk*)(to + kSideP + fq.place[l]) = cq[u][l];
+                if (k + u + kAhead < k1) bring(u, k + u + kAhead);
+                // One barrier a stage: whoever writes this place next has passed
+                // the other one's, after all reads of this.
+                __syncthreads();
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+                    chunk a[FM], b[FN];
+#pragma unroll
+                    for (int x = 0; x < FM; ++x) a[x] = operand<TP, BM>(to, wi + x * 16, kk);
+#pragma unroll
+                    for (int y = 0; y < FN; ++y) b[y] = operand<TQ, BN>(to + kSideP, wj + y * 16, kk);
+#pragma unroll
+                    for (int x = 0; x < FM; ++x)
+#pragma unroll
+                        for (int y = 0; y < FN; ++y) {
+                            if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                                        b[y][e], a[x][e], acc[x][y], 0, 0, 0);
+                            } else {
+                                acc[x][y] = matrix_16x16x32(b[y], a[x], acc[x][y]);
+                            }
+                        }
+                }
+                buf ^= 1;
+            }
+        }
+        __syncthreads();
+    }
+
+    __device__ __forceinline__ int row_of(int x) const { return wi + x * 16 + (lane & 15); }
+    __device__ __forceinline__ int col_of(int y) const {
+        return wj + (lane >> 4) * kRow + (kRow == 8 ? y * 4 : y * 16);
+    }
+};
+
+template <class T, int MODE, int BM>
+__global__ __launch_bounds__(256) void k_ced_logits(CeSide x, CeSide w, CeLogits l, int64_t tn,
+                                                    int64_t tm, CeRows rows, CeScalars* scalars) {
+    typedef CeDirect<T, false, false, BM> Tile;
+    __shared__ __align__(16) char lds[Tile::kBytes];
+    int64_t ti, tj;
+    ce_place(xcd_order(blockIdx.x, gridDim.x), tm, tn, &ti, &tj);
+    const int64_t i0 = ti * BM, j0 = tj * 64;
+    Tile tile;
+    tile.init();
+    tile.run(lds, x, w, i0, j0, 0, (x.cols + Tile::kInner - 1) / Tile::kInner);
+    auto same = [](float v) { return v; };
+    if constexpr (MODE == kCeLoss) {
+        ce_loss_tile<BM, 64, Tile::WGN>(tile, (float*)lds, i0, j0, tj, x.rows, w.rows, l, same);
+    } else {
+        CeFactor f;
+        f.init(rows, sizeof(T) == 4, (double*)lds, (float*)lds + 64);
+        if (blockIdx.x == 0 && threadIdx.x == 0) {
+            scalars->ek = f.ek;
+            scalars->mu = f.mu;
+        }
+        ce_grad_tile<T, false, 64>(tile, i0, j0, x.rows, w.rows, l, same,
+                                   [&](int64_t i) { return f.of(rows, i); });
+    }
+}
+
+// Tile `at` of a product of `m` rows, the inner axis of `k` values cut into `splits`.
+template <class T, bool TP, int BM>
+__device__ __forceinline__ void ced_product(char* lds, const CeSide& p, const CeSide& q,
+                                            const CeResult& w, int64_t at, int64_t tiles,
+                                            int splits, int64_t m, int64_t n, int64_t k,
+                                            const CeScalars* sc) {
+    CeDirect<T, TP, true, BM> tile;
+    const int64_t split = at / tiles, t = at % tiles, tn = (n + 63) / 64;
+    const int64_t steps = (k + tile.kInner - 1) / tile.kInner;
+    const int64_t i0 = t / tn * BM, j0 = t % tn * 64;
+    tile.init();
+    tile.run(lds, p, q, i0, j0, split * steps / splits, (split + 1) * steps / splits);
+    const int e = sc->ek;
+    const float mu = sc->mu;
+    ce_store_tile<T>(tile, i0, j0, m, n, w, w.parts ? w.parts + split * m * w.ld : nullptr,
+                     [&](float v) { return ce_unscale(v, mu, e); });
+}
+
+template <class T, int BM_DX, int BM_DW>
+__global__ __launch_bounds__(256) void k_ced_products(CeBoth b) {
+    __shared__ __align__(16) char lds[CeDirect<T, true, true, 64>::kBytes];
+    // The product whose blocks take longer begins.
+    const int64_t dx = b.dx_tiles * b.dx_splits, dw = b.dw_tiles * b.dw_splits;
+    const bool dw_first = b.rows / b.dw_splits > b.classes / b.dx_splits;
+    const int64_t at = blockIdx.x, first = dw_first ? dw : dx;
+    if ((at < first) != dw_first)
+        ced_product<T, false, BM_DX>(lds, b.g, b.w, b.dx, dw_first ? at - dw : at, b.dx_tiles,
+                                     b.dx_splits, b.rows, b.cols, b.classes, b.scalars);
+    else
+        ced_product<T, true, BM_DW>(lds, b.g, b.x, b.dw, dw_first ? at : at - dx, b.dw_tiles,
+                                    b.dw_splits, b.classes, b.cols, b.rows, b.scalars);
+}
+
+template <class F>
+static int ced_types(int32_t dtype, F&& f) {
+    if (dtype == SPOPT_DTYPE_F32)
+        f(float{});
+    else if (dtype == SPOPT_DTYPE_F16)
+        f(_Float16{});
+    else
+        f(__bf16{});
+    SPOPT_LAUNCHED();
+    return SPOPT_OK;
+}
+
+typedef std::integral_constant<int, 16> Rows16;
+typedef std::integral_constant<int, 64> Rows64;
+
+template <class F>
+static void ced_rows(int tile, F&& f) {
+    if (tile == 16)
+        f(Rows16{});
+    else
+        f(Rows64{});
+}
+
+int ce_direct_loss(int32_t dtype, int tile, const CeSide& x, const CeSide& w, const CeLogits& l,
+                   hipStream_t s) {
+    return ced_types(dtype, [&](auto t) {
+        ced_rows(tile, [&](auto bm) {
+            const int64_t tm = ceil_div(x.rows, bm.value), tn = ceil_div(w.rows, 64);
+            k_ced_logits<decltype(t), kCeLoss, bm.value>
+                <<<(unsigned)(tm * tn), 256, 0, s>>>(x, w, l, tn, tm, CeRows{}, nullptr);
+        });
+    });
+}
+
+int ce_direct_grad(int32_t dtype, int tile, const CeSide& x, const CeSide& w,
+                   const CeLogits& l, const CeRows& rows, CeScalars* scalars, hipStream_t s) {
+    return ced_types(dtype, [&](auto t) {
+        ced_rows(tile, [&](auto bm) {
+            const int64_t tm = ceil_div(x.rows, bm.value), tn = ceil_div(w.rows, 64);
+            k_ced_logits<decltype(t), kCeGrad, bm.value>
+                <<<(unsigned)(tm * tn), 256, 0, s>>>(x, w, l, tn, tm, rows, scalars);
+        });
+    });
+}
+
+int ce_direct_products(int32_t dtype, const CeBoth& b, hipStream_t s) {
+    const int64_t blocks = b.dx_tiles * b.dx_splits + b.dw_tiles * b.dw_splits;
+    return ced_types(dtype, [&](auto t) {
+        ced_rows(b.dx_tile, [&](auto bx) {
+            ced_rows(b.dw_tile, [&](auto bw) {
+                k_ced_products<decltype(t), bx.value, bw.value>
+                    <<<(unsigned)blocks, 256, 0, s>>>(b);
+            });
+        });
+    });
+}
+
+}  // namespace spopt

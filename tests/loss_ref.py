@@ -21,7 +21,8 @@ def product_bound(a, b, k, split):
     """How far a product of matrices a (m x k) and b (k x n) may be off, from magnitudes."""
     a, b = a.abs(), b.abs()
     m = a @ b
-    e = 2 * U * (k + 8) * m
+    # below 2^-126 a step is 2^-149 whatever the value: one for each product and each addition
+    e = 2 * U * (k + 8) * m + 2 * (k + 8) * 2.0 ** -149
     if split:
         # a = hi + lo + r: |r| <= 2^-22 |a|, or half of float16's smallest step at a scale that
         # brings the largest value to 2^14 at least; lo lo, left out, is 2^-22 |a b| at most
