@@ -37,7 +37,7 @@ struct CeProduct {
     CeOperand p, q;
     int64_t m, n;     // the result's rows and columns
     int64_t steps;    // of the inner axis, 64 values each (32 split)
-    int splits;       // parts of the inner axis
+    int splits;       // parts of the inner axis, or (logits) of the tiles of classes
     int64_t tiles_m, tiles_n;
 };
 
@@ -139,27 +139,41 @@ struct CeTile {
         wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         wi = (wv / TL::WGN) * WM;
         wj = (wv % TL::WGN) * WN;
+    }
+
+    __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int x = 0; x < FM; ++x)
 #pragma unroll
             for (int y = 0; y < FN; ++y) acc[x][y] = float4v{0.f, 0.f, 0.f, 0.f};
     }
 
-    // Steps [k0, k1) of the inner axis, at least one.
-    __device__ __forceinline__ void run(T* lds, const CeProduct& c, int64_t i0, int64_t j0,
-                                        int64_t k0, int64_t k1) {
+    // Tiles [t0, t1) of a row of tiles, steps [k0, k1) of the inner axis for each (one
+    // at least): `done(t)` where a tile's sums are there.  The loads run on from
+    // tile to tile: the next one's are on their way while this one's sums are dealt
+    // with.
+    template <class F>
+    __device__ __forceinline__ void run(T* lds, const CeProduct& c, int64_t i0, int64_t t0,
+                                        int64_t t1, int64_t k0, int64_t k1, F done) {
         Feed<TP, BM, kLoadsP> fp;
         Feed<TQ, BN, kLoadsQ> fq;
         fp.init(c.p, i0, lane, wv, false);
-        fq.init(c.q, j0, lane, wv, !TQ);
+        fq.init(c.q, t0 * BN, lane, wv, !TQ);
         constexpr int kLoads = kLoadsP + kLoadsQ;
+        int64_t bt = t0, bk = k0;
         // Past the end the last step is brought again, so that every wait counts
         // the same loads; nothing reads it.
-        auto stage = [&](int buf, int64_t k) {
-            if (k >= k1) k = k1 - 1;
+        auto stage = [&](int buf) {
             T* const to = lds + buf * TL::kStage;
-            fp.bring(k, to, wv);
-            fq.bring(k, to + BM * kTile, wv);
+            fp.bring(bk, to, wv);
+            fq.bring(bk, to + BM * kTile, wv);
+            if (bk + 1 < k1) {
+                ++bk;
+            } else if (bt + 1 < t1) {
+                ++bt;
+                bk = k0;
+                fq.init(c.q, bt * BN, lane, wv, !TQ);
+            }
         };
         vec8 fa0[FM], fb0[FN], fa1[FM], fb1[FN];
         auto operands = [&](int buf, int kk, vec8 (&fa)[FM], vec8 (&fb)[FN]) {
@@ -172,26 +186,33 @@ struct CeTile {
         };
         int buf = 0;
 #pragma unroll
-        for (int k = 0; k < TL::STAGES - 1; ++k) stage(k, k0 + k);
-        for (int64_t k = k0; k < k1; ++k) {
-            // This stage's loads have landed in every wave, and every wave has
-            // read the stage before, whose place the next loads take.
-            wait_stage<(TL::STAGES - 2) * kLoads>();
-            stage(buf == 0 ? TL::STAGES - 1 : buf - 1, k + TL::STAGES - 1);
-            operands(buf, 0, fa0, fb0);
-            multiply(fa0, fb0);
-            operands(buf, 1, fa1, fb1);
-            if constexpr (SPLIT) {
-                multiply(fa0, fb1);
-                multiply(fa1, fb0);
-            } else {
-                multiply(fa1, fb1);
+        for (int k = 0; k < TL::STAGES - 1; ++k) stage(k);
+        for (int64_t t = t0; t < t1; ++t) {
+            clear();
+            for (int64_t k = k0; k < k1; ++k) {
+                // This stage's loads have landed in every wave, and every wave has
+                // read the stage before, whose place the next loads take.
+                wait_stage<(TL::STAGES - 2) * kLoads>();
+                stage(buf == 0 ? TL::STAGES - 1 : buf - 1);
+                operands(buf, 0, fa0, fb0);
+                multiply(fa0, fb0);
+                operands(buf, 1, fa1, fb1);
+                if constexpr (SPLIT) {
+                    multiply(fa0, fb1);
+                    multiply(fa1, fb0);
+                } else {
+                    multiply(fa1, fb1);
+                }
+                buf = buf + 1 == TL::STAGES ? 0 : buf + 1;
             }
-            buf = buf + 1 == TL::STAGES ? 0 : buf + 1;
+            done(t);
         }
         wait_loads<0>();
     }
 
+    static constexpr int kRowLanes = 16;
+    __device__ __forceinline__ float at(int x, int y, int e) const { return acc[x][y][e]; }
+    __device__ __forceinline__ float4v four(int x, int y) const { return acc[x][y]; }
     // Row x and column (y, e) of this lane, within the tile.
     __device__ __forceinline__ int row_of(int x) const { return wi + x * 16 + (lane & 15); }
     __device__ __forceinline__ int col_of(int y) const {
@@ -199,45 +220,254 @@ struct CeTile {
     }
 };
 
+// A tile of 256 x 256 by four waves, 128 x 128 each, which read two thirds of what
+// eight would from LDS.  A wave is alone on its SIMD, so that what it waits for
+// is laid between its products (of 32 x 32, whose issue leaves it room): while
+// one half of a stage is multiplied, the other's operands are read, and the loads
+// of the stage after next go out, P's in the first half and Q's in the second.  LDS
+// (all 160 KB) has three places for P and two for Q, so that P's go to one that is
+// free already, and Q's to what this step's first half has emptied.  One barrier a
+// stage, of 64 matrix instructions a wave.
+template <class T, bool TP, bool TQ>
+struct CeWide {
+    static constexpr int BM = 256, BN = 256, WGN = 2, FM = 4, FN = 16, kRowLanes = 32;
+    static constexpr int kRow = TQ ? 4 : 8;
+    static constexpr int kSide = 256 * kTile;  // values of a side's stage
+    typedef T vec8 __attribute__((ext_vector_type(8)));
+    typedef T vec4 __attribute__((ext_vector_type(4)));
+
+    // Where row v of a turned side has its 16 columns from 16 u on: at u ^ turn(v).
+    // Two such parts of four rows then lie in different eighths of 256 bytes.
+    static __device__ __forceinline__ int turn(int v) { return (v & 3) << 1; }
+
+    // A side's eight loads a stage: each lane's distance from a base that is the
+    // same for the wave.
+    template <bool TURN>
+    struct Feed {
+        const char* base;
+        int64_t ld, last;
+        uint32_t off[8];
+        __device__ __forceinline__ void init(const CeOperand& o, int64_t first, int lane, int wv,
+                                             bool pair) {
+            ld = o.ld * 2;
+            last = o.last;
+            base = (const char*)o.base + (TURN ? 0 : first * ld);
+#pragma unroll
+            for (int l = 0; l < 8; ++l) {
+                if constexpr (TURN) {
+                    const int v = (l * 4 + wv) * 2 + (lane >> 5), slot = lane & 31;
+                    int64_t c = first + (((slot >> 1) ^ turn(v)) * 2 + (slot & 1)) * 8;
+                    if (c > o.cols - 8) c = o.cols - 8;
+                    off[l] = (uint32_t)(v * ld + c * 2);
+                } else {
+                    const int at = (l * 4 + wv) * 8 + (lane >> 3), in = at & 31;
+                    int64_t r = pair ? at - in + (in >> 4) * 16 + (in >> 2 & 1) * 8 +
+                                           (in >> 3 & 1) * 4 + (in & 3)
+                                     : at;
+                    if (r > last - first) r = last - first;
+                    off[l] = (uint32_t)(r * ld + ((lane & 7) ^ (lane >> 3)) * 16);
+                }
+            }
+        }
+        // Load l of step k.
+        __device__ __forceinline__ void bring(int l, int64_t k, T* to, int lane, int wv) const {
+            const char* from = base + (TURN ? k * 64 * ld : k * 128);
+            uint32_t o = off[l];
+            if constexpr (TURN) {
+                // Rows past the last bring that one: g's zeros meet it.
+                const int v = (l * 4 + wv) * 2 + (lane >> 5);
+                const int over = v + (int)(k * 64 - last);
+                o -= (uint32_t)(over > 0 ? over : 0) * (uint32_t)ld;
+            }
+            load_lds16_from(from, o, to + (l * 4 + wv) * 512);
+        }
+    };
+
+    int lane, wv, wi, wj;
+    float16v acc[4][4];
+
+    __device__ __forceinline__ void init() {
+        lane = lane_id();
+        wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        wi = (wv >> 1) * 128;
+        wj = (wv & 1) * 128;
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[x][y][e] = 0.f;
+    }
+
+    // The operand of 32 rows (or columns) from `first` on, 16 values of the inner
+    // axis: the kk-th of a stage's four.
+    template <bool TURN>
+    __device__ __forceinline__ vec8 operand(const T* l, int first, int kk) const {
+        if constexpr (TURN) {
+            const int row = (lane >> 5) * 8 + ((lane & 15) >> 2);
+            const T* a = l + (kk * 16 + row) * 256 +
+                         ((first / 16 + (lane >> 4 & 1)) ^ turn(row)) * 16 + (lane & 3) * 4;
+            const vec4 lo = __builtin_bit_cast(vec4, read_turned((const _Float16*)a));
+            const vec4 hi = __builtin_bit_cast(vec4, read_turned((const _Float16*)(a + 4 * 256)));
+            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        } else {
+            return *(const vec8*)(l + (first + (lane & 31)) * kTile +
+                                  ((kk * 2 + (lane >> 5)) ^ (lane & 7)) * 8);
+        }
+    }
+
+    // Tile t0 alone: a loop over tiles around it would take registers that it lacks.
+    template <class F>
+    __device__ __forceinline__ void run(T* lds, const CeProduct& c, int64_t i0, int64_t t0, int64_t,
+                                        int64_t k0, int64_t k1, F done) {
+        const int64_t j0 = t0 * 256;
+        clear();
+        Feed<TP> fp;
+        Feed<TQ> fq;
+        fp.init(c.p, i0, lane, wv, false);
+        fq.init(c.q, j0, lane, wv, !TQ);
+        // Past the end the last step is brought again; nothing reads it.
+        auto bring_p = [&](int l, int slot, int64_t k) {
+            if (k >= k1) k = k1 - 1;
+            fp.bring(l, k, lds + slot * kSide, lane, wv);
+        };
+        auto bring_q = [&](int l, int slot, int64_t k) {
+            if (k >= k1) k = k1 - 1;
+            fq.bring(l, k, lds + (3 + slot) * kSide, lane, wv);
+        };
+        vec8 a[4][4], b[4][4];
+        // Operand g of half h: in the order in which they are met.
+        auto read = [&](int g, int ps, int qs, int h) {
+            const int kk = 2 * h + g / 8, i = g % 8;
+            if (i < 4)
+                b[kk][i] = operand<TQ>(lds + (3 + qs) * kSide, wj + i * 32, kk);
+            else
+                a[kk][i - 4] = operand<TP>(lds + ps * kSide, wi + (i - 4) * 32, kk);
+        };
+        // 32 products of half h, and between them the other half's operands (in
+        // slots ps and qs) and eight loads of step k.
+        auto half = [&](auto h_, int ps, int qs, int slot, int64_t k) {
+            constexpr int h = decltype(h_)::value;
+#pragma unroll
+            for (int g = 0; g < 16; ++g) {
+                if (h == 0 && g % 2 == 0) bring_p(g / 2, slot, k);
+                if (h == 1 && g < 8) bring_q(g, slot, k);
+                if (g < 4) {
+                    read(2 * g, ps, qs, 1 - h);
+                    read(2 * g + 1, ps, qs, 1 - h);
+                } else if (g < 12) {
+                    read(g + 4, ps, qs, 1 - h);
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int kk = 2 * h + g / 8, x = g % 8 / 2, y = g % 2 * 2 + u;
+                    acc[x][y] = matrix_32x32x16(b[kk][y], a[kk][x], acc[x][y]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        typedef std::integral_constant<int, 0> First;
+        typedef std::integral_constant<int, 1> Second;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int l = 0; l < 8; ++l) {
+                bring_p(l, k, k0 + k);
+                bring_q(l, k, k0 + k);
+            }
+        wait_stage<16>();
+#pragma unroll
+        for (int g = 0; g < 16; ++g) read(g, 0, 0, 0);
+        int ps = 0, qs = 0;
+        for (int64_t k = k0; k < k1; ++k) {
+            const int p1 = ps == 2 ? 0 : ps + 1, p2 = ps == 0 ? 2 : ps - 1;
+            // P's rows of the step after next go to where the step before had its own.
+            half(First{}, ps, qs, p2, k + 2);
+            // All but those have landed in every wave, and every wave has read this step.
+            wait_stage<8>();
+            half(Second{}, p1, qs ^ 1, qs, k + 2);
+            ps = p1;
+            qs ^= 1;
+        }
+        wait_stage<0>();
+        done(t0);
+    }
+
+    __device__ __forceinline__ float at(int x, int y, int e) const {
+        return acc[x][y / 4][y % 4 * 4 + e];
+    }
+    __device__ __forceinline__ float4v four(int x, int y) const {
+        return float4v{at(x, y, 0), at(x, y, 1), at(x, y, 2), at(x, y, 3)};
+    }
+    __device__ __forceinline__ int row_of(int x) const { return wi + x * 32 + (lane & 31); }
+    __device__ __forceinline__ int col_of(int y) const {
+        const int g = y % 4, h = lane >> 5;
+        return wj + y / 4 * 32 + (kRow == 8 ? (g >> 1) * 16 + h * 8 + (g & 1) * 4 : g * 8 + h * 4);
+    }
+};
+
+// The tile's struct: four waves of 128 x 128 where it is 256 wide.
+template <class T, bool SPLIT, bool TP, bool TQ, class TL>
+using CeTileOf = std::conditional_t<TL::BM == 256, CeWide<T, TP, TQ>, CeTile<T, SPLIT, TP, TQ, TL>>;
+
+// A block takes one of `parts` parts of the piece's tiles of classes, for one tile
+// of rows: their maxima and sums stay in registers from tile to tile.  Blocks of
+// the same part follow one another, so that an XCD's L2 sees W's rows once.
 template <class T, bool SPLIT, int MODE, class TL>
-__global__ __launch_bounds__(TL::kThreads) void k_ce_logits(CeProduct c, CeLogits w) {
+__global__ __launch_bounds__(TL::kThreads)
+    __attribute__((amdgpu_waves_per_eu(TL::BM == 256 ? 1 : 2))) void k_ce_logits(CeProduct c,
+                                                                                 CeLogits w) {
     extern __shared__ __align__(16) char lds_raw[];
-    typedef CeTile<T, SPLIT, false, false, TL> Tile;
+    typedef CeTileOf<T, SPLIT, false, false, TL> Tile;
     constexpr int BM = TL::BM, BN = TL::BN;
-    int64_t ti, tj;
-    ce_place(xcd_order(blockIdx.x, gridDim.x), c.tiles_m, c.tiles_n, &ti, &tj);
-    const int64_t i0 = ti * BM, j0 = tj * BN;
+    const int64_t b = xcd_order(blockIdx.x, gridDim.x);
+    int64_t part = b / c.tiles_m, ti = b % c.tiles_m;
+    if (BM == 256) ce_place(b, c.tiles_m, c.tiles_n, &ti, &part);
+    const int64_t i0 = ti * BM;
+    const int64_t t0 = part * c.tiles_n / c.splits, t1 = (part + 1) * c.tiles_n / c.splits;
     Tile tile;
     tile.init();
-    tile.run((T*)lds_raw, c, i0, j0, 0, c.steps);
     const int e = SPLIT ? -(w.scalars->ex + w.scalars->ew) : 0;
-    auto scale = [&](float v) { return SPLIT ? ldexpf(v, e) : v; };
-    if constexpr (MODE == kCeLoss)
-        ce_loss_tile<BM, BN, TL::WGN>(tile, (float*)lds_raw, i0, j0, tj, c.m, c.n, w, scale);
-    else
-        ce_grad_tile<T, SPLIT, BN>(tile, i0, j0, c.m, c.n, w, scale,
-                                   [&](int64_t i) { return w.coef[i]; });
+    if constexpr (MODE == kCeLoss) {
+        CeRowSums<Tile> sums;
+        sums.init(tile, w, i0, c.m, c.n, e);
+        tile.run((T*)lds_raw, c, i0, t0, t1, 0, c.steps, [&](int64_t t) {
+            sums.template add<BN, TL::WGN>(tile, w, i0, t * BN, c.n);
+        });
+        sums.template store<BM, TL::WGN>(tile, w, (float*)lds_raw, i0, c.m, w.first_part + part);
+    } else {
+        CeRowGrads<Tile> grads;
+        grads.init(tile, w, i0, c.m, c.n, e, [&](int64_t i) { return w.coef[i]; });
+        tile.run((T*)lds_raw, c, i0, t0, t1, 0, c.steps, [&](int64_t t) {
+            grads.template store<T, SPLIT, BN>(tile, w, i0, t * BN, c.n);
+        });
+    }
 }
 
 template <class T, bool SPLIT, int MODE, class TL>
-__global__ __launch_bounds__(TL::kThreads) void k_ce_product(CeProduct c, CeResult w,
-                                                             const CeScalars* sc) {
+__global__ __launch_bounds__(TL::kThreads)
+    __attribute__((amdgpu_waves_per_eu(TL::BM == 256 ? 1 : 2))) void k_ce_product(
+        CeProduct c, CeResult w, const CeScalars* sc) {
     extern __shared__ __align__(16) char lds_raw[];
-    typedef CeTile<T, SPLIT, MODE == kCeDw, true, TL> Tile;
+    typedef CeTileOf<T, SPLIT, MODE == kCeDw, true, TL> Tile;
     typedef std::conditional_t<SPLIT, float, T> O;
     const int64_t tiles = c.tiles_m * c.tiles_n;
     const int64_t b = xcd_order(blockIdx.x, gridDim.x);
     const int64_t split = b / tiles;
     int64_t ti, tj;
     ce_place(b % tiles, c.tiles_m, c.tiles_n, &ti, &tj);
-    const int64_t i0 = ti * TL::BM, j0 = tj * TL::BN;
+    const int64_t i0 = ti * TL::BM;
     const int64_t k0 = split * c.steps / c.splits, k1 = (split + 1) * c.steps / c.splits;
     Tile tile;
     tile.init();
-    if (k0 < k1) tile.run((T*)lds_raw, c, i0, j0, k0, k1);
+    // A last, shorter piece of the classes may leave a split nothing to add.
+    if (k0 == k1) return;
+    tile.run((T*)lds_raw, c, i0, tj, tj + 1, k0, k1, [](int64_t) {});
     const int e = sc->ek + (SPLIT ? MODE == kCeDx ? sc->ew : sc->ex : 0);
     const float mu = sc->mu;
-    ce_store_tile<O>(tile, i0, j0, c.m, c.n, w,
+    ce_store_tile<O>(tile, i0, tj * TL::BN, c.m, c.n, w,
                      w.parts == nullptr ? nullptr : w.parts + split * c.m * w.ld,
                      [&](float v) { return ce_unscale(v, mu, e); });
 }
@@ -515,7 +745,26 @@ __global__ __launch_bounds__(256) void k_ce_check(const T* x, int64_t ld, int64_
 
 typedef Tiling<64, 64, 2, 2, 2> CeS;
 typedef Tiling<128, 128, 2, 4, 2> CeM;
-typedef Tiling<256, 256, 2, 4, 2> CeL;
+typedef Tiling<256, 256, 2, 2, 2> CeL;
+
+// Into how many parts the tiles of classes are shared out for each of tiles_m tiles
+// of rows: as many blocks as the card holds at once (two of 128 a CU, four of 64),
+// and parts alike; each by itself of the largest.
+static int ce_parts(int64_t tiles_m, int64_t tiles_n, int tile) {
+    if (tile == 256) return (int)tiles_n;
+    const int64_t room = tile == 128 ? 512 : 1024;
+    int64_t best = 1, least = INT64_MAX;
+    const int64_t most = tiles_n < 1024 ? tiles_n : 1024;
+    for (int64_t p = 1; p <= most; ++p) {
+        // Tiles a place goes through one after another, and a little for each part.
+        const int64_t cost = 64 * ceil_div(tiles_m * p, room) * ceil_div(tiles_n, p) + p;
+        if (cost < least) {
+            least = cost;
+            best = p;
+        }
+    }
+    return (int)best;
+}
 
 // How a product is tiled, and into how many parts its inner axis is cut.
 struct CePlan {
@@ -531,10 +780,11 @@ static CePlan ce_plan(int64_t m, int64_t n, int64_t steps, bool cut, bool split)
     CePlan best{64, 1, INFINITY};
     const struct { int b; double us; } kind[3] = {{64, 0.2}, {128, 0.5}, {256, 1.8}};
     for (const auto& k : kind) {
+        if (split && k.b == 256) break;
         const int64_t tiles = ceil_div(m, k.b) * ceil_div(n, k.b);
         for (int s = 1; s <= (cut ? 32 : 1); s *= 2) {
             if (s > 1 && steps < 4 * s) break;
-            if (tiles * s > (1 << 22) && !(k.b == 256 && s == 1)) continue;
+            if (tiles * s > (1 << 22) && !(k.b == (split ? 128 : 256) && s == 1)) continue;
             const double us = (double)ceil_div(tiles * s, 256) * (double)(ceil_div(steps, s) + 2) *
                                   k.us * (split ? 1.5 : 1.) +
                               (s > 1 ? 3. + (double)s * (double)m * (double)n * 8. / 5e6 : 0.);
@@ -600,7 +850,7 @@ struct CeRun {
     bool direct;         // the kernels of cross_entropy_direct.hip
     int64_t piece;
     CePlan logits, dx, dw;
-    int64_t tiles;       // of classes, in the forward pass
+    int64_t parts;       // of the classes, in the forward pass
 };
 
 // As ce_plan, for the direct kernels: an inner step takes a tile of 16 and 64
@@ -636,7 +886,7 @@ static CeRun ce_run(const CeShape& s, bool backward) {
     d.s = p.s = s;
     d.direct = true;
     d.piece = ceil_div(s.classes, 64) * 64;
-    d.tiles = ceil_div(s.classes, 64);
+    d.parts = ceil_div(s.classes, 64);
     d.logits = ce_direct_plan(s, s.rows, s.classes, s.cols, false);
     p.piece = ce_piece(s, backward);
     const int64_t inner = s.split ? 32 : 64;
@@ -663,7 +913,8 @@ static CeRun ce_run(const CeShape& s, bool backward) {
     if (fits && us_d <= 1.1 * us_p) return d;
     for (int64_t v = 0; v < s.classes; v += p.piece) {
         const int64_t n = s.classes - v < p.piece ? s.classes - v : p.piece;
-        p.tiles += ceil_div(n, p.logits.tile);
+        p.parts += ce_parts(ceil_div(s.rows, p.logits.tile), ceil_div(n, p.logits.tile),
+                            p.logits.tile);
     }
     return p;
 }
@@ -683,8 +934,8 @@ static size_t ce_layout(const CeRun& r, bool backward, char* base, CeBuffers* b)
         b->w = take((size_t)(r.piece * s.cols_p * s.value) * 2);
     }
     if (!backward) {
-        b->parts = (float2*)take((size_t)(r.tiles * s.rows) * 8);
-        b->sums = (float*)take((size_t)(r.tiles * s.rows) * 4);
+        b->parts = (float2*)take((size_t)(r.parts * s.rows) * 8);
+        b->sums = (float*)take((size_t)(r.parts * s.rows) * 4);
         b->at_target = (float*)take((size_t)s.rows * 4);
         b->row_loss = (float*)take((size_t)s.rows * 4);
         return at;
@@ -719,19 +970,21 @@ static void ce_types(int32_t dtype, F&& f) {
         f(__bf16{}, std::false_type{});
 }
 
-template <class F>
+template <bool SPLIT, class F>
 static void ce_tilings(int tile, F&& f) {
-    if (tile == 64)
+    if (tile == 64) {
         f(CeS{});
-    else if (tile == 128)
+    } else if (SPLIT || tile == 128) {
         f(CeM{});
-    else
-        f(CeL{});
+    } else {
+        if constexpr (!SPLIT) f(CeL{});
+    }
 }
 
 template <class K, class TL, class... A>
 static int ce_launch(K kernel, TL, int64_t blocks, hipStream_t s, const A&... a) {
-    constexpr int bytes = TL::STAGES * TL::kStage * 2;
+    // The 256 tile holds three stages of one side and two of the other.
+    constexpr int bytes = TL::BM == 256 ? 160 * 1024 : TL::STAGES * TL::kStage * 2;
     if constexpr (bytes > 64 * 1024) {
         SPOPT_HIP(hipFuncSetAttribute((const void*)kernel,
                                       hipFuncAttributeMaxDynamicSharedMemorySize, bytes));
@@ -744,14 +997,14 @@ static int ce_launch(K kernel, TL, int64_t blocks, hipStream_t s, const A&... a)
 template <int MODE>
 static int ce_logits(const CeRun& r, CeProduct c, const CeLogits& w, hipStream_t s) {
     int rc = SPOPT_OK;
-    c.splits = 1;
     c.tiles_m = ceil_div(c.m, r.logits.tile);
     // g's columns beyond the piece's last class are written too, as zeros.
     c.tiles_n = ceil_div(MODE == kCeGrad ? w.cols_p : c.n, r.logits.tile);
+    c.splits = ce_parts(c.tiles_m, c.tiles_n, r.logits.tile);
     ce_types(r.s.dtype, [&](auto t, auto split) {
-        ce_tilings(r.logits.tile, [&](auto tl) {
+        ce_tilings<decltype(split)::value>(r.logits.tile, [&](auto tl) {
             rc = ce_launch(k_ce_logits<decltype(t), decltype(split)::value, MODE, decltype(tl)>,
-                           tl, c.tiles_m * c.tiles_n, s, c, w);
+                           tl, c.tiles_m * c.splits, s, c, w);
         });
     });
     return rc;
@@ -765,7 +1018,7 @@ static int ce_product(const CeRun& r, const CePlan& plan, CeProduct c, const CeR
     c.tiles_m = ceil_div(c.m, plan.tile);
     c.tiles_n = ceil_div(c.n, plan.tile);
     ce_types(r.s.dtype, [&](auto t, auto split) {
-        ce_tilings(plan.tile, [&](auto tl) {
+        ce_tilings<decltype(split)::value>(plan.tile, [&](auto tl) {
             rc = ce_launch(k_ce_product<decltype(t), decltype(split)::value, MODE, decltype(tl)>,
                            tl, c.tiles_m * c.tiles_n * c.splits, s, c, w, sc);
         });
@@ -783,7 +1036,7 @@ static unsigned ce_grid(int64_t items) {
 static int ce_operand(const CeShape& s, const void* a, int64_t ld, int64_t rows, int64_t rows_p,
                       bool copy, const int64_t* targets, int64_t ignored, const uint32_t* amax,
                       int n_amax, int* exponent, void* to, CeOperand* o, hipStream_t stream) {
-    if (!copy && !s.split && s.cols % 64 == 0 && ld % 8 == 0 && aligned16(a)) {
+    if (!copy && !s.split && s.cols % 64 == 0 && ld % 8 == 0 && ld <= (1 << 21) && aligned16(a)) {
         *o = CeOperand{a, ld, rows - 1, s.cols_p};
         return SPOPT_OK;
     }
@@ -946,16 +1199,17 @@ extern "C" int linear_cross_entropy_forward(const void* x, int64_t x_stride, con
                         &b.scalars->ew, b.w, &c.q, s);
         if (!rc) rc = ce_logits<kCeLoss>(r, c, w, s);
         if (rc) return rc;
-        w.first_tile += ceil_div(c.n, r.logits.tile);
+        w.first_part += ce_parts(ceil_div(rows, r.logits.tile), ceil_div(c.n, r.logits.tile),
+                                 r.logits.tile);
     }
     // Rows of few tiles one a thread; and where one block is enough (for up to
     // 128 rows, or 2048 of few tiles), it spares the launch that sums the rows.
-    int per = rows > 64 && r.tiles <= 8 ? 1024 : 64;
+    int per = rows > 64 && r.parts <= 16 ? 1024 : 64;
     while (per <= 64 && per > 1 && rows <= per / 2) per /= 2;
     int64_t blocks = ceil_div(rows, per);
     if (reduction != SPOPT_REDUCE_NONE && blocks == 2) blocks = 1;
     k_ce_join<<<(unsigned)blocks, 1024, 0, s>>>(
-        b.parts, w.sums, b.at_target, targets, ignore_index, rows, r.tiles, classes,
+        b.parts, w.sums, b.at_target, targets, ignore_index, rows, r.parts, classes,
         w.smoothing, per, reduction, b.row_loss, loss, lse);
     SPOPT_LAUNCHED();
     if (reduction != SPOPT_REDUCE_NONE && blocks > 1) {

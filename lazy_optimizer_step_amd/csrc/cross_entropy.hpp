@@ -21,6 +21,15 @@ __device__ __forceinline__ float4v matrix_16x16x32(bhalf8 a, bhalf8 b, float4v c
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
+typedef float float16v __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ float16v matrix_32x32x16(half8 a, half8 b, float16v c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ float16v matrix_32x32x16(bhalf8 a, bhalf8 b, float16v c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
 // What a call's kernels hand on to the next ones.
 struct CeScalars {
     int ex, ew;  // powers of two in front of the operands x and W (float32)
@@ -36,10 +45,10 @@ struct CeLogits {
     int64_t classes;     // of all pieces
     float smoothing;
     // forward
-    float2* parts;       // [tile of classes][row]: maximum, sum of exponentials
-    float* sums;         // [tile of classes][row]: sum of the logits (smoothing only)
+    float2* parts;       // [part of the classes][row]: maximum, sum of exponentials
+    float* sums;         // [part][row]: sum of the logits (smoothing only)
     float* at_target;    // [row]
-    int64_t first_tile;
+    int64_t first_part;
     // backward
     const float* lse;
     const float* coef;   // [row] c_i 2^ek / mu
@@ -58,13 +67,6 @@ __device__ __forceinline__ void ce_place(int64_t t, int64_t tm, int64_t tn, int6
     *tj = in / rows;
 }
 
-// The column of class `target` in a tile whose first is `first`; -1 where it lies
-// far from it.
-__device__ __forceinline__ int ce_column(int64_t target, int64_t first) {
-    const uint64_t j = (uint64_t)target - (uint64_t)first;
-    return j < 4096 ? (int)j : -1;
-}
-
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // exp(z - b), the difference formed before it is scaled.
@@ -72,114 +74,200 @@ __device__ __forceinline__ float exp_less(float z, float b) {
     return __builtin_amdgcn_exp2f((z - b) * kLog2e);
 }
 
-// A tile of the logits, one of `tn` in a row of the piece's, in the lanes of a
-// block's WGN columns of waves: each row's maximum, its sum of exponentials and of
-// logits into the tile's places, and the target's logit into its own.  `red`:
-// 3 BM WGN floats of LDS that no wave reads or awaits any more.
-template <int BM, int BN, int WGN, class Tile, class S>
-__device__ __forceinline__ void ce_loss_tile(Tile& tile, float* red, int64_t i0, int64_t j0,
-                                             int64_t tj, int64_t m, int64_t n, const CeLogits& w,
-                                             S scale) {
-    const bool whole = j0 + BN <= n;
-    const int wn = tile.wv % WGN;
-    __syncthreads();
-#pragma unroll
-    for (int x = 0; x < Tile::FM; ++x) {
-        const int r = tile.row_of(x);
-        const int64_t i = i0 + r;
-        const int t = i < m ? ce_column(w.targets[i], w.first + j0) : -1;
-        float top = -INFINITY, z = 0.f, s = 0.f;
-#pragma unroll
-        for (int y = 0; y < Tile::FN; ++y)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float v = scale(tile.acc[x][y][e]);
-                const int j = tile.col_of(y) + e;
-                if (whole || j0 + j < n) {
-                    z += v;
-                    if (j == t) w.at_target[i] = v;
-                } else {
-                    v = -INFINITY;
-                }
-                tile.acc[x][y][e] = v;
-                top = fmaxf(top, v);
-            }
-        top = fmaxf(top, __shfl_xor(top, 16, kWave));
-        top = fmaxf(top, __shfl_xor(top, 32, kWave));
-        const float base = top == -INFINITY ? 0.f : top;
-#pragma unroll
-        for (int y = 0; y < Tile::FN; ++y)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s += exp_less(tile.acc[x][y][e], base);
-        s += __shfl_xor(s, 16, kWave);
-        s += __shfl_xor(s, 32, kWave);
-        z += __shfl_xor(z, 16, kWave);
-        z += __shfl_xor(z, 32, kWave);
-        if (tile.lane < 16) {
-            red[(wn * 3 + 0) * BM + r] = top;
-            red[(wn * 3 + 1) * BM + r] = s;
-            red[(wn * 3 + 2) * BM + r] = z;
-        }
-    }
-    __syncthreads();
-    for (int r = threadIdx.x; r < BM; r += blockDim.x) {
-        if (i0 + r >= m) break;
-        float top = -INFINITY, s = 0.f, z = 0.f;
-#pragma unroll
-        for (int k = 0; k < WGN; ++k) top = fmaxf(top, red[k * 3 * BM + r]);
-        const float base = top == -INFINITY ? 0.f : top;
-#pragma unroll
-        for (int k = 0; k < WGN; ++k) {
-            s += red[(k * 3 + 1) * BM + r] * exp_less(red[k * 3 * BM + r], base);
-            z += red[(k * 3 + 2) * BM + r];
-        }
-        const int64_t at = (w.first_tile + tj) * m + i0 + r;
-        w.parts[at] = make_float2(top, s);
-        if (w.sums) w.sums[at] = z;
-    }
+// A tile's struct says where its result lies: row_of(x), x < FM, is the row of a
+// lane's values of row x, which kRowLanes lanes apart others share; col_of(y), y <
+// FN, the first of the four adjacent columns of at(x, y, 0 .. 3).
+
+// 2^exponent, within [2^-120, 2^120]: sums of products of split operands lie in
+// [2^-48, 2^50], so that beyond it logits are infinite, or zero beside any exponential.
+__device__ __forceinline__ float ce_logit_scale(int exponent) {
+    return ldexpf(1.f, exponent < -120 ? -120 : exponent > 120 ? 120 : exponent);
 }
 
-// g of a tile of the logits, coef(i) the factor of row i.  Split: hi and lo.
-template <class T, bool SPLIT, int BN, class Tile, class S, class C>
-__device__ __forceinline__ void ce_grad_tile(const Tile& tile, int64_t i0, int64_t j0, int64_t m,
-                                             int64_t n, const CeLogits& w, S scale, C coef_of) {
-    constexpr int V = Tile::kRow;  // adjacent columns of a lane
-    T* const g = (T*)w.g;
-    const bool whole = j0 + BN <= n;
-    const float off = w.smoothing / (float)w.classes, on = 1.f - w.smoothing;
+// The rows of a lane while the classes' tiles go by: the maximum so far, the sum of
+// exponentials under it and the sum of the logits, over this lane's columns.  Maxima
+// are of z / scale, scale a power of two.
+template <class Tile>
+struct CeRowSums {
+    float top[Tile::FM], s[Tile::FM], z[Tile::FM];
+    int target[Tile::FM];  // its column in the piece; -1 where that lies elsewhere
+    float scale, to_bits;  // scale * log2 e
+
+    __device__ __forceinline__ void init(const Tile& tile, const CeLogits& w, int64_t i0,
+                                         int64_t m, int64_t n, int exponent) {
+        scale = ce_logit_scale(exponent);
+        to_bits = scale * kLog2e;
 #pragma unroll
-    for (int x = 0; x < Tile::FM; ++x) {
-        const int64_t i = i0 + tile.row_of(x);
-        if (i >= w.rows_p) continue;
-        const bool row = i < m;
-        const int t = row ? ce_column(w.targets[i], w.first + j0) : -1;
-        const float coef = row ? coef_of(i) : 0.f, lse = row ? w.lse[i] : 0.f;
+        for (int x = 0; x < Tile::FM; ++x) {
+            const int64_t i = i0 + tile.row_of(x);
+            const int64_t t = i < m ? w.targets[i] - w.first : -1;
+            target[x] = t >= 0 && t < n ? (int)t : -1;
+            top[x] = -INFINITY;
+            s[x] = z[x] = 0.f;
+        }
+    }
+
+    // A tile's logits, from column j0 of the piece's n on.
+    template <int BN, int WGN>
+    __device__ __forceinline__ void add(const Tile& tile, const CeLogits& w, int64_t i0, int64_t j0,
+                                        int64_t n) {
+        const bool whole = j0 + BN <= n;
+        const int left = whole ? BN : (int)(n - j0);
 #pragma unroll
-        for (int y = 0; y < Tile::FN; y += V / 4) {
-            const int j = tile.col_of(y);
-            if (j0 + j >= w.cols_p) continue;
-            float v[V];
+        for (int x = 0; x < Tile::FM; ++x) {
+            // Columns past the last weigh nothing.
+            auto value = [&](int y, int e) {
+                return whole || tile.col_of(y) + e < left ? tile.at(x, y, e) : -INFINITY;
+            };
+            float m = top[x];
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                float p = exp_less(scale(tile.acc[x][y + e / 4][e & 3]), lse) - off;
-                if (j + e == t) p -= on;
-                p *= coef;
-                // Rows that do not count may hold anything.
-                v[e] = coef == 0.f || (!whole && j0 + j + e >= n) ? 0.f : p;
+            for (int y = 0; y < Tile::FN; ++y)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) m = fmaxf(m, value(y, e));
+            const float base = m == -INFINITY ? 0.f : m;
+            float sum = s[x] * __builtin_amdgcn_exp2f((top[x] - base) * to_bits);
+#pragma unroll
+            for (int y = 0; y < Tile::FN; ++y)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    sum += __builtin_amdgcn_exp2f((value(y, e) - base) * to_bits);
+            top[x] = m;
+            s[x] = sum;
+            if (w.sums) {
+                float add = 0.f;
+#pragma unroll
+                for (int y = 0; y < Tile::FN; ++y)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (whole || tile.col_of(y) + e < left) add += tile.at(x, y, e);
+                z[x] += add;
             }
-            if constexpr (SPLIT) {
-                float lo[V];
+            // Few waves hold the target of one of their rows.
+            const int t = target[x] - (int)j0;
+            if (ballot(target[x] >= 0 && t >= tile.wj && t < tile.wj + BN / WGN)) {
+                float hit = 0.f;
+                bool found = false;
 #pragma unroll
-                for (int e = 0; e < V; ++e) lo[e] = v[e] - (float)(T)v[e];
-                T* to = g + i * w.ldg + (j0 + j) / 32 * 64 + (j0 + j) % 32;
-                store_v<T, V>(to, v);
-                store_v<T, V>(to + 32, lo);
-            } else {
-                store_v<T, V>(g + i * w.ldg + j0 + j, v);
+                for (int y = 0; y < Tile::FN; ++y)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (tile.col_of(y) + e == t) {
+                            hit = tile.at(x, y, e);
+                            found = target[x] >= 0;
+                        }
+                if (found) w.at_target[i0 + tile.row_of(x)] = hit * scale;
             }
         }
     }
-}
+
+    // The lanes' and waves' sums as one, into the place of part `part`.  `red`: 3 BM
+    // WGN floats of LDS that no wave reads or awaits any more.
+    template <int BM, int WGN>
+    __device__ __forceinline__ void store(const Tile& tile, const CeLogits& w, float* red,
+                                          int64_t i0, int64_t m, int64_t part) {
+        __syncthreads();
+        const int wn = tile.wv % WGN;
+#pragma unroll
+        for (int x = 0; x < Tile::FM; ++x) {
+            float t = top[x], v = s[x], u = z[x];
+#pragma unroll
+            for (int off = Tile::kRowLanes; off < kWave; off <<= 1)
+                t = fmaxf(t, __shfl_xor(t, off, kWave));
+            v *= __builtin_amdgcn_exp2f((top[x] - (t == -INFINITY ? 0.f : t)) * to_bits);
+#pragma unroll
+            for (int off = Tile::kRowLanes; off < kWave; off <<= 1) {
+                v += __shfl_xor(v, off, kWave);
+                u += __shfl_xor(u, off, kWave);
+            }
+            if (tile.lane < Tile::kRowLanes) {
+                const int r = tile.row_of(x);
+                red[(wn * 3 + 0) * BM + r] = t;
+                red[(wn * 3 + 1) * BM + r] = v;
+                red[(wn * 3 + 2) * BM + r] = u;
+            }
+        }
+        __syncthreads();
+        for (int r = threadIdx.x; r < BM; r += blockDim.x) {
+            if (i0 + r >= m) break;
+            float t = -INFINITY, v = 0.f, u = 0.f;
+#pragma unroll
+            for (int k = 0; k < WGN; ++k) t = fmaxf(t, red[k * 3 * BM + r]);
+            const float base = t == -INFINITY ? 0.f : t;
+#pragma unroll
+            for (int k = 0; k < WGN; ++k) {
+                v += red[(k * 3 + 1) * BM + r] *
+                     __builtin_amdgcn_exp2f((red[k * 3 * BM + r] - base) * to_bits);
+                u += red[(k * 3 + 2) * BM + r];
+            }
+            w.parts[part * m + i0 + r] = make_float2(t * scale, v);
+            if (w.sums) w.sums[part * m + i0 + r] = u * scale;
+        }
+    }
+};
+
+// The rows of a lane while g is formed tile by tile.
+template <class Tile>
+struct CeRowGrads {
+    float coef[Tile::FM], lse[Tile::FM];
+    int target[Tile::FM];
+    float scale;
+
+    template <class C>
+    __device__ __forceinline__ void init(const Tile& tile, const CeLogits& w, int64_t i0,
+                                         int64_t m, int64_t n, int exponent, C coef_of) {
+        scale = ce_logit_scale(exponent);
+#pragma unroll
+        for (int x = 0; x < Tile::FM; ++x) {
+            const int64_t i = i0 + tile.row_of(x);
+            const bool row = i < m;
+            const int64_t t = row ? w.targets[i] - w.first : -1;
+            target[x] = t >= 0 && t < n ? (int)t : -1;
+            coef[x] = row ? coef_of(i) : 0.f;
+            lse[x] = row ? w.lse[i] : 0.f;
+        }
+    }
+
+    // g of a tile; split: hi and lo.
+    template <class T, bool SPLIT, int BN>
+    __device__ __forceinline__ void store(const Tile& tile, const CeLogits& w, int64_t i0,
+                                          int64_t j0, int64_t n) const {
+        constexpr int V = Tile::kRow;  // adjacent columns of a lane
+        T* const g = (T*)w.g;
+        const bool whole = j0 + BN <= n;
+        const float off = w.smoothing / (float)w.classes, on = 1.f - w.smoothing;
+#pragma unroll
+        for (int x = 0; x < Tile::FM; ++x) {
+            const int64_t i = i0 + tile.row_of(x);
+            if (i >= w.rows_p) continue;
+            const int t = target[x] < 0 ? -1 : target[x] - (int)j0;
+#pragma unroll
+            for (int y = 0; y < Tile::FN; y += V / 4) {
+                const int j = tile.col_of(y);
+                if (j0 + j >= w.cols_p) continue;
+                float v[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float less = __builtin_fmaf(tile.at(x, y + e / 4, e & 3), scale, -lse[x]);
+                    float p = __builtin_amdgcn_exp2f(less * kLog2e) - off;
+                    if (j + e == t) p -= on;
+                    p *= coef[x];
+                    // Rows that do not count may hold anything.
+                    v[e] = coef[x] == 0.f || (!whole && j0 + j + e >= n) ? 0.f : p;
+                }
+                if constexpr (SPLIT) {
+                    float lo[V];
+#pragma unroll
+                    for (int e = 0; e < V; ++e) lo[e] = v[e] - (float)(T)v[e];
+                    T* to = g + i * w.ldg + (j0 + j) / 32 * 64 + (j0 + j) % 32;
+                    store_v<T, V>(to, v);
+                    store_v<T, V>(to + 32, lo);
+                } else {
+                    store_v<T, V>(g + i * w.ldg + j0 + j, v);
+                }
+            }
+        }
+    }
+};
 
 // Where a product's result goes: sums in float32, [row][ld], added to what is
 // there or not; or (parts NULL) scaled and rounded to where it belongs.
@@ -192,7 +280,7 @@ struct CeResult {
 };
 
 template <class O, class Tile, class S>
-__device__ __forceinline__ void ce_store_tile(const Tile& tile, int64_t i0, int64_t j0, int64_t m,
+__device__ __forceinline__ void ce_store_tile(Tile& tile, int64_t i0, int64_t j0, int64_t m,
                                               int64_t n, const CeResult& w, float* parts,
                                               S scale) {
 #pragma unroll
@@ -205,12 +293,13 @@ __device__ __forceinline__ void ce_store_tile(const Tile& tile, int64_t i0, int6
             if (parts != nullptr) {
                 if (j >= w.ld) continue;
                 float4v* const to = (float4v*)(parts + i * w.ld + j);
-                *to = w.add ? *to + tile.acc[x][y] : tile.acc[x][y];
+                const float4v v = tile.four(x, y);
+                *to = w.add ? *to + v : v;
                 continue;
             }
             float v[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = scale(tile.acc[x][y][e]);
+            for (int e = 0; e < 4; ++e) v[e] = scale(tile.at(x, y, e));
             O* const to = (O*)w.out + i * w.out_ld + j;
             if (j + 4 <= n) {
                 store_v<O, 4>(to, v);

@@ -185,6 +185,9 @@ struct CeDirect {
         __syncthreads();
     }
 
+    static constexpr int kRowLanes = 16;
+    __device__ __forceinline__ float at(int x, int y, int e) const { return acc[x][y][e]; }
+    __device__ __forceinline__ float4v four(int x, int y) const { return acc[x][y]; }
     __device__ __forceinline__ int row_of(int x) const { return wi + x * 16 + (lane & 15); }
     __device__ __forceinline__ int col_of(int y) const {
         return wj + (lane >> 4) * kRow + (kRow == 8 ? y * 4 : y * 16);
@@ -202,9 +205,11 @@ __global__ __launch_bounds__(256) void k_ced_logits(CeSide x, CeSide w, CeLogits
     Tile tile;
     tile.init();
     tile.run(lds, x, w, i0, j0, 0, (x.cols + Tile::kInner - 1) / Tile::kInner);
-    auto same = [](float v) { return v; };
     if constexpr (MODE == kCeLoss) {
-        ce_loss_tile<BM, 64, Tile::WGN>(tile, (float*)lds, i0, j0, tj, x.rows, w.rows, l, same);
+        CeRowSums<Tile> sums;
+        sums.init(tile, l, i0, x.rows, w.rows, 0);
+        sums.template add<64, Tile::WGN>(tile, l, i0, j0, w.rows);
+        sums.template store<BM, Tile::WGN>(tile, l, (float*)lds, i0, x.rows, tj);
     } else {
         CeFactor f;
         f.init(rows, sizeof(T) == 4, (double*)lds, (float*)lds + 64);
@@ -212,8 +217,9 @@ __global__ __launch_bounds__(256) void k_ced_logits(CeSide x, CeSide w, CeLogits
             scalars->ek = f.ek;
             scalars->mu = f.mu;
         }
-        ce_grad_tile<T, false, 64>(tile, i0, j0, x.rows, w.rows, l, same,
-                                   [&](int64_t i) { return f.of(rows, i); });
+        CeRowGrads<Tile> grads;
+        grads.init(tile, l, i0, x.rows, w.rows, 0, [&](int64_t i) { return f.of(rows, i); });
+        grads.template store<T, false, 64>(tile, l, i0, j0, w.rows);
     }
 }
 

@@ -37,6 +37,17 @@ __device__ __forceinline__ void load_lds16(const void* from, void* to) {
                  : "memory");
 }
 
+// The same from `off` bytes behind an address that all lanes share.
+__device__ __forceinline__ void load_lds16_from(const void* from, uint32_t off, void* to) {
+    const uint32_t m0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)to;
+    const uint64_t at = (uint64_t)from;
+    const uint64_t base = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(at >> 32)) << 32 |
+                          (uint32_t)__builtin_amdgcn_readfirstlane((int)at);
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off),
+                 "s"(base), "s"(m0)
+                 : "memory");
+}
+
 __device__ __forceinline__ half4 read_turned(const _Float16* p) {
     typedef short short4v __attribute__((ext_vector_type(4)));
     return __builtin_bit_cast(half4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
