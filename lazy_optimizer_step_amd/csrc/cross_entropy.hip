@@ -486,10 +486,18 @@ __global__ __launch_bounds__(256) void k_ce_gather(const float* parts, int split
         const int64_t i = q / quads, j = q % quads * 4;
         if (j >= cols) continue;
         double s[4] = {};
-        for (int k = 0; k < splits; ++k) {
-            const float4v p = *(const float4v*)(parts + ((int64_t)k * rows + i) * ld + j);
+        const float* from = parts + i * ld + j;
+        // Eight loads on their way at once.
+        for (int k0 = 0; k0 < splits; k0 += 8) {
+            float4v p[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[e] += (double)p[e];
+            for (int k = 0; k < 8; ++k)
+                p[k] = k0 + k < splits ? *(const float4v*)(from + (k0 + k) * rows * ld)
+                                       : float4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[e] += (double)p[k][e];
         }
         float v[4];
 #pragma unroll
@@ -756,8 +764,8 @@ static int ce_parts(int64_t tiles_m, int64_t tiles_n, int tile) {
     int64_t best = 1, least = INT64_MAX;
     const int64_t most = tiles_n < 1024 ? tiles_n : 1024;
     for (int64_t p = 1; p <= most; ++p) {
-        // Tiles a place goes through one after another, and a little for each part.
-        const int64_t cost = 64 * ceil_div(tiles_m * p, room) * ceil_div(tiles_n, p) + p;
+        // Tiles that a place goes through one after another; then the fewest parts.
+        const int64_t cost = ceil_div(tiles_m * p, room) * ceil_div(tiles_n, p);
         if (cost < least) {
             least = cost;
             best = p;
@@ -773,19 +781,23 @@ struct CePlan {
     double us;   // what it is expected to take
 };
 
-// An inner step takes a tile of 64, 128 and 256 about 0.2, 0.5 and 1.8 us of its
-// CU, of split operands half as much again.  Cut products write and read their
-// parts once more, 5 bytes a picosecond.
+// An inner step takes a tile of 64, 128 and 256 about 0.22, 0.45 and 1.6 us of its
+// CU, and what comes before and after two steps more, six of 256's, which is alone
+// on its CU; split operands half as much again.  Cut products write and read
+// their parts once more, 5 bytes a picosecond.  Measured, bfloat16, forward, by
+// tile: 8192 x 512 x 50000 898, 466 and 567 us, 1000 x 2048 x 32000 207, 139 and
+// 133, 4000 x 128 x 10000 40, 37 and 60.
 static CePlan ce_plan(int64_t m, int64_t n, int64_t steps, bool cut, bool split) {
     CePlan best{64, 1, INFINITY};
-    const struct { int b; double us; } kind[3] = {{64, 0.2}, {128, 0.5}, {256, 1.8}};
+    const struct { int b; double us, more; } kind[3] = {
+        {64, 0.22, 2}, {128, 0.45, 2}, {256, 1.6, 6}};
     for (const auto& k : kind) {
         if (split && k.b == 256) break;
         const int64_t tiles = ceil_div(m, k.b) * ceil_div(n, k.b);
         for (int s = 1; s <= (cut ? 32 : 1); s *= 2) {
             if (s > 1 && steps < 4 * s) break;
             if (tiles * s > (1 << 22) && !(k.b == (split ? 128 : 256) && s == 1)) continue;
-            const double us = (double)ceil_div(tiles * s, 256) * (double)(ceil_div(steps, s) + 2) *
+            const double us = (double)ceil_div(tiles * s, 256) * ((double)ceil_div(steps, s) + k.more) *
                                   k.us * (split ? 1.5 : 1.) +
                               (s > 1 ? 3. + (double)s * (double)m * (double)n * 8. / 5e6 : 0.);
             if (us < best.us) best = CePlan{k.b, s, us};
@@ -812,11 +824,14 @@ static CeShape ce_shape(int64_t rows, int64_t cols, int64_t classes, int32_t dty
 }
 
 // Classes at a time.  Forward: copies of W's rows of up to 256 MiB, and grids of
-// up to 2^22 tiles.  Backward: g of up to 512 MiB, for at least 2048 classes.
+// up to 2^22 tiles.  Backward: g of up to 512 MiB, or 256 where rows are short and
+// g's traffic bounds the pass, as the last-level cache then keeps much of it (8192
+// x 128 x 50021 float32 1700 against 1450 us, bfloat16 1080 against 731; 4096 x 1024 x
+// 131072 bfloat16 3225 against 4044); for at least 2048 classes.
 static int64_t ce_piece(const CeShape& s, bool backward) {
     int64_t most = ((int64_t)1 << 28) / (s.cols_p * s.value * 2);
     if (backward) {
-        const int64_t g = ((int64_t)1 << 29) / (s.rows_p * s.value * 2);
+        const int64_t g = ((int64_t)1 << (s.cols <= 512 ? 28 : 29)) / (s.rows_p * s.value * 2);
         most = most < g ? most : g;
     }
     if (most < 2048) most = 2048;
@@ -878,7 +893,7 @@ static CePlan ce_direct_plan(const CeShape& s, int64_t m, int64_t n, int64_t k, 
 // finds the largest; of 16 bits, 4 bytes a value of rows that have a remainder);
 // the direct kernels multiply more slowly, those of float32 far more.  Both sides
 // measured at 114 sizes, forward and backward: the estimates choose the slower one
-// at 7 of 228, by 1.04 to 1.2 times.  4 x 256 x 1000 float32: 18.7 against 28.9 us forward
+// at 19 of 228, by 1.03 to 1.24 times.  4 x 256 x 1000 float32: 18.7 against 28.9 us forward
 // and 25.9 against 39.1 backward; 500 x 256 x 100000 float32: 337 against 176 and
 // 934 against 446.
 static CeRun ce_run(const CeShape& s, bool backward) {
