@@ -167,20 +167,23 @@ SPOPT_API int muon_step(void* params, int32_t pdtype, float* buf, const void* g,
  *             rows that count or their mean, for SPOPT_REDUCE_SUM and _MEAN (0
  *             where no row counts).
  *   lse       float [rows], what the backward pass takes.
- * Types: 16-bit operands are multiplied as they are, with float32 sums.  Each
- * value of float32 operands is taken as two float16 after a power of two that
- * brings the operand's largest finite value (of x: in rows that count) to
- * 2^14: 22 bits, for values below 2^-18 of the largest an absolute 2^-40 of it.
- * The products of the two low parts are left out, sums are float32.  A NaN or
- * an infinity in x makes its row NaN (of 16-bit types an infinity may cancel
- * instead), in weight every row.
+ * Types: 16-bit operands are multiplied as they are, with float32 sums, and so
+ * are float32 ones in small calls.  In others (which is which goes by the sizes
+ * alone) each value of a float32 operand is taken as two float16 after a power of
+ * two that brings the operand's largest finite value (of x: in rows that count) to
+ * 2^14: 22 bits, for values below 2^-18 of the largest an absolute 2^-39 of it.
+ * The products of the two low parts are left out, sums are float32.  A NaN in x
+ * makes its row NaN, in weight every row; an infinity does so too, or leaves an
+ * infinite or a finite value where the formula does.
  * Workspace: device, 16-byte aligned, linear_cross_entropy_workspace_size bytes
- * for the pass (backward 0 or 1).  Inputs with cols a multiple of 64, strides
- * multiples of 8 and 16-byte aligned bases are read in place where they are of
- * 16 bits; others are copied into it, the weight up to 256 MiB at a time.
+ * for the pass (backward 0 or 1).  Small calls read their inputs in place.  In
+ * others those with cols a multiple of 64, strides multiples of 8 and 16-byte
+ * aligned bases are read in place where they are of 16 bits, and the rest (x
+ * always in the backward pass) are copied into the workspace, the weight up to
+ * 256 MiB (or 2048 rows) at a time.
  * Errors: SPOPT_EINVAL (NULL, sizes, a stride below cols, types, reduction,
- * label_smoothing outside [0, 1]), SPOPT_EWORKSPACE; rows up to 2^28, cols to
- * 2^20, classes to 2^30, either matrix to 2^38 values.  SPOPT_VALIDATE reads
+ * label_smoothing outside [0, 1]), SPOPT_EWORKSPACE; rows up to 2^27, cols to
+ * 2^20, classes to 2^30, either matrix to 2^36 values.  SPOPT_VALIDATE reads
  * the targets, the rows of x that count, and weight. */
 SPOPT_API int linear_cross_entropy_workspace_size(int64_t rows, int64_t cols, int64_t classes,
                                                   int32_t dtype, int32_t backward, size_t* bytes);
@@ -203,10 +206,11 @@ SPOPT_API int linear_cross_entropy_forward(const void* x, int64_t x_stride, cons
  *   dweight   classes x cols of `dtype`, with its row stride, or NULL.  Written,
  *             not added to; all zero for rows == 0.
  * None of the outputs may overlap another, an input or the workspace.
- * g is rounded to the operands' type before the products (float32: taken as two
- * float16 like the operands, after a power of two that brings the largest c_i
- * to 2^13); sums are float32, rounded once.  g exists for one piece of the
- * classes at a time, of up to 512 MiB (or 2048 classes).  A row whose target is
+ * g is rounded to the operands' type before the products, with a factor in front
+ * that brings max |c_i| (1 - e) to 2^13 (float32: kept as it is in small calls,
+ * else taken as two float16 like the operands, with that factor); sums are
+ * float32, rounded once.  g exists for one piece of the classes at a time, of up
+ * to 512 MiB (or 2048 classes).  A row whose target is
  * neither a class nor ignore_index makes its row of dx and all of dweight NaN.
  * Workspace, errors and validation as above. */
 SPOPT_API int linear_cross_entropy_backward(

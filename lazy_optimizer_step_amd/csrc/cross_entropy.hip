@@ -760,12 +760,14 @@ typedef Tiling<256, 256, 2, 2, 2> CeL;
 // and parts alike; each by itself of the largest.
 static int ce_parts(int64_t tiles_m, int64_t tiles_n, int tile) {
     if (tile == 256) return (int)tiles_n;
-    const int64_t room = tile == 128 ? 512 : 1024;
+    const int64_t room = tile == 128 ? 512 : 1024, fewest = ceil_div(tiles_m, room);
     int64_t best = 1, least = INT64_MAX;
-    const int64_t most = tiles_n < 1024 ? tiles_n : 1024;
-    for (int64_t p = 1; p <= most; ++p) {
-        // Tiles that a place goes through one after another; then the fewest parts.
-        const int64_t cost = ceil_div(tiles_m * p, room) * ceil_div(tiles_n, p);
+    // By how many times the blocks fill the card: the tiles that a place goes
+    // through one after another.
+    for (int64_t rounds = fewest; rounds < fewest + 8; ++rounds) {
+        int64_t p = rounds * room / tiles_m;
+        if (p > tiles_n) p = tiles_n;
+        const int64_t cost = rounds * ceil_div(tiles_n, p);
         if (cost < least) {
             least = cost;
             best = p;
@@ -923,7 +925,8 @@ static CeRun ce_run(const CeShape& s, bool backward) {
         us_p += copies ? 0. : (double)(s.rows * s.cols) * 4. / 4.2e6;
     }
     // Grids and g have to fit at once.
-    const int64_t blocks = ceil_div(s.rows, 16) * ceil_div(s.classes, 64);
+    const int64_t blocks = ceil_div(s.rows, 16) * ceil_div(s.classes, 64) +
+                           (ceil_div(s.rows, 16) + ceil_div(s.classes, 16)) * ceil_div(s.cols, 64);
     const bool fits = blocks < (1 << 22) && s.rows_p <= ((int64_t)1 << 29) / (d.piece * 2 * s.value);
     if (fits && us_d <= 1.1 * us_p) return d;
     for (int64_t v = 0; v < s.classes; v += p.piece) {
@@ -967,8 +970,8 @@ static int ce_check_size(const char* what, int64_t rows, int64_t cols, int64_t c
                          int32_t dtype) {
     if (dtype != SPOPT_DTYPE_F32 && dtype != SPOPT_DTYPE_BF16 && dtype != SPOPT_DTYPE_F16)
         return fail(SPOPT_EINVAL, "%s: unknown element type %d", what, dtype);
-    constexpr int64_t kMost = (int64_t)1 << 38;
-    if (rows < 0 || cols < 1 || classes < 1 || rows > (1 << 28) || cols > (1 << 20) ||
+    constexpr int64_t kMost = (int64_t)1 << 36;
+    if (rows < 0 || cols < 1 || classes < 1 || rows > (1 << 27) || cols > (1 << 20) ||
         classes > (1 << 30) || rows > kMost / cols || classes > kMost / cols)
         return fail(SPOPT_EINVAL, "%s: bad size %lld x %lld for %lld classes", what,
                     (long long)rows, (long long)cols, (long long)classes);

@@ -69,6 +69,51 @@ def test_large_tiles(dtype):
     check(*make(2050, 576, 8200, dtype))
 
 
+@pytest.mark.parametrize("dtype,cols", [(BF16, 4000), (F16, 4000), (BF16, 4096)], ids=str)
+def test_largest_tiles(dtype, cols):
+    """Sizes that fill the card with the largest tiles in all three products; rows that are
+    copied (in two pieces in the forward pass) and rows that are read in place."""
+    check(*make(3990, cols, 33003, dtype))
+
+
+def test_more_values_than_an_int_counts():
+    """A table of more than 2^31 values: its last rows."""
+    rows, cols, classes, last = 3, 2048, 1_100_000, 500
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(rows, cols, device="cuda", generator=g).to(BF16)
+    w = torch.empty(classes, cols, device="cuda", dtype=BF16)
+    for part in w.split(100_000):
+        part.copy_(torch.randn(part.shape, device="cuda", generator=g) / 32)
+    t = torch.tensor([classes - 1, 5, classes - 7], device="cuda")
+    loss, lse = L.linear_cross_entropy_forward(x, w, t, reduction="none")
+    xd, z, ez = x.double(), [], []
+    for part in w.split(100_000):
+        z.append(xd @ part.double().T)
+        ez.append(R.product_bound(xd, part.double().T.contiguous(), cols, False))
+    z, ez = torch.cat(z, 1), torch.cat(ez, 1)
+    want = torch.logsumexp(z, 1)
+    p = torch.exp(z - want[:, None])
+    bound = (p * (ez + 3 * R.U * (z.max() - z))).sum(1) + 100 * R.U + R.U * want.abs()
+    R.within(lse, want, 2 * bound, "lse")
+    at = t[:, None]
+    R.within(loss, want - z.gather(1, at)[:, 0],
+             2 * (bound + ez.gather(1, at)[:, 0] + R.U * want.abs()), "loss")
+    dl = torch.ones(rows, device="cuda")
+    dx, dw = L.linear_cross_entropy_backward(dl, x, w, t, lse, reduction="none")
+    # the last rows' gradients, as of a table of their own under the same lse
+    own = t - (classes - last)
+    own[own < 0] = R.IGNORED
+    p = torch.exp(z[:, -last:] - lse.double()[:, None])
+    eg = p * (ez[:, -last:] + 3 * R.U * (z[:, -last:] - lse.double()[:, None]).abs() + 8 * R.U)
+    for i in range(rows):
+        if own[i] >= 0:
+            p[i, own[i]] -= 1
+    eg = eg + (2.0 ** -8 + 8 * R.U) * p.abs()
+    ref = p.T @ xd
+    R.within(dw[-last:], ref, 2.0 ** -8 * ref.abs() + 2 * eg.T @ xd.abs(), "dweight")
+    assert torch.isfinite(dx).all()
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=str)
 def test_pieces_backward(dtype):
     """g of all classes at once would pass the workspace's share: pieces, the last one short."""
@@ -313,7 +358,8 @@ def test_two_streams_at_once():
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=str)
-@pytest.mark.parametrize("size", [(8, 128, 1001), (300, 100, 3001)], ids=str)
+@pytest.mark.parametrize("size", [(8, 128, 1001), (300, 100, 3001), (1500, 520, 9001),
+                                  (3990, 2048, 33003)], ids=str)
 def test_captured(size, dtype):
     x, w, t = make(*size, dtype)
     dl = torch.tensor(0.7, device="cuda")
