@@ -441,7 +441,7 @@ __global__ __launch_bounds__(TL::kThreads)
         CeRowGrads<Tile> grads;
         grads.init(tile, w, i0, c.m, c.n, e, [&](int64_t i) { return w.coef[i]; });
         tile.run((T*)lds_raw, c, i0, t0, t1, 0, c.steps, [&](int64_t t) {
-            grads.template store<T, SPLIT, BN>(tile, w, i0, t * BN, c.n);
+            grads.template store<T, SPLIT, BN, TL::WGN>(tile, w, i0, t * BN, c.n);
         });
     }
 }

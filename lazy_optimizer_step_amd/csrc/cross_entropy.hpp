@@ -205,30 +205,37 @@ struct CeRowSums {
     }
 };
 
-// The rows of a lane while g is formed tile by tile.
+// The rows of a lane while g is formed tile by tile: with c = log2 e, 2^(c z - bits),
+// bits = c lse rounded, times a factor that takes the rounding back.  A value costs
+// a fused multiply-add, an exponential (at a quarter of the rate), a product and a
+// select.
 template <class Tile>
 struct CeRowGrads {
-    float coef[Tile::FM], lse[Tile::FM];
+    float coef[Tile::FM], bits[Tile::FM], factor[Tile::FM];
     int target[Tile::FM];
-    float scale;
+    float to_bits;
 
     template <class C>
     __device__ __forceinline__ void init(const Tile& tile, const CeLogits& w, int64_t i0,
                                          int64_t m, int64_t n, int exponent, C coef_of) {
-        scale = ce_logit_scale(exponent);
+        to_bits = ce_logit_scale(exponent) * kLog2e;
 #pragma unroll
         for (int x = 0; x < Tile::FM; ++x) {
             const int64_t i = i0 + tile.row_of(x);
             const bool row = i < m;
             const int64_t t = row ? w.targets[i] - w.first : -1;
+            const float lse = row ? w.lse[i] : 0.f;
             target[x] = t >= 0 && t < n ? (int)t : -1;
             coef[x] = row ? coef_of(i) : 0.f;
-            lse[x] = row ? w.lse[i] : 0.f;
+            bits[x] = lse * kLog2e;
+            factor[x] = coef[x] * __builtin_amdgcn_exp2f(-__builtin_fmaf(lse, kLog2e, -bits[x]));
+            // Rows that do not count may have any lse.
+            if (coef[x] == 0.f) factor[x] = 0.f;
         }
     }
 
     // g of a tile; split: hi and lo.
-    template <class T, bool SPLIT, int BN>
+    template <class T, bool SPLIT, int BN, int WGN>
     __device__ __forceinline__ void store(const Tile& tile, const CeLogits& w, int64_t i0,
                                           int64_t j0, int64_t n) const {
         constexpr int V = Tile::kRow;  // adjacent columns of a lane
@@ -240,6 +247,9 @@ struct CeRowGrads {
             const int64_t i = i0 + tile.row_of(x);
             if (i >= w.rows_p) continue;
             const int t = target[x] < 0 ? -1 : target[x] - (int)j0;
+            const float less = off * coef[x], once = on * coef[x];
+            // Few waves hold the target of one of their rows.
+            const bool hit = ballot(t >= tile.wj && t < tile.wj + BN / WGN) != 0;
 #pragma unroll
             for (int y = 0; y < Tile::FN; y += V / 4) {
                 const int j = tile.col_of(y);
@@ -247,12 +257,24 @@ struct CeRowGrads {
                 float v[V];
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    const float less = __builtin_fmaf(tile.at(x, y + e / 4, e & 3), scale, -lse[x]);
-                    float p = __builtin_amdgcn_exp2f(less * kLog2e) - off;
-                    if (j + e == t) p -= on;
-                    p *= coef[x];
+                    const float p = __builtin_amdgcn_exp2f(
+                        __builtin_fmaf(tile.at(x, y + e / 4, e & 3), to_bits, -bits[x]));
                     // Rows that do not count may hold anything.
-                    v[e] = coef[x] == 0.f || (!whole && j0 + j + e >= n) ? 0.f : p;
+                    v[e] = factor[x] == 0.f ? 0.f : factor[x] * p;
+                }
+                if (w.smoothing != 0.f) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) v[e] -= less;
+                }
+                if (hit) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        if (j + e == t) v[e] -= once;
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        if (j0 + j + e >= n) v[e] = 0.f;
                 }
                 if constexpr (SPLIT) {
                     float lo[V];

@@ -219,7 +219,7 @@ __global__ __launch_bounds__(256) void k_ced_logits(CeSide x, CeSide w, CeLogits
         }
         CeRowGrads<Tile> grads;
         grads.init(tile, l, i0, x.rows, w.rows, 0, [&](int64_t i) { return f.of(rows, i); });
-        grads.template store<T, false, 64>(tile, l, i0, j0, w.rows);
+        grads.template store<T, false, 64, Tile::WGN>(tile, l, i0, j0, w.rows);
     }
 }
 
