@@ -240,6 +240,10 @@ struct CeWide {
     // Two such parts of four rows then lie in different eighths of 256 bytes.
     static __device__ __forceinline__ int turn(int v) { return (v & 3) << 1; }
 
+    // Chunk c of row r of the other sides lies at c ^ turn_row(r): LDS gives the same
+    // chunk of rows r .. r + 7 and r + 16 .. r + 23 at once.
+    static __device__ __forceinline__ int turn_row(int r) { return (r & 7) ^ (r >> 4 & 1); }
+
     // A side's eight loads a stage: each lane's distance from a base that is the
     // same for the wave.
     template <bool TURN>
@@ -265,7 +269,7 @@ struct CeWide {
                                            (in >> 3 & 1) * 4 + (in & 3)
                                      : at;
                     if (r > last - first) r = last - first;
-                    off[l] = (uint32_t)(r * ld + ((lane & 7) ^ (lane >> 3)) * 16);
+                    off[l] = (uint32_t)(r * ld + ((lane & 7) ^ turn_row(at)) * 16);
                 }
             }
         }
@@ -314,7 +318,7 @@ struct CeWide {
             return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
         } else {
             return *(const vec8*)(l + (first + (lane & 31)) * kTile +
-                                  ((kk * 2 + (lane >> 5)) ^ (lane & 7)) * 8);
+                                  ((kk * 2 + (lane >> 5)) ^ turn_row(lane & 31)) * 8);
         }
     }
 
