@@ -1320,9 +1320,13 @@ extern "C" int linear_cross_entropy_backward(
         both.dw_splits = r.dw.splits;
         both.scalars = b.scalars;
         if (dx != nullptr)
-            both.dx_tiles = ceil_div(rows, r.dx.tile) * ceil_div(cols, 64);
-        if (dweight != nullptr)
-            both.dw_tiles = ceil_div(classes, r.dw.tile) * ceil_div(cols, 64);
+            both.dx_blocks = ceil_div(rows, r.dx.tile) * ceil_div(cols, 64);
+        // Tiles of few inner steps are mostly waits for loads and stores: a block goes
+        // through as many as leave the card full, the loads running on.
+        const int64_t tiles = ceil_div(classes, r.dw.tile), across = ceil_div(cols, 64);
+        const int64_t most = tiles * across * r.dw.splits / 2048;
+        both.dw_group = (int)(most < 1 ? 1 : most > tiles ? tiles : most);
+        if (dweight != nullptr) both.dw_blocks = ceil_div(tiles, both.dw_group) * across;
         both.dx = CeResult{r.dx.splits > 1 ? b.dx_parts : nullptr, sh.cols_p, 0, dx, dx_stride};
         both.dw = CeResult{r.dw.splits > 1 ? b.dw_parts : nullptr, sh.cols_p, 0, dweight,
                            dweight_stride};

@@ -434,7 +434,8 @@ struct CeBoth {
     CeSide g, w, x;
     CeResult dx, dw;
     int64_t rows, cols, classes;
-    int64_t dx_tiles, dw_tiles;  // 0 where not wanted
+    int64_t dx_blocks, dw_blocks;  // of each split; 0 where not wanted
+    int dw_group;                // tiles of dW that a block goes through
     int dx_tile, dw_tile;        // rows of a tile
     int dx_splits, dw_splits;
     const CeScalars* scalars;

@@ -11,6 +11,8 @@
 
 namespace spopt {
 
+typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
+
 template <class T, bool TP, bool TQ, int BM_>
 struct CeDirect {
     static constexpr int BM = BM_, BN = 64, WGN = BM == 64 ? 2 : 4;  // four waves
@@ -64,8 +66,9 @@ struct CeDirect {
                 }
             }
         }
-        __device__ __forceinline__ chunk load(int64_t k, int l) const {
-            int64_t r = row[l], c = col;
+        // Chunk l of step k, `shift` columns on (of a turned side).
+        __device__ __forceinline__ chunk load(int64_t k, int l, int64_t shift) const {
+            int64_t r = row[l], c = TURN ? col + shift : col;
             bool in;
             if constexpr (TURN) {
                 r += k * kInner;
@@ -76,11 +79,27 @@ struct CeDirect {
             }
             chunk v = {};
             if (!in || c >= cols) return v;
-            const T* p = base + r * ld + c;
-            if (c + E <= cols) return *(const typename Pack<T, E>::type*)p;
+            const T* p = base + r * ld;
+            if (cols < E) {
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (c + e < cols) v[e] = p[e];
+                for (int e = 0; e < E; ++e)
+                    if (c + e < cols) v[e] = p[c + e];
+                return v;
+            }
+            // The chunk at a row's end is moved back to end with it, and its values
+            // forward again: loads of single values would keep the whole wave.
+            const int64_t at = c + E <= cols ? c : cols - E;
+            v = *(const typename Pack<T, E>::type*)(p + at);
+            const int skip = (int)(c - at);
+            if (skip != 0) {
+                uint4v q = __builtin_bit_cast(uint4v, v);
+                if (skip & E / 2) q = uint4v{q[2], q[3], 0, 0};
+                if (skip & E / 4) q = uint4v{q[1], q[2], q[3], 0};
+                if (E == 8 && skip & 1)
+                    q = uint4v{q[0] >> 16 | q[1] << 16, q[1] >> 16 | q[2] << 16,
+                               q[2] >> 16 | q[3] << 16, q[3] >> 16};
+                v = __builtin_bit_cast(chunk, q);
+            }
             return v;
         }
     };
@@ -93,6 +112,8 @@ struct CeDirect {
         wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         wi = wv / WGN * FM * 16;
         wj = wv % WGN * FN * 16;
+    }
+    __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int x = 0; x < FM; ++x)
 #pragma unroll
@@ -121,9 +142,12 @@ struct CeDirect {
         }
     }
 
-    // Steps [k0, k1) of the inner axis.
+    // `tiles` tiles one below the other (one, but for a turned P), steps [k0, k1) of
+    // the inner axis for each: `done(t)` where tile t's sums are there.  The loads run
+    // on from tile to tile.
+    template <class F>
     __device__ __forceinline__ void run(char* lds, const CeSide& p, const CeSide& q, int64_t i0,
-                                        int64_t j0, int64_t k0, int64_t k1) {
+                                        int tiles, int64_t j0, int64_t k0, int64_t k1, F done) {
         typedef Feed<TP, BM> FeedP;
         typedef Feed<TQ, BN> FeedQ;
         FeedP fp;
@@ -132,21 +156,29 @@ struct CeDirect {
         fq.init(q, j0, kRow == 8);
         const bool with_p = BM == 64 || threadIdx.x < 8 * BM;
         chunk cp[kAhead][FeedP::kLoads], cq[kAhead][FeedQ::kLoads];
-        auto bring = [&](int u, int64_t k) {
+        int64_t bk = k0, shift = 0, left = tiles * (k1 - k0);
+        auto bring = [&](int u) {
+            if (left == 0) return;
 #pragma unroll
             for (int l = 0; l < FeedP::kLoads; ++l)
-                if (with_p) cp[u][l] = fp.load(k, l);
+                if (with_p) cp[u][l] = fp.load(bk, l, shift);
 #pragma unroll
-            for (int l = 0; l < FeedQ::kLoads; ++l) cq[u][l] = fq.load(k, l);
+            for (int l = 0; l < FeedQ::kLoads; ++l) cq[u][l] = fq.load(bk, l, 0);
+            --left;
+            if (++bk == k1) {
+                bk = k0;
+                shift += BM;
+            }
         };
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-            if (k0 + u < k1) bring(u, k0 + u);
-        int buf = 0;
-        for (int64_t k = k0; k < k1; k += kAhead) {
+        for (int u = 0; u < kAhead; ++u) bring(u);
+        clear();
+        int buf = 0, t = 0;
+        int64_t k = k0;
+        while (t < tiles) {
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                if (k + u >= k1) break;
+                if (t == tiles) break;
                 char* const to = lds + buf * (kSideP + kSideQ);
 #pragma unroll
                 for (int l = 0; l < FeedP::kLoads; ++l)
@@ -154,7 +186,7 @@ struct CeDirect {
 #pragma unroll
                 for (int l = 0; l < FeedQ::kLoads; ++l)
                     *(chunk*)(to + kSideP + fq.place[l]) = cq[u][l];
-                if (k + u + kAhead < k1) bring(u, k + u + kAhead);
+                bring(u);
                 // One barrier a stage: whoever writes this place next has passed
                 // the other one's, after all reads of this.
                 __syncthreads();
@@ -180,6 +212,11 @@ struct CeDirect {
                         }
                 }
                 buf ^= 1;
+                if (++k == k1) {
+                    done(t);
+                    k = k0;
+                    if (++t < tiles) clear();
+                }
             }
         }
         __syncthreads();
@@ -204,7 +241,7 @@ __global__ __launch_bounds__(256) void k_ced_logits(CeSide x, CeSide w, CeLogits
     const int64_t i0 = ti * BM, j0 = tj * 64;
     Tile tile;
     tile.init();
-    tile.run(lds, x, w, i0, j0, 0, (x.cols + Tile::kInner - 1) / Tile::kInner);
+    tile.run(lds, x, w, i0, 1, j0, 0, (x.cols + Tile::kInner - 1) / Tile::kInner, [](int) {});
     if constexpr (MODE == kCeLoss) {
         CeRowSums<Tile> sums;
         sums.init(tile, l, i0, x.rows, w.rows, 0);
@@ -223,37 +260,42 @@ __global__ __launch_bounds__(256) void k_ced_logits(CeSide x, CeSide w, CeLogits
     }
 }
 
-// Tile `at` of a product of `m` rows, the inner axis of `k` values cut into `splits`.
+// Block `at` of a product of m rows, the inner axis of k values cut into `splits`:
+// `group` tiles one below the other.
 template <class T, bool TP, int BM>
 __device__ __forceinline__ void ced_product(char* lds, const CeSide& p, const CeSide& q,
-                                            const CeResult& w, int64_t at, int64_t tiles,
-                                            int splits, int64_t m, int64_t n, int64_t k,
+                                            const CeResult& w, int64_t at, int64_t blocks,
+                                            int group, int splits, int64_t m, int64_t n, int64_t k,
                                             const CeScalars* sc) {
     CeDirect<T, TP, true, BM> tile;
-    const int64_t split = at / tiles, t = at % tiles, tn = (n + 63) / 64;
+    const int64_t split = at / blocks, t = at % blocks, tn = (n + 63) / 64;
     const int64_t steps = (k + tile.kInner - 1) / tile.kInner;
-    const int64_t i0 = t / tn * BM, j0 = t % tn * 64;
-    tile.init();
-    tile.run(lds, p, q, i0, j0, split * steps / splits, (split + 1) * steps / splits);
+    const int64_t i0 = t / tn * group * BM, j0 = t % tn * 64;
+    const int64_t left = (m - i0 + BM - 1) / BM;
     const int e = sc->ek;
     const float mu = sc->mu;
-    ce_store_tile<T>(tile, i0, j0, m, n, w, w.parts ? w.parts + split * m * w.ld : nullptr,
-                     [&](float v) { return ce_unscale(v, mu, e); });
+    tile.init();
+    tile.run(lds, p, q, i0, left < group ? (int)left : group, j0, split * steps / splits,
+             (split + 1) * steps / splits, [&](int g) {
+                 ce_store_tile<T>(tile, i0 + g * BM, j0, m, n, w,
+                                  w.parts ? w.parts + split * m * w.ld : nullptr,
+                                  [&](float v) { return ce_unscale(v, mu, e); });
+             });
 }
 
 template <class T, int BM_DX, int BM_DW>
 __global__ __launch_bounds__(256) void k_ced_products(CeBoth b) {
     __shared__ __align__(16) char lds[CeDirect<T, true, true, 64>::kBytes];
     // The product whose blocks take longer begins.
-    const int64_t dx = b.dx_tiles * b.dx_splits, dw = b.dw_tiles * b.dw_splits;
+    const int64_t dx = b.dx_blocks * b.dx_splits, dw = b.dw_blocks * b.dw_splits;
     const bool dw_first = b.rows / b.dw_splits > b.classes / b.dx_splits;
     const int64_t at = blockIdx.x, first = dw_first ? dw : dx;
     if ((at < first) != dw_first)
-        ced_product<T, false, BM_DX>(lds, b.g, b.w, b.dx, dw_first ? at - dw : at, b.dx_tiles,
-                                     b.dx_splits, b.rows, b.cols, b.classes, b.scalars);
+        ced_product<T, false, BM_DX>(lds, b.g, b.w, b.dx, dw_first ? at - dw : at, b.dx_blocks,
+                                     1, b.dx_splits, b.rows, b.cols, b.classes, b.scalars);
     else
-        ced_product<T, true, BM_DW>(lds, b.g, b.x, b.dw, dw_first ? at : at - dx, b.dw_tiles,
-                                    b.dw_splits, b.classes, b.cols, b.rows, b.scalars);
+        ced_product<T, true, BM_DW>(lds, b.g, b.x, b.dw, dw_first ? at : at - dx, b.dw_blocks,
+                                    b.dw_group, b.dw_splits, b.classes, b.cols, b.rows, b.scalars);
 }
 
 template <class F>
@@ -302,7 +344,7 @@ int ce_direct_grad(int32_t dtype, int tile, const CeSide& x, const CeSide& w,
 }
 
 int ce_direct_products(int32_t dtype, const CeBoth& b, hipStream_t s) {
-    const int64_t blocks = b.dx_tiles * b.dx_splits + b.dw_tiles * b.dw_splits;
+    const int64_t blocks = b.dx_blocks * b.dx_splits + b.dw_blocks * b.dw_splits;
     return ced_types(dtype, [&](auto t) {
         ced_rows(b.dx_tile, [&](auto bx) {
             ced_rows(b.dw_tile, [&](auto bw) {
