@@ -363,10 +363,10 @@ struct CeRows {
 // c_i times the number that brings the largest gradient that is to be expected,
 // (1 - smoothing) max |c| at a target of no probability, to 2^13.  float16 then
 // holds small probabilities; and of a call whose rows count alike the gradients
-// at the targets, the largest by far, lie just below a power of two, where
-// rounding takes least of them (with 2^13 times a mantissa that may lie
-// anywhere, gradients of bfloat16 and float16 were off by 1.2 to 1.48 times what
-// the rounding of the results alone does; now by ... ).
+// at the targets, the largest by far, lie at a power of two or just below, where
+// rounding takes least of them.  8192 x 4096 x 131072 bfloat16, errors of dx and dW
+// (norm of the difference over norm): 1.7e-3, which is the results' own rounding;
+// with a power of two in front 1.8e-3 to 2.5e-3, by where c's mantissa lies.
 struct CeFactor {
     float one, inv;
     int ek;

@@ -4,9 +4,13 @@
 //
 // A launch costs the host 3.5 us, which is all that a small call takes.  These
 // take two launches forward (the logits' tiles, the join) and two backward (g;
-// both products), where packed operands take up to five and nine.  Operands go
-// through registers into LDS, three stages on their way, 64 x 64 tiles, one
-// layout in LDS with cross_entropy.hip's.
+// both products, and a third where an inner axis is cut), where packed operands
+// take up to five and nine.  Operands go through registers into LDS, four or six
+// stages on their way, in tiles of 64 x 64 or, of few rows, 16 x 64, laid out in LDS
+// as cross_entropy.hip's.  4 x 256 x 1000 float32: 18.7 us forward and 25.9 backward a
+// call, packed 28.9 and 39.1; of the 18.7 the host takes about 13.  6 x 966 x 67682
+// float16 backward 143 us, where one pass over W takes 26: rows at odd addresses
+// (960 columns 131 us), and W read twice.
 #include "cross_entropy.hpp"
 
 namespace spopt {
