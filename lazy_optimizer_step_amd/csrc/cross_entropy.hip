@@ -22,7 +22,7 @@
 // instructions in place of one; errors are float32's (8192 x 128 x 50021: 3.8e-7 of
 // dx, float32 products 3.6e-6).
 //
-// Measured on one MI355X (boxes differ by 7%): 4096 x 2048 x 131072 bfloat16 forward
+// Measured on one MI355X (cards differ by 7%): 4096 x 2048 x 131072 bfloat16 forward
 // 1.79 to 1.94 ms (1.13 to 1.23 PFLOP/s), 8192 x 4096 x 131072 backward 20.7 to 21.9
 // ms (1.20 to 1.28 PFLOP/s; a library product of these sizes 1.31 to 1.50), 8192 x 128
 // x 50021 float32 0.33 to 0.36 and 1.40 to 1.54 ms.
@@ -894,7 +894,8 @@ static CePlan ce_direct_plan(const CeShape& s, int64_t m, int64_t n, int64_t k, 
     for (int tile = 16; tile <= 64; tile += 48)
         for (int splits = 1; splits <= (cut ? 32 : 1); splits *= 2) {
             const int64_t blocks = ceil_div(m, tile) * ceil_div(n, 64) * splits;
-            if (splits > 1 && blocks > 1024) break;
+            // Each part has a step at least.
+            if (splits > 1 && (blocks > 1024 || splits > steps)) break;
             const double step = s.split ? tile == 16 ? 0.4 : 0.7 : tile == 16 ? 0.25 : 0.3;
             const double us = (double)ceil_div(blocks, 256) *
                                   ((double)ceil_div(steps, splits) * step + 1.) +

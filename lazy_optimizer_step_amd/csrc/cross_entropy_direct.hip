@@ -147,7 +147,7 @@ struct CeDirect {
     }
 
     // `tiles` tiles one below the other (one, but for a turned P), steps [k0, k1) of
-    // the inner axis for each: `done(t)` where tile t's sums are there.  The loads run
+    // the inner axis for each, one at least: `done(t)` where tile t's sums are there.  The loads run
     // on from tile to tile.
     template <class F>
     __device__ __forceinline__ void run(char* lds, const CeSide& p, const CeSide& q, int64_t i0,
@@ -161,6 +161,7 @@ struct CeDirect {
         const bool with_p = BM == 64 || threadIdx.x < 8 * BM;
         chunk cp[kAhead][FeedP::kLoads], cq[kAhead][FeedQ::kLoads];
         int64_t bk = k0, shift = 0, left = tiles * (k1 - k0);
+        if (left <= 0) return;  // the host cuts no axis into more parts than it has steps
         auto bring = [&](int u) {
             if (left == 0) return;
 #pragma unroll

@@ -58,6 +58,15 @@ def test_one_row_of_many_classes(dtype):
     check(*make(65, 72, 20001, dtype), "none", 0.1)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=str)
+@pytest.mark.parametrize("steps", [13, 17, 20, 25, 31, 33, 47])
+def test_cut_axes_of_any_length(dtype, steps):
+    """Inner axes of a number of steps that no power of two divides, cut for either gradient."""
+    k = steps * (32 if dtype == F32 else 64) - 5
+    check(*make(4, 64, k, dtype), "none")
+    check(*make(k, 64, 4, dtype), "none")
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16, F16], ids=str)
 def test_many_rows_of_few_classes(dtype):
     """The inner axis of dweight cut into parts."""
