@@ -307,7 +307,11 @@ class Dropout(torch.nn.Module):
     Each training pass takes the next offset under ``seed``: two modules need two seeds.  The
     seed is an int, or a device int64 tensor of one value, read when the kernel runs: a pass
     captured into a graph replays its offset, so change the tensor between replays.  ``offset``
-    is part of the state dict."""
+    is part of the state dict.
+
+    ``forward(x, residual, offset=k)`` takes offset k and leaves the count as it is: for a pass
+    that is run again for its gradients (activation checkpointing), which needs the first
+    run's mask."""
 
     def __init__(self, p: float, seed=0):
         super().__init__()
@@ -321,10 +325,11 @@ class Dropout(torch.nn.Module):
     def set_extra_state(self, state):
         self.offset = state["offset"]
 
-    def forward(self, x: torch.Tensor, residual=None) -> torch.Tensor:
+    def forward(self, x: torch.Tensor, residual=None, *, offset=None) -> torch.Tensor:
         if not self.training:
             return x if residual is None else x + residual
-        offset, self.offset = self.offset, self.offset + 1
+        if offset is None:
+            offset, self.offset = self.offset, self.offset + 1
         return _Dropout.apply(x, residual, self.p, self.seed, offset)
 
 

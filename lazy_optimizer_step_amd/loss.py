@@ -68,6 +68,11 @@ def _floats(t, name, x, numel):
         raise ValueError(f"{name} must hold {numel} values, has shape {tuple(t.shape)}")
 
 
+def _space(workspace, x):
+    if workspace is not None and _need(workspace, torch.uint8, "workspace").device != x.device:
+        raise ValueError(f"workspace is on {workspace.device}, x on {x.device}")
+
+
 def linear_cross_entropy_forward(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, *,
                                  reduction: str = "mean", ignore_index: int = -100,
                                  label_smoothing: float = 0.0, out=None, lse=None, workspace=None,
@@ -84,8 +89,7 @@ def linear_cross_entropy_forward(x: torch.Tensor, weight: torch.Tensor, targets:
         _floats(out, "out", x, rows if reduction == "none" else 1)
     if lse is not None:
         _floats(lse, "lse", x, rows)
-    if workspace is not None:
-        _need(workspace, torch.uint8, "workspace")
+    _space(workspace, x)
     with _alloc_on(stream):
         if out is None:
             out = x.new_empty(shape, dtype=torch.float32)
@@ -120,8 +124,7 @@ def linear_cross_entropy_backward(dloss: torch.Tensor, x: torch.Tensor, weight: 
             raise ValueError(f"dweight has shape {tuple(dweight.shape)}, weight "
                              f"{tuple(weight.shape)}")
         _, _, dws = _rows(dweight, "dweight")
-    if workspace is not None:
-        _need(workspace, torch.uint8, "workspace")
+    _space(workspace, x)
     with _alloc_on(stream):
         if want_dx and out is None:
             out = _like(x)
@@ -167,7 +170,11 @@ class LinearCrossEntropy(torch.nn.Module):
 
     weight: the table to use, (classes, dim) (shared, not copied), else one of its own,
     N(0, 1 / dim).  forward(x, targets) gives the loss: x of the table's type, (..., dim);
-    targets int64 of x's leading shape."""
+    targets int64 of x's leading shape.
+
+    Before a backward pass is captured into a graph, let go of the losses of eager passes over
+    the same parameters: while one lives, torch adds the parameters' gradients up on the stream
+    of that pass, outside the capture."""
 
     def __init__(self, dim: int, classes: int, *, weight=None, reduction: str = "mean",
                  ignore_index: int = -100, label_smoothing: float = 0.0, dtype=torch.float32,

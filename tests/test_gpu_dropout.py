@@ -1,6 +1,7 @@
 """Dropout on the GPU: the mask bit for bit, the values against 64 bits."""
 import pytest
 import torch
+import torch.utils.checkpoint
 
 import lazy_optimizer_step_amd as L
 from lazy_optimizer_step_amd import _lib
@@ -168,6 +169,16 @@ def test_module_keeps_the_seed_that_its_forward_read():
     seed.fill_(99)
     y.sum().backward()
     assert torch.equal(x.grad != 0, y != 0)
+
+
+def test_module_with_a_pass_that_is_run_again():
+    m = L.Dropout(0.5, seed=6)
+    x = draw((50, 60), F32).requires_grad_()
+    m(x)
+    y = torch.utils.checkpoint.checkpoint(lambda t: m(t * 2, offset=40), x, use_reentrant=False)
+    assert torch.equal(y, L.dropout_forward(x.detach() * 2, 0.5, 6, offset=40))
+    y.sum().backward()
+    assert torch.equal(x.grad, 4.0 * (y != 0)) and m.offset == 1
 
 
 def test_module_takes_any_layout():

@@ -479,3 +479,17 @@ def test_another_current_device(monkeypatch):
         L.linear_cross_entropy_forward(x, w, t)
     with pytest.raises(ValueError, match="current device"):
         L.dropout_forward(x, 0.5, 1)
+
+
+def test_workspace_of_another_device():
+    """A tensor that says it lies on the next device stands in for one that does."""
+    class Elsewhere(torch.Tensor):
+        device = torch.device("cuda", 1)
+
+    x, w, t = make(8, 16, 20, F32)
+    space = torch.empty(1 << 20, dtype=torch.uint8, device="cuda").as_subclass(Elsewhere)
+    loss, lse = L.linear_cross_entropy_forward(x, w, t)
+    with pytest.raises(ValueError, match="workspace is on cuda:1"):
+        L.linear_cross_entropy_forward(x, w, t, workspace=space)
+    with pytest.raises(ValueError, match="workspace is on cuda:1"):
+        L.linear_cross_entropy_backward(loss, x, w, t, lse, workspace=space)
