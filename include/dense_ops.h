@@ -187,6 +187,23 @@ SPOPT_API int muon_step(void* params, int32_t pdtype, float* buf, const void* g,
  * the targets, the rows of x that count, and weight. */
 SPOPT_API int linear_cross_entropy_workspace_size(int64_t rows, int64_t cols, int64_t classes,
                                                   int32_t dtype, int32_t backward, size_t* bytes);
+
+/* Which kernels a pass takes at a size, by the sizes alone: what two calls share
+ * that give the same bits, and what a measurement of the rule asks for. */
+typedef struct spopt_ce_plan {
+    int32_t direct;       /* 1: operands read in place by kernels for small calls; tiles below 16 or 64 */
+    int32_t tile_logits;  /* rows of a tile of the logits, */
+    int32_t tile_dx;      /* and (backward; else 0) of the two products: 64, 128 or 256 */
+    int32_t tile_dw;
+    int32_t splits_dx;    /* parts that their inner axes are cut into */
+    int32_t splits_dw;
+    int64_t piece;        /* classes at a time */
+} spopt_ce_plan;
+
+/* Errors: SPOPT_EINVAL (rows < 1, and as linear_cross_entropy_workspace_size). */
+SPOPT_API int linear_cross_entropy_plan(int64_t rows, int64_t cols, int64_t classes, int32_t dtype,
+                                        int32_t backward, spopt_ce_plan* plan);
+
 SPOPT_API int linear_cross_entropy_forward(const void* x, int64_t x_stride, const void* weight,
                                            int64_t weight_stride, int64_t rows, int64_t cols,
                                            int64_t classes, int32_t dtype, const int64_t* targets,

@@ -39,7 +39,8 @@ __all__ = ["coo_from_lookups", "csr_from_coo", "csr_from_lookups", "csr_to_coo",
            "layer_norm_forward", "layer_norm_backward", "layer_norm_backward_workspace_size",
            "LayerNorm", "newton_schulz", "newton_schulz_workspace_size", "muon_step", "Muon",
            "linear_cross_entropy_forward", "linear_cross_entropy_backward",
-           "linear_cross_entropy_workspace_size", "LinearCrossEntropy",
+           "linear_cross_entropy_workspace_size", "linear_cross_entropy_plan",
+           "LinearCrossEntropy",
            "dropout_forward", "dropout_backward", "Dropout"]
 
 
@@ -600,4 +601,5 @@ from .dense import (Dropout, LayerNorm, Muon, dropout_backward, dropout_forward,
                     layer_norm_backward, layer_norm_backward_workspace_size, layer_norm_forward,
                     muon_step, newton_schulz, newton_schulz_workspace_size)
 from .loss import (LinearCrossEntropy, linear_cross_entropy_backward,  # noqa: E402
-                   linear_cross_entropy_forward, linear_cross_entropy_workspace_size)
+                   linear_cross_entropy_forward, linear_cross_entropy_plan,
+                   linear_cross_entropy_workspace_size)

@@ -69,6 +69,12 @@ class SparseOptError(RuntimeError):
         self.code = code
 
 
+class CePlan(C.Structure):
+    _fields_ = [("direct", C.c_int32), ("tile_logits", C.c_int32), ("tile_dx", C.c_int32),
+                ("tile_dw", C.c_int32), ("splits_dx", C.c_int32), ("splits_dw", C.c_int32),
+                ("piece", C.c_int64)]
+
+
 _lib = None
 
 
@@ -134,6 +140,7 @@ def lib() -> C.CDLL:
                                 U32]
         U64 = C.c_uint64
         L.linear_cross_entropy_workspace_size.argtypes = [I64, I64, I64, I32, I32, C.POINTER(SZ)]
+        L.linear_cross_entropy_plan.argtypes = [I64, I64, I64, I32, I32, C.POINTER(CePlan)]
         L.linear_cross_entropy_forward.argtypes = [P, I64, P, I64, I64, I64, I64, I32, P, I64, F64,
                                                    I32, P, P, P, SZ, P, U32]
         L.linear_cross_entropy_backward.argtypes = [P, P, I64, P, I64, I64, I64, I64, I32, P, I64,
@@ -144,8 +151,8 @@ def lib() -> C.CDLL:
         for f in (L.layer_norm_forward, L.layer_norm_backward_workspace_size,
                   L.layer_norm_backward, L.newton_schulz_workspace_size, L.newton_schulz,
                   L.muon_step, L.linear_cross_entropy_workspace_size,
-                  L.linear_cross_entropy_forward, L.linear_cross_entropy_backward,
-                  L.dropout_forward, L.dropout_backward):
+                  L.linear_cross_entropy_plan, L.linear_cross_entropy_forward,
+                  L.linear_cross_entropy_backward, L.dropout_forward, L.dropout_backward):
             f.restype = C.c_int
         _lib = L
     return _lib
@@ -164,5 +171,6 @@ EXPORTED = ("sparse_opt_create", "sparse_opt_destroy", "sparse_opt_get_step", "s
             "sparse_opt_host_alloc", "sparse_opt_host_free", "sparse_opt_host_device_pointer",
             "layer_norm_forward", "layer_norm_backward_workspace_size", "layer_norm_backward",
             "newton_schulz_workspace_size", "newton_schulz", "muon_step",
-            "linear_cross_entropy_workspace_size", "linear_cross_entropy_forward",
-            "linear_cross_entropy_backward", "dropout_forward", "dropout_backward")
+            "linear_cross_entropy_workspace_size", "linear_cross_entropy_plan",
+            "linear_cross_entropy_forward", "linear_cross_entropy_backward",
+            "dropout_forward", "dropout_backward")

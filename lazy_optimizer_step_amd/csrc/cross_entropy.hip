@@ -1171,6 +1171,19 @@ extern "C" int linear_cross_entropy_workspace_size(int64_t rows, int64_t cols, i
     return SPOPT_OK;
 }
 
+extern "C" int linear_cross_entropy_plan(int64_t rows, int64_t cols, int64_t classes, int32_t dtype,
+                                         int32_t backward, spopt_ce_plan* plan) {
+    const char* what = "linear_cross_entropy_plan";
+    if (plan == nullptr) return fail(SPOPT_EINVAL, "%s: NULL output", what);
+    const int rc = ce_check_size(what, rows, cols, classes, dtype);
+    if (rc) return rc;
+    if (rows == 0) return fail(SPOPT_EINVAL, "%s: no rows", what);
+    const CeRun r = ce_run(ce_shape(rows, cols, classes, dtype), backward != 0);
+    *plan = spopt_ce_plan{r.direct, r.logits.tile, r.dx.tile, r.dw.tile,
+                          r.dx.splits, r.dw.splits, r.piece};
+    return SPOPT_OK;
+}
+
 extern "C" int linear_cross_entropy_forward(const void* x, int64_t x_stride, const void* weight,
                                             int64_t weight_stride, int64_t rows, int64_t cols,
                                             int64_t classes, int32_t dtype,

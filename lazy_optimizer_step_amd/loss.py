@@ -33,6 +33,16 @@ def linear_cross_entropy_workspace_size(rows: int, cols: int, classes: int, dtyp
     return _workspace_size(rows, cols, classes, _DTYPES[dtype], 1 if backward else 0)
 
 
+def linear_cross_entropy_plan(rows: int, cols: int, classes: int, dtype: torch.dtype, *,
+                              backward: bool) -> dict:
+    """Which kernels the forward (or the backward) pass takes at a size: spopt_ce_plan of
+    dense_ops.h."""
+    p = _lib.CePlan()
+    check(_lib.lib().linear_cross_entropy_plan(rows, cols, classes, _DTYPES[dtype],
+                                               1 if backward else 0, C.byref(p)))
+    return {name: getattr(p, name) for name, _ in p._fields_}
+
+
 def _table(weight, name, x, cols):
     """(classes, row stride) of a classes x cols matrix of x's type."""
     if not isinstance(weight, torch.Tensor):
