@@ -732,18 +732,35 @@ __global__ __launch_bounds__(1024) void k_ce_reduce(const float* row_loss, const
     if (threadIdx.x == 0) *loss = (float)(reduction == kCeMean ? s / fmax(n, 1.) : s);
 }
 
-// Each row's factor, 0 beyond the last.  One block.
+// What CeFactor takes from all rows, each block's share.
+__global__ __launch_bounds__(256) void k_ce_scan(CeRows rows, CeScan* scans) {
+    __shared__ double lds[4];
+    __shared__ float tops[4];
+    CeScan s = ce_scan_rows(rows, (int64_t)blockIdx.x * 256 + threadIdx.x, rows.rows,
+                            (int64_t)gridDim.x * 256);
+    s.n = ce_block_sum(s.n, lds);
+#pragma unroll
+    for (int off = kWave / 2; off; off >>= 1) s.top = fmaxf(s.top, __shfl_xor(s.top, off, kWave));
+    if (lane_id() == 0) tops[threadIdx.x >> 6] = s.top;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int k = 0; k < 4; ++k) s.top = fmaxf(s.top, tops[k]);
+    scans[blockIdx.x] = s;
+}
+
+// Each row's factor, 0 beyond the last.  One block, or more where the rows have been
+// scanned.
 __global__ __launch_bounds__(1024) void k_ce_coef(CeRows rows, int64_t rows_p, float* coef,
                                                   CeScalars* scalars) {
     __shared__ double lds[16];
     __shared__ float top_of[16];
     CeFactor f;
     f.init(rows, false, lds, top_of);
-    if (threadIdx.x == 0) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
         scalars->ek = f.ek;
         scalars->mu = f.mu;
     }
-    for (int64_t i = threadIdx.x; i < rows_p; i += 1024)
+    for (int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x; i < rows_p; i += gridDim.x * 1024)
         coef[i] = i < rows.rows ? f.of(rows, i) : 0.f;
 }
 
@@ -862,6 +879,7 @@ static int64_t ce_piece(const CeShape& s, bool backward) {
 
 struct CeBuffers {
     CeScalars* scalars;
+    CeScan* scans;
     uint32_t* amax;
     void* x;            // x's copy
     void* w;            // a piece of W's copy
@@ -962,6 +980,7 @@ static size_t ce_layout(const CeRun& r, bool backward, char* base, CeBuffers* b)
         return (void*)p;
     };
     b->scalars = (CeScalars*)take(sizeof(CeScalars));
+    b->scans = (CeScan*)take(backward ? kCeScans * sizeof(CeScan) : 0);
     if (!r.direct) {
         b->amax = (uint32_t*)take(2 * kAmaxParts * 4);
         b->x = take((size_t)(s.rows_p * s.cols_p * s.value) * 2);
@@ -1146,6 +1165,27 @@ static int ce_validate(const char* what, const CeShape& s, const void* x, int64_
     });
 }
 
+// Scans the rows once where every block of g's kernel (direct), or the one of
+// k_ce_coef, would take longer over them than a launch does.  Backward, in the blocks
+// against once: 64 columns and 10 classes float32, 4000 rows 26 against 28 us, 16384 rows
+// 50 against 47, 1000000 rows 23500 against 2180; 256 x 1000 bfloat16 with a factor for each
+// row, 2000 rows 45.7 against 48, 4000 rows 73 against 67; packed, 256 x 1000 float32, 8192
+// rows 104.6 against 106.2, 16384 rows 153 against 151, 65536 rows 500 against 473.
+static int ce_scan(CeRows* rows, const CeRun& r, const CeBuffers& b, hipStream_t s) {
+    if (rows->reduction == SPOPT_REDUCE_SUM ||
+        (rows->reduction == SPOPT_REDUCE_NONE && r.direct && r.s.split))
+        return SPOPT_OK;
+    const int64_t readers =
+        r.direct ? ceil_div(rows->rows, r.logits.tile) * ceil_div(rows->classes, 64) : 256;
+    if (rows->rows <= ((int64_t)1 << 21) / readers) return SPOPT_OK;
+    const int64_t blocks = ceil_div(rows->rows, 1024);
+    rows->n_scans = (int)(blocks < kCeScans ? blocks : kCeScans);
+    k_ce_scan<<<(unsigned)rows->n_scans, 256, 0, s>>>(*rows, b.scans);
+    SPOPT_LAUNCHED();
+    rows->scans = b.scans;
+    return SPOPT_OK;
+}
+
 static int ce_workspace(const char* what, const void* workspace, size_t have, size_t need) {
     if (need != 0 && (workspace == nullptr || !aligned16(workspace) || have < need))
         return fail(SPOPT_EWORKSPACE, "%s: workspace of %zu bytes, needs %zu", what, have, need);
@@ -1314,8 +1354,10 @@ extern "C" int linear_cross_entropy_backward(
         rc = ce_validate(what, sh, x, x_stride, weight, weight_stride, targets, ignore_index, s);
         if (rc) return rc;
     }
-    const CeRows factors{dloss, targets, ignore_index, rows, classes, reduction,
-                         (float)(1.0 - label_smoothing)};
+    CeRows factors{dloss, targets, ignore_index, rows, classes, reduction,
+                   (float)(1.0 - label_smoothing), nullptr, 0};
+    rc = ce_scan(&factors, r, b, s);
+    if (rc) return rc;
     CeLogits w{};
     w.scalars = b.scalars;
     w.targets = targets;
@@ -1367,7 +1409,9 @@ extern "C" int linear_cross_entropy_backward(
     int amax = 0;
     rc = ce_amax(sh, x, x_stride, targets, ignore_index, weight, weight_stride, b, &amax, s);
     if (rc) return rc;
-    k_ce_coef<<<1, 1024, 0, s>>>(factors, sh.rows_p, b.coef, b.scalars);
+    const int64_t coefs = factors.scans == nullptr ? 1 : ceil_div(sh.rows_p, 4096);
+    k_ce_coef<<<(unsigned)(coefs < 1024 ? coefs : 1024), 1024, 0, s>>>(factors, sh.rows_p, b.coef,
+                                                                       b.scalars);
     SPOPT_LAUNCHED();
     // x is copied for its rows that are ignored: they may hold anything, and meet
     // g's zeros in dW.

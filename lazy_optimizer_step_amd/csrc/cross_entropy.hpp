@@ -362,6 +362,13 @@ enum : int {
     kCeMean = SPOPT_REDUCE_MEAN
 };
 
+// What a block of k_ce_scan found in its share of the rows.
+struct CeScan {
+    double n;   // rows that count
+    float top;  // the largest finite |dloss| (kCeNone)
+};
+constexpr int kCeScans = 256;
+
 // What a row's factor c_i is made of.
 struct CeRows {
     const float* dloss;
@@ -369,7 +376,21 @@ struct CeRows {
     int64_t ignored, rows, classes;
     int reduction;
     float on;  // 1 - smoothing
+    const CeScan* scans;  // or NULL: each block goes over the rows itself
+    int n_scans;
 };
+
+// Rows [first, end) in steps, as one thread's share.
+__device__ __forceinline__ CeScan ce_scan_rows(const CeRows& a, int64_t first, int64_t end,
+                                               int64_t step) {
+    CeScan s{0., 0.f};
+    for (int64_t i = first; i < end; i += step) {
+        if (a.targets[i] == a.ignored) continue;
+        s.n += 1.;
+        if (a.reduction == kCeNone && finite_f(a.dloss[i])) s.top = fmaxf(s.top, fabsf(a.dloss[i]));
+    }
+    return s;
+}
 
 // c_i times the number that brings the largest gradient that is to be expected,
 // (1 - smoothing) max |c| at a target of no probability, to 2^13.  float16 then
@@ -387,11 +408,16 @@ struct CeFactor {
                                          float* top_of) {
         double n = 0.;
         float top = 0.f;
-        for (int64_t i = threadIdx.x; i < a.rows; i += blockDim.x) {
-            if (a.targets[i] == a.ignored) continue;
-            n += 1.;
-            if (!plain && a.reduction == kCeNone && finite_f(a.dloss[i]))
-                top = fmaxf(top, fabsf(a.dloss[i]));
+        // A sum's factors, and those of a float32 g, take nothing from the other rows.
+        if (a.reduction == kCeMean || (a.reduction == kCeNone && !plain)) {
+            if (a.scans == nullptr) {
+                const CeScan s = ce_scan_rows(a, threadIdx.x, a.rows, blockDim.x);
+                n = s.n;
+                top = s.top;
+            } else if ((int)threadIdx.x < a.n_scans) {
+                n = a.scans[threadIdx.x].n;
+                top = a.scans[threadIdx.x].top;
+            }
         }
         one = 0.f;
         if (a.reduction == kCeNone) {
