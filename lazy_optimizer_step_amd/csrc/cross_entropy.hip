@@ -454,7 +454,8 @@ __global__ __launch_bounds__(TL::kThreads)
         sums.template store<BM, TL::WGN>(tile, w, (float*)lds_raw, i0, c.m, w.first_part + part);
     } else {
         CeRowGrads<Tile> grads;
-        grads.init(tile, w, i0, c.m, c.n, e, [&](int64_t i) { return w.coef[i]; });
+        grads.init(tile, w, i0, c.m, c.n, e, [&](int64_t i) { return w.coef[i]; },
+                   [](int64_t) { return 1.f; });
         tile.run((T*)lds_raw, c, i0, t0, t1, 0, c.steps, [&](int64_t t) {
             grads.template store<T, SPLIT, BN, TL::WGN>(tile, w, i0, t * BN, c.n);
         });
@@ -480,11 +481,11 @@ __global__ __launch_bounds__(TL::kThreads)
     // A last, shorter piece of the classes may leave a split nothing to add.
     if (k0 == k1) return;
     tile.run((T*)lds_raw, c, i0, tj, tj + 1, k0, k1, [](int64_t) {});
-    const int e = sc->ek + (SPLIT ? MODE == kCeDx ? sc->ew : sc->ex : 0);
+    const int e = sc->ek + (MODE == kCeDw ? sc->ed : SPLIT ? sc->ew : 0);
     const float mu = sc->mu;
     ce_store_tile<O>(tile, i0, tj * TL::BN, c.m, c.n, w,
                      w.parts == nullptr ? nullptr : w.parts + split * c.m * w.ld,
-                     [&](float v) { return ce_unscale(v, mu, e); });
+                     [&](float v, int power) { return ce_unscale(v, mu, e + power); });
 }
 
 // out = the splits' sums (zeros where there are none), scaled and rounded.  HBM
@@ -492,10 +493,11 @@ __global__ __launch_bounds__(TL::kThreads)
 template <class O>
 __global__ __launch_bounds__(256) void k_ce_gather(const float* parts, int splits, int64_t rows,
                                                    int64_t ld, int64_t cols, const CeScalars* sc,
-                                                   int use_w, int use_x, O* out, int64_t out_ld) {
+                                                   int use_w, int use_d, const int* powers, O* out,
+                                                   int64_t out_ld) {
     const int64_t quads = ld / 4, all = rows * quads;
     const float mu = splits == 0 ? 0.f : sc->mu;
-    const int scale = splits == 0 ? 0 : sc->ek + (use_w ? sc->ew : 0) + (use_x ? sc->ex : 0);
+    const int scale = splits == 0 ? 0 : sc->ek + (use_w ? sc->ew : 0) + (use_d ? sc->ed : 0);
     for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < all;
          q += (int64_t)gridDim.x * 256) {
         const int64_t i = q / quads, j = q % quads * 4;
@@ -515,8 +517,9 @@ __global__ __launch_bounds__(256) void k_ce_gather(const float* parts, int split
                 for (int e = 0; e < 4; ++e) s[e] += (double)p[k][e];
         }
         float v[4];
+        const int by = scale + (powers ? powers[i] : 0);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = ce_unscale((float)s[e], mu, scale);
+        for (int e = 0; e < 4; ++e) v[e] = ce_unscale((float)s[e], mu, by);
         O* const to = out + i * out_ld + j;
         if (j + 4 <= cols) {
             store_v<O, 4>(to, v);
@@ -530,15 +533,16 @@ __global__ __launch_bounds__(256) void k_ce_gather(const float* parts, int split
 
 constexpr int kAmaxParts = 512;
 
-// The largest finite magnitude that each block meets, as its bits.  Row 0 of
+// The largest finite magnitude that each block meets, as its bits in float32.  Row 0 of
 // the grid takes x, but for the rows that are ignored, row 1 W.
-__global__ __launch_bounds__(256) void k_ce_amax(const float* x, int64_t x_ld, int64_t rows,
+template <class S>
+__global__ __launch_bounds__(256) void k_ce_amax(const S* x, int64_t x_ld, int64_t rows,
                                                  const int64_t* targets, int64_t ignored,
-                                                 const float* w, int64_t w_ld, int64_t classes,
+                                                 const S* w, int64_t w_ld, int64_t classes,
                                                  int64_t cols, uint32_t* parts) {
     __shared__ uint32_t lds[4];
     const bool of_w = blockIdx.y == 1;
-    const float* a = of_w ? w : x;
+    const S* a = of_w ? w : x;
     const int64_t ld = of_w ? w_ld : x_ld, n = of_w ? classes : rows;
     uint32_t top = 0;
     auto take = [&](float v) {
@@ -550,14 +554,14 @@ __global__ __launch_bounds__(256) void k_ce_amax(const float* x, int64_t x_ld, i
          q += (int64_t)gridDim.x * 256) {
         const int64_t r = q / chunks, j = q % chunks * 4;
         if (!of_w && targets[r] == ignored) continue;
-        const float* p = a + r * ld + j;
+        const S* p = a + r * ld + j;
         if (j + 4 <= cols) {
             float v[4];
-            load_v<float, 4>(p, v);
+            load_v<S, 4>(p, v);
 #pragma unroll
             for (int e = 0; e < 4; ++e) take(v[e]);
         } else {
-            for (int e = 0; j + e < cols; ++e) take(p[e]);
+            for (int e = 0; j + e < cols; ++e) take((float)p[e]);
         }
     }
 #pragma unroll
@@ -576,16 +580,19 @@ __global__ __launch_bounds__(256) void k_ce_amax(const float* x, int64_t x_ld, i
 // A copy of an operand as the products take it: rows_p rows of cols_p columns
 // (a multiple of 64), zeros beyond the matrix and in rows that do not count.
 // float32: scaled by 2^e and split; `amax` holds the blocks' shares of the
-// largest value, and block 0 leaves e in *exponent.
+// largest value, and block 0 leaves e in *exponent.  With `powers`, a second copy as
+// dW's operand, row i times 2^(e - powers[i]): what float16 takes of it is off by
+// 2^-39 of x's largest value at most, whatever the rows' factors.
 template <class S, class T>
 __global__ __launch_bounds__(256) void k_ce_pack(const S* a, int64_t ld, int64_t rows,
                                                  int64_t cols, int64_t rows_p, int64_t cols_p,
                                                  const int64_t* targets, int64_t ignored,
                                                  const uint32_t* amax, int n_amax, int* exponent,
-                                                 T* out) {
+                                                 T* out, const int* powers, int* exponent2,
+                                                 T* out2) {
     constexpr bool kSplit = std::is_same_v<S, float>;
     int ex = 0;
-    if constexpr (kSplit) {
+    if (kSplit || powers != nullptr) {
         __shared__ uint32_t lds[4];
         uint32_t top = 0;
         for (int k = threadIdx.x; k < n_amax; k += 256) top = amax[k] > top ? amax[k] : top;
@@ -601,7 +608,10 @@ __global__ __launch_bounds__(256) void k_ce_pack(const S* a, int64_t ld, int64_t
             frexpf(__builtin_bit_cast(float, top), &ex);  // |a| < 2^ex
             ex = 15 - ex;
         }
-        if (blockIdx.x == 0 && threadIdx.x == 0) *exponent = ex;
+        if (blockIdx.x == 0 && threadIdx.x == 0) {
+            if (kSplit) *exponent = ex;
+            if (exponent2 != nullptr) *exponent2 = ex;
+        }
     }
     const int64_t chunks = cols_p / 8, all = rows_p * chunks;
     for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < all;
@@ -618,19 +628,33 @@ __global__ __launch_bounds__(256) void k_ce_pack(const S* a, int64_t ld, int64_t
                     if (j + e < cols) v[e] = (float)p[e];
             }
         }
-        if constexpr (kSplit) {
-            float lo[8];
+        if (kSplit && powers == nullptr) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = ldexpf(v[e], ex);
+        }
+        auto put = [&](T* to, const float (&u)[8]) {
+            if constexpr (kSplit) {
+                float lo[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) lo[e] = u[e] - (float)(T)u[e];
+                to += r * 2 * cols_p + j / 32 * 64 + j % 32;
+                store_v<T, 8>(to, u);
+                store_v<T, 8>(to + 32, lo);
+            } else {
+                store_v<T, 8>(to + r * cols_p + j, u);
+            }
+        };
+        if (powers != nullptr) {
+            const int by = ex - powers[r];
+            float u[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                v[e] = ldexpf(v[e], ex);
-                lo[e] = v[e] - (float)(T)v[e];
+                u[e] = ldexpf(v[e], by);
+                if (kSplit) v[e] = ldexpf(v[e], ex);
             }
-            T* to = out + r * 2 * cols_p + j / 32 * 64 + j % 32;
-            store_v<T, 8>(to, v);
-            store_v<T, 8>(to + 32, lo);
-        } else {
-            store_v<T, 8>(out + r * cols_p + j, v);
+            put(out2, u);
         }
+        put(out, v);
     }
 }
 
@@ -748,10 +772,10 @@ __global__ __launch_bounds__(256) void k_ce_scan(CeRows rows, CeScan* scans) {
     scans[blockIdx.x] = s;
 }
 
-// Each row's factor, 0 beyond the last.  One block, or more where the rows have been
+// Each row's factor and power, 0 beyond the last.  One block, or more where the rows have been
 // scanned.
 __global__ __launch_bounds__(1024) void k_ce_coef(CeRows rows, int64_t rows_p, float* coef,
-                                                  CeScalars* scalars) {
+                                                  int* powers, CeScalars* scalars) {
     __shared__ double lds[16];
     __shared__ float top_of[16];
     CeFactor f;
@@ -759,9 +783,12 @@ __global__ __launch_bounds__(1024) void k_ce_coef(CeRows rows, int64_t rows_p, f
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         scalars->ek = f.ek;
         scalars->mu = f.mu;
+        scalars->ed = 0;
     }
-    for (int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x; i < rows_p; i += gridDim.x * 1024)
+    for (int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x; i < rows_p; i += gridDim.x * 1024) {
         coef[i] = i < rows.rows ? f.of(rows, i) : 0.f;
+        if (rows.powers) powers[i] = i < rows.rows ? f.power(rows, i) : 0;
+    }
 }
 
 // Sets kStatusRange for a target that is neither ignored nor a class, and
@@ -882,6 +909,7 @@ struct CeBuffers {
     CeScan* scans;
     uint32_t* amax;
     void* x;            // x's copy
+    void* x2;           // and the one that dW takes where rows have powers
     void* w;            // a piece of W's copy
     // forward
     float2* parts;
@@ -890,7 +918,9 @@ struct CeBuffers {
     float* row_loss;
     // backward
     float* coef;
+    int* powers;
     void* g;
+    void* g2;
     float* dx_parts;
     float* dw_parts;
 };
@@ -993,7 +1023,15 @@ static size_t ce_layout(const CeRun& r, bool backward, char* base, CeBuffers* b)
         b->row_loss = (float*)take((size_t)s.rows * 4);
         return at;
     }
+    // The reduction, which decides whether rows have powers, does not change the size.
     if (!r.direct) b->coef = (float*)take((size_t)s.rows_p * 4);
+    if (s.dtype != SPOPT_DTYPE_BF16 && !(r.direct && s.split)) {
+        b->powers = (int*)take((size_t)s.rows_p * 4);
+        if (r.direct)
+            b->g2 = take((size_t)(s.rows_p * r.piece) * 2);
+        else
+            b->x2 = take((size_t)(s.rows_p * s.cols_p * s.value) * 2);
+    }
     b->g = take((size_t)(s.rows_p * r.piece * s.value) * 2);
     b->dx_parts = (float*)take((size_t)(r.dx.splits * s.rows * s.cols_p) * 4);
     b->dw_parts = (float*)take(
@@ -1088,7 +1126,8 @@ static unsigned ce_grid(int64_t items) {
 // a time without a remainder, else a copy in `to`.
 static int ce_operand(const CeShape& s, const void* a, int64_t ld, int64_t rows, int64_t rows_p,
                       bool copy, const int64_t* targets, int64_t ignored, const uint32_t* amax,
-                      int n_amax, int* exponent, void* to, CeOperand* o, hipStream_t stream) {
+                      int n_amax, int* exponent, void* to, CeOperand* o, hipStream_t stream,
+                      const int* powers = nullptr, int* exponent2 = nullptr, void* to2 = nullptr) {
     if (!copy && !s.split && s.cols % 64 == 0 && ld % 8 == 0 && ld <= (1 << 21) && aligned16(a)) {
         *o = CeOperand{a, ld, rows - 1, s.cols_p};
         return SPOPT_OK;
@@ -1097,31 +1136,37 @@ static int ce_operand(const CeShape& s, const void* a, int64_t ld, int64_t rows,
     if (s.split)
         k_ce_pack<float, _Float16><<<grid, 256, 0, stream>>>(
             (const float*)a, ld, rows, s.cols, rows_p, s.cols_p, targets, ignored, amax, n_amax,
-            exponent, (_Float16*)to);
+            exponent, (_Float16*)to, powers, exponent2, (_Float16*)to2);
     else if (s.dtype == SPOPT_DTYPE_F16)
         k_ce_pack<_Float16, _Float16><<<grid, 256, 0, stream>>>(
-            (const _Float16*)a, ld, rows, s.cols, rows_p, s.cols_p, targets, ignored, nullptr, 0,
-            nullptr, (_Float16*)to);
+            (const _Float16*)a, ld, rows, s.cols, rows_p, s.cols_p, targets, ignored, amax, n_amax,
+            nullptr, (_Float16*)to, powers, exponent2, (_Float16*)to2);
     else
         k_ce_pack<__bf16, __bf16><<<grid, 256, 0, stream>>>(
             (const __bf16*)a, ld, rows, s.cols, rows_p, s.cols_p, targets, ignored, nullptr, 0,
-            nullptr, (__bf16*)to);
+            nullptr, (__bf16*)to, nullptr, nullptr, nullptr);
     SPOPT_LAUNCHED();
     *o = CeOperand{to, s.cols_p * s.value, rows_p - 1, s.cols_p};
     return SPOPT_OK;
 }
 
+// Both operands' largest values where they are split; x's where its rows get powers.
 static int ce_amax(const CeShape& s, const void* x, int64_t x_ld, const int64_t* targets,
-                   int64_t ignored, const void* w, int64_t w_ld, const CeBuffers& b, int* parts,
-                   hipStream_t stream) {
+                   int64_t ignored, const void* w, int64_t w_ld, bool powers, const CeBuffers& b,
+                   int* parts, hipStream_t stream) {
     *parts = 0;
-    if (!s.split) return SPOPT_OK;
-    const int64_t values = (s.classes > s.rows ? s.classes : s.rows) * s.cols;
-    int64_t n = ceil_div(values, 256 * 16);
+    if (!s.split && !powers) return SPOPT_OK;
+    const int64_t most = s.split && s.classes > s.rows ? s.classes : s.rows;
+    int64_t n = ceil_div(most * s.cols, 256 * 16);
     if (n > kAmaxParts) n = kAmaxParts;
-    k_ce_amax<<<dim3((unsigned)n, 2), 256, 0, stream>>>((const float*)x, x_ld, s.rows, targets,
-                                                        ignored, (const float*)w, w_ld, s.classes,
-                                                        s.cols, b.amax);
+    if (s.split)
+        k_ce_amax<<<dim3((unsigned)n, 2), 256, 0, stream>>>(
+            (const float*)x, x_ld, s.rows, targets, ignored, (const float*)w, w_ld, s.classes,
+            s.cols, b.amax);
+    else
+        k_ce_amax<<<dim3((unsigned)n, 1), 256, 0, stream>>>(
+            (const _Float16*)x, x_ld, s.rows, targets, ignored, (const _Float16*)nullptr, 0, 0,
+            s.cols, b.amax);
     SPOPT_LAUNCHED();
     *parts = (int)n;
     return SPOPT_OK;
@@ -1270,7 +1315,8 @@ extern "C" int linear_cross_entropy_forward(const void* x, int64_t x_stride, con
         rc = ce_direct_loss(dtype, r.logits.tile, CeSide{x, x_stride, rows, cols, targets, ignore_index},
                             CeSide{weight, weight_stride, classes, cols, nullptr, 0}, w, s);
     } else {
-        rc = ce_amax(sh, x, x_stride, targets, ignore_index, weight, weight_stride, b, &amax, s);
+        rc = ce_amax(sh, x, x_stride, targets, ignore_index, weight, weight_stride, false, b, &amax,
+                     s);
         c.m = rows;
         c.steps = sh.cols_p / (sh.split ? 32 : 64);
         if (!rc)
@@ -1328,26 +1374,26 @@ extern "C" int linear_cross_entropy_backward(
     if (dx == nullptr && dweight == nullptr) return SPOPT_OK;
     // The splits' sums of an operand's gradient, to where it belongs.
     auto gather = [&](const float* parts, const CeScalars* sc, int splits, int64_t n, int uw,
-                      int ux, void* out, int64_t ld) {
+                      int ud, const int* powers, void* out, int64_t ld) {
         const unsigned grid = ce_grid(n * (sh.cols_p / 4));
         if (dtype == SPOPT_DTYPE_F32)
-            k_ce_gather<<<grid, 256, 0, s>>>(parts, splits, n, sh.cols_p, cols, sc, uw, ux,
+            k_ce_gather<<<grid, 256, 0, s>>>(parts, splits, n, sh.cols_p, cols, sc, uw, ud, powers,
                                              (float*)out, ld);
         else if (dtype == SPOPT_DTYPE_F16)
-            k_ce_gather<<<grid, 256, 0, s>>>(parts, splits, n, sh.cols_p, cols, sc, uw, ux,
+            k_ce_gather<<<grid, 256, 0, s>>>(parts, splits, n, sh.cols_p, cols, sc, uw, ud, powers,
                                              (_Float16*)out, ld);
         else
-            k_ce_gather<<<grid, 256, 0, s>>>(parts, splits, n, sh.cols_p, cols, sc, uw, ux,
+            k_ce_gather<<<grid, 256, 0, s>>>(parts, splits, n, sh.cols_p, cols, sc, uw, ud, powers,
                                              (__bf16*)out, ld);
     };
     if (rows == 0) {
         if (dweight == nullptr) return SPOPT_OK;
-        gather(nullptr, nullptr, 0, classes, 0, 0, dweight, dweight_stride);
+        gather(nullptr, nullptr, 0, classes, 0, 0, nullptr, dweight, dweight_stride);
         SPOPT_LAUNCHED();
         return SPOPT_OK;
     }
     const CeRun r = ce_run(sh, true);
-    CeBuffers b;
+    CeBuffers b{};
     rc = ce_workspace(what, workspace, workspace_bytes, ce_layout(r, true, (char*)workspace, &b));
     if (rc) return rc;
     if (flags & SPOPT_VALIDATE) {
@@ -1355,7 +1401,9 @@ extern "C" int linear_cross_entropy_backward(
         if (rc) return rc;
     }
     CeRows factors{dloss, targets, ignore_index, rows, classes, reduction,
-                   (float)(1.0 - label_smoothing), nullptr, 0};
+                   (float)(1.0 - label_smoothing), nullptr, 0,
+                   reduction == SPOPT_REDUCE_NONE && b.powers != nullptr};
+    const int* const powers = factors.powers ? b.powers : nullptr;
     rc = ce_scan(&factors, r, b, s);
     if (rc) return rc;
     CeLogits w{};
@@ -1372,10 +1420,12 @@ extern "C" int linear_cross_entropy_backward(
         w.rows_p = rows;
         const CeSide xs{x, x_stride, rows, cols, targets, ignore_index};
         const CeSide ws{weight, weight_stride, classes, cols, nullptr, 0};
-        rc = ce_direct_grad(dtype, r.logits.tile, xs, ws, w, factors, b.scalars, s);
+        w.g2 = b.g2;
+        rc = ce_direct_grad(dtype, r.logits.tile, xs, ws, w, factors, b.scalars, b.powers, s);
         if (rc) return rc;
         CeBoth both{};
-        both.g = CeSide{b.g, r.piece, rows, classes, nullptr, 0};
+        both.g = both.g2 = CeSide{b.g, r.piece, rows, classes, nullptr, 0};
+        if (powers != nullptr) both.g2.base = b.g2;
         both.w = ws;
         both.x = xs;
         both.rows = rows;
@@ -1394,31 +1444,36 @@ extern "C" int linear_cross_entropy_backward(
         const int64_t most = tiles * across * r.dw.splits / 2048;
         both.dw_group = (int)(most < 1 ? 1 : most > tiles ? tiles : most);
         if (dweight != nullptr) both.dw_blocks = ceil_div(tiles, both.dw_group) * across;
-        both.dx = CeResult{r.dx.splits > 1 ? b.dx_parts : nullptr, sh.cols_p, 0, dx, dx_stride};
+        both.dx = CeResult{r.dx.splits > 1 ? b.dx_parts : nullptr, sh.cols_p, 0, dx, dx_stride,
+                           powers};
         both.dw = CeResult{r.dw.splits > 1 ? b.dw_parts : nullptr, sh.cols_p, 0, dweight,
-                           dweight_stride};
+                           dweight_stride, nullptr};
         rc = ce_direct_products(dtype, both, s);
         if (rc) return rc;
         if (dx != nullptr && r.dx.splits > 1)
-            gather(b.dx_parts, b.scalars, r.dx.splits, rows, 0, 0, dx, dx_stride);
+            gather(b.dx_parts, b.scalars, r.dx.splits, rows, 0, 0, powers, dx, dx_stride);
         if (dweight != nullptr && r.dw.splits > 1)
-            gather(b.dw_parts, b.scalars, r.dw.splits, classes, 0, 0, dweight, dweight_stride);
+            gather(b.dw_parts, b.scalars, r.dw.splits, classes, 0, 0, nullptr, dweight,
+                   dweight_stride);
         SPOPT_LAUNCHED();
         return SPOPT_OK;
     }
     int amax = 0;
-    rc = ce_amax(sh, x, x_stride, targets, ignore_index, weight, weight_stride, b, &amax, s);
+    rc = ce_amax(sh, x, x_stride, targets, ignore_index, weight, weight_stride, powers != nullptr, b,
+                 &amax, s);
     if (rc) return rc;
     const int64_t coefs = factors.scans == nullptr ? 1 : ceil_div(sh.rows_p, 4096);
     k_ce_coef<<<(unsigned)(coefs < 1024 ? coefs : 1024), 1024, 0, s>>>(factors, sh.rows_p, b.coef,
-                                                                       b.scalars);
+                                                                       b.powers, b.scalars);
     SPOPT_LAUNCHED();
     // x is copied for its rows that are ignored: they may hold anything, and meet
     // g's zeros in dW.
     CeOperand xo{}, wo{}, g{};
     rc = ce_operand(sh, x, x_stride, rows, sh.rows_p, true, targets, ignore_index, b.amax, amax,
-                    &b.scalars->ex, b.x, &xo, s);
+                    &b.scalars->ex, b.x, &xo, s, powers, &b.scalars->ed, b.x2);
     if (rc) return rc;
+    CeOperand xd = xo;
+    if (powers != nullptr) xd.base = b.x2;
     const int64_t inner = sh.split ? 32 : 64;
     for (int64_t v = 0; v < classes; v += r.piece) {
         const int64_t n = classes - v < r.piece ? classes - v : r.piece;
@@ -1450,13 +1505,14 @@ extern "C" int linear_cross_entropy_backward(
             o.out_ld = dx_stride;
             o.ld = sh.cols_p;
             o.add = v > 0;
+            o.powers = powers;
             o.parts = r.dx.splits == 1 && r.piece >= classes ? nullptr : b.dx_parts;
             rc = ce_product<kCeDx>(r, r.dx, c, o, b.scalars, s);
             if (rc) return rc;
         }
         if (dweight != nullptr) {
             c.p = g;
-            c.q = xo;
+            c.q = xd;
             c.m = n;
             c.n = cols;
             c.steps = sh.rows_p / inner;
@@ -1464,18 +1520,19 @@ extern "C" int linear_cross_entropy_backward(
             o.out_ld = dweight_stride;
             o.ld = sh.cols_p;
             o.add = 0;
+            o.powers = nullptr;
             o.parts = r.dw.splits == 1 ? nullptr : b.dw_parts;
             rc = ce_product<kCeDw>(r, r.dw, c, o, b.scalars, s);
             if (rc) return rc;
             if (r.dw.splits > 1) {
-                gather(b.dw_parts, b.scalars, r.dw.splits, n, 0, sh.split, o.out,
+                gather(b.dw_parts, b.scalars, r.dw.splits, n, 0, 1, nullptr, o.out,
                        dweight_stride);
                 SPOPT_LAUNCHED();
             }
         }
     }
     if (dx != nullptr && (r.dx.splits > 1 || r.piece < classes)) {
-        gather(b.dx_parts, b.scalars, r.dx.splits, rows, sh.split, 0, dx, dx_stride);
+        gather(b.dx_parts, b.scalars, r.dx.splits, rows, sh.split, 0, powers, dx, dx_stride);
         SPOPT_LAUNCHED();
     }
     return SPOPT_OK;

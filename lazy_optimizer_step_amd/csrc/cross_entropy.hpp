@@ -33,7 +33,8 @@ __device__ __forceinline__ float16v matrix_32x32x16(bhalf8 a, bhalf8 b, float16v
 // What a call's kernels hand on to the next ones.
 struct CeScalars {
     int ex, ew;  // powers of two in front of the operands x and W (float32)
-    int ek;      // g is times 2^ek / mu
+    int ed;      // and of x as dW's operand
+    int ek;      // g is times 2^ek / mu, and a power of two of each row (CeRows::powers)
     float mu;
 };
 
@@ -53,6 +54,7 @@ struct CeLogits {
     const float* lse;
     const float* coef;   // [row] c_i 2^ek / mu
     void* g;             // [row][ldg]
+    void* g2;            // the same without the rows' powers (CeRowGrads with TWO)
     int64_t ldg, rows_p, cols_p;  // g's extent, zeros beyond the matrix
 };
 
@@ -220,15 +222,17 @@ struct CeRowSums {
 // bits = c lse rounded, times a factor that takes the rounding back.  A value costs
 // a fused multiply-add, an exponential (at a quarter of the rate), a product and a
 // select.
-template <class Tile>
+// TWO: g2 as well, for which down_of(i) takes a row's power back.
+template <class Tile, bool TWO = false>
 struct CeRowGrads {
-    float coef[Tile::FM], bits[Tile::FM], factor[Tile::FM];
+    float coef[Tile::FM], bits[Tile::FM], factor[Tile::FM], down[TWO ? Tile::FM : 1];
     int target[Tile::FM];
     float to_bits;
 
-    template <class C>
+    template <class C, class D>
     __device__ __forceinline__ void init(const Tile& tile, const CeLogits& w, int64_t i0,
-                                         int64_t m, int64_t n, int exponent, C coef_of) {
+                                         int64_t m, int64_t n, int exponent, C coef_of,
+                                         D down_of) {
         to_bits = ce_logit_scale(exponent) * kLog2e;
 #pragma unroll
         for (int x = 0; x < Tile::FM; ++x) {
@@ -238,6 +242,7 @@ struct CeRowGrads {
             const float lse = row ? w.lse[i] : 0.f;
             target[x] = t >= 0 && t < n ? (int)t : -1;
             coef[x] = row ? coef_of(i) : 0.f;
+            if constexpr (TWO) down[x] = row ? down_of(i) : 0.f;
             bits[x] = lse * kLog2e;
             factor[x] = coef[x] * __builtin_amdgcn_exp2f(-__builtin_fmaf(lse, kLog2e, -bits[x]));
             // Rows that do not count may have any lse.
@@ -296,6 +301,11 @@ struct CeRowGrads {
                     store_v<T, V>(to + 32, lo);
                 } else {
                     store_v<T, V>(g + i * w.ldg + j0 + j, v);
+                    if constexpr (TWO) {
+#pragma unroll
+                        for (int e = 0; e < V; ++e) v[e] *= down[x];
+                        store_v<T, V>((T*)w.g2 + i * w.ldg + j0 + j, v);
+                    }
                 }
             }
         }
@@ -310,6 +320,7 @@ struct CeResult {
     int add;
     void* out;
     int64_t out_ld;
+    const int* powers;  // of each row, or NULL
 };
 
 template <class O, class Tile, class S>
@@ -331,8 +342,9 @@ __device__ __forceinline__ void ce_store_tile(Tile& tile, int64_t i0, int64_t j0
                 continue;
             }
             float v[4];
+            const int power = w.powers ? w.powers[i] : 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = scale(tile.at(x, y, e));
+            for (int e = 0; e < 4; ++e) v[e] = scale(tile.at(x, y, e), power);
             O* const to = (O*)w.out + i * w.out_ld + j;
             if (j + 4 <= n) {
                 store_v<O, 4>(to, v);
@@ -378,6 +390,7 @@ struct CeRows {
     float on;  // 1 - smoothing
     const CeScan* scans;  // or NULL: each block goes over the rows itself
     int n_scans;
+    bool powers;  // each row of g is brought to the largest's binade by a power of its own
 };
 
 // Rows [first, end) in steps, as one thread's share.
@@ -399,9 +412,15 @@ __device__ __forceinline__ CeScan ce_scan_rows(const CeRows& a, int64_t first, i
 // rounding takes least of them.  8192 x 4096 x 131072 bfloat16, errors of dx and dW
 // (norm of the difference over norm): 1.7e-3, which is the results' own rounding;
 // with a power of two in front 1.8e-3 to 2.5e-3, by where c's mantissa lies.
+//
+// Where every row has a factor of its own and g is held in float16 (one or two), a row
+// whose factor is small beside the largest would lose what its classes of small
+// probability add up to.  So its g has a power of two more, which its row of dx is
+// brought back by; dW sums over rows, so that there x's rows have the opposite power,
+// or (direct) g is stored a second time without it.
 struct CeFactor {
     float one, inv;
-    int ek;
+    int ek, e0;  // |c| < 2^e0
     float mu;
     // By all threads of a block.  `plain`: the factors as they are, for a float32 g.
     __device__ __forceinline__ void init(const CeRows& a, bool plain, double* lds,
@@ -435,20 +454,30 @@ struct CeFactor {
                 one = (float)((double)one / fmax(ce_block_sum(n, lds), 1.));
             top = fabsf(one);
         }
-        ek = 0;
+        ek = e0 = 0;
         mu = inv = 1.f;
         if (!plain && top > 0.f && finite_f(top)) {
             // Where 1 - smoothing is small, what is expected is not the largest.
             mu = frexpf(top * fmaxf(a.on, 0.5f), &ek);
             inv = 1.f / mu;
             ek = 13 - ek;
+            frexpf(top, &e0);
         }
+    }
+    // The power of two of row i beyond 2^ek.
+    __device__ __forceinline__ int power(const CeRows& a, int64_t i) const {
+        if (!a.powers || a.targets[i] == a.ignored) return 0;
+        const float c = a.dloss[i];
+        if (c == 0.f || !finite_f(c)) return 0;
+        int e;
+        frexpf(c, &e);
+        return e0 - e;
     }
     __device__ __forceinline__ float of(const CeRows& a, int64_t i) const {
         const int64_t t = a.targets[i];
         if (t == a.ignored) return 0.f;
         if (t < 0 || t >= a.classes) return NAN;
-        return ldexpf((a.reduction == kCeNone ? a.dloss[i] : one) * inv, ek);
+        return ldexpf(a.reduction == kCeNone ? a.dloss[i] : one, ek + power(a, i)) * inv;
     }
 };
 
@@ -469,6 +498,7 @@ struct CeSide {
 // The two products of the gradients: tiles of dx come first, then those of dW.
 struct CeBoth {
     CeSide g, w, x;
+    CeSide g2;  // dW's g
     CeResult dx, dw;
     int64_t rows, cols, classes;
     int64_t dx_blocks, dw_blocks;  // of each split; 0 where not wanted
@@ -482,7 +512,7 @@ struct CeBoth {
 int ce_direct_loss(int32_t dtype, int tile, const CeSide& x, const CeSide& w, const CeLogits& l,
                    hipStream_t s);
 int ce_direct_grad(int32_t dtype, int tile, const CeSide& x, const CeSide& w, const CeLogits& l,
-                   const CeRows& rows, CeScalars* scalars, hipStream_t s);
+                   const CeRows& rows, CeScalars* scalars, int* powers, hipStream_t s);
 int ce_direct_products(int32_t dtype, const CeBoth& b, hipStream_t s);
 
 }  // namespace spopt

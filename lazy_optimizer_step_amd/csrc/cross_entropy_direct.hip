@@ -238,7 +238,8 @@ struct CeDirect {
 
 template <class T, int MODE, int BM>
 __global__ __launch_bounds__(256) void k_ced_logits(CeSide x, CeSide w, CeLogits l, int64_t tn,
-                                                    int64_t tm, CeRows rows, CeScalars* scalars) {
+                                                    int64_t tm, CeRows rows, CeScalars* scalars,
+                                                    int* powers) {
     typedef CeDirect<T, false, false, BM> Tile;
     __shared__ __align__(16) char lds[Tile::kBytes];
     int64_t ti, tj;
@@ -259,9 +260,20 @@ __global__ __launch_bounds__(256) void k_ced_logits(CeSide x, CeSide w, CeLogits
             scalars->ek = f.ek;
             scalars->mu = f.mu;
         }
-        CeRowGrads<Tile> grads;
-        grads.init(tile, l, i0, x.rows, w.rows, 0, [&](int64_t i) { return f.of(rows, i); });
-        grads.template store<T, false, 64, Tile::WGN>(tile, l, i0, j0, w.rows);
+        auto store = [&](auto& grads) {
+            grads.init(tile, l, i0, x.rows, w.rows, 0, [&](int64_t i) { return f.of(rows, i); },
+                       [&](int64_t i) { return ldexpf(1.f, -f.power(rows, i)); });
+            grads.template store<T, false, 64, Tile::WGN>(tile, l, i0, j0, w.rows);
+        };
+        if (std::is_same_v<T, _Float16> && rows.powers) {
+            const int64_t i = i0 + threadIdx.x;
+            if (tj == 0 && threadIdx.x < BM && i < x.rows) powers[i] = f.power(rows, i);
+            CeRowGrads<Tile, true> grads;
+            store(grads);
+        } else {
+            CeRowGrads<Tile> grads;
+            store(grads);
+        }
     }
 }
 
@@ -284,7 +296,7 @@ __device__ __forceinline__ void ced_product(char* lds, const CeSide& p, const Ce
              (split + 1) * steps / splits, [&](int g) {
                  ce_store_tile<T>(tile, i0 + g * BM, j0, m, n, w,
                                   w.parts ? w.parts + split * m * w.ld : nullptr,
-                                  [&](float v) { return ce_unscale(v, mu, e); });
+                                  [&](float v, int power) { return ce_unscale(v, mu, e + power); });
              });
 }
 
@@ -299,7 +311,7 @@ __global__ __launch_bounds__(256) void k_ced_products(CeBoth b) {
         ced_product<T, false, BM_DX>(lds, b.g, b.w, b.dx, dw_first ? at - dw : at, b.dx_blocks,
                                      1, b.dx_splits, b.rows, b.cols, b.classes, b.scalars);
     else
-        ced_product<T, true, BM_DW>(lds, b.g, b.x, b.dw, dw_first ? at : at - dx, b.dw_blocks,
+        ced_product<T, true, BM_DW>(lds, b.g2, b.x, b.dw, dw_first ? at : at - dx, b.dw_blocks,
                                     b.dw_group, b.dw_splits, b.classes, b.cols, b.rows, b.scalars);
 }
 
@@ -332,18 +344,19 @@ int ce_direct_loss(int32_t dtype, int tile, const CeSide& x, const CeSide& w, co
         ced_rows(tile, [&](auto bm) {
             const int64_t tm = ceil_div(x.rows, bm.value), tn = ceil_div(w.rows, 64);
             k_ced_logits<decltype(t), kCeLoss, bm.value>
-                <<<(unsigned)(tm * tn), 256, 0, s>>>(x, w, l, tn, tm, CeRows{}, nullptr);
+                <<<(unsigned)(tm * tn), 256, 0, s>>>(x, w, l, tn, tm, CeRows{}, nullptr, nullptr);
         });
     });
 }
 
 int ce_direct_grad(int32_t dtype, int tile, const CeSide& x, const CeSide& w,
-                   const CeLogits& l, const CeRows& rows, CeScalars* scalars, hipStream_t s) {
+                   const CeLogits& l, const CeRows& rows, CeScalars* scalars, int* powers,
+                   hipStream_t s) {
     return ced_types(dtype, [&](auto t) {
         ced_rows(tile, [&](auto bm) {
             const int64_t tm = ceil_div(x.rows, bm.value), tn = ceil_div(w.rows, 64);
             k_ced_logits<decltype(t), kCeGrad, bm.value>
-                <<<(unsigned)(tm * tn), 256, 0, s>>>(x, w, l, tn, tm, rows, scalars);
+                <<<(unsigned)(tm * tn), 256, 0, s>>>(x, w, l, tn, tm, rows, scalars, powers);
         });
     });
 }
