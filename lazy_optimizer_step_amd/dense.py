@@ -304,32 +304,45 @@ class Dropout(torch.nn.Module):
     """Dropout of probability ``p`` in training, forward and backward in the library's kernels;
     ``forward(x, residual)`` adds the residual stream in the same pass.
 
-    Each training pass takes the next offset under ``seed``: two modules need two seeds.  The
-    seed is an int, or a device int64 tensor of one value, read when the kernel runs: a pass
-    captured into a graph replays its offset, so change the tensor between replays.  ``offset``
-    is part of the state dict.
+    Each training pass takes the next offset under ``seed``: modules of one seed have the same
+    masks.  The seed is an int, or a device int64 tensor of one value, read when the kernel
+    runs: a pass captured into a graph replays its offset, so change the tensor between
+    replays.  None draws one from torch's default generator (``torch.manual_seed``) at the
+    first training pass, so that modules that are copied before it differ too.  Seed and
+    ``offset`` are part of the state dict.
 
     ``forward(x, residual, offset=k)`` takes offset k and leaves the count as it is: for a pass
     that is run again for its gradients (activation checkpointing), which needs the first
     run's mask."""
 
-    def __init__(self, p: float, seed=0):
+    def __init__(self, p: float, seed=None):
         super().__init__()
         if not 0.0 <= p <= 1.0:
             raise ValueError(f"p must lie in [0, 1], got {p}")
         self.p, self.seed, self.offset = p, seed, 0
 
     def get_extra_state(self):
-        return {"offset": self.offset}
+        seed = self.seed.clone() if isinstance(self.seed, torch.Tensor) else self.seed
+        return {"offset": self.offset, "seed": seed}
 
     def set_extra_state(self, state):
         self.offset = state["offset"]
+        seed = state.get("seed")
+        if seed is None:
+            return
+        if isinstance(self.seed, torch.Tensor):
+            # In place: a captured graph reads it there.
+            self.seed.copy_(torch.as_tensor(seed))
+        else:
+            self.seed = int(seed)
 
     def forward(self, x: torch.Tensor, residual=None, *, offset=None) -> torch.Tensor:
         if not self.training:
             return x if residual is None else x + residual
         if offset is None:
             offset, self.offset = self.offset, self.offset + 1
+        if self.seed is None:
+            self.seed = int(torch.randint(1 << 62, (), device="cpu"))
         return _Dropout.apply(x, residual, self.p, self.seed, offset)
 
 
