@@ -313,7 +313,8 @@ class Dropout(torch.nn.Module):
 
     ``forward(x, residual, offset=k)`` takes offset k and leaves the count as it is: for a pass
     that is run again for its gradients (activation checkpointing), which needs the first
-    run's mask."""
+    run's mask.  Inside a backward pass, where such a run takes place, a training pass without
+    ``offset`` is refused: it would take another mask."""
 
     def __init__(self, p: float, seed=None):
         super().__init__()
@@ -340,6 +341,10 @@ class Dropout(torch.nn.Module):
         if not self.training:
             return x if residual is None else x + residual
         if offset is None:
+            if torch._C._current_graph_task_id() != -1:
+                raise RuntimeError("Dropout is run again inside a backward pass (activation "
+                                   "checkpointing): it needs the first run's mask, so give both "
+                                   "runs the same offset, forward(x, offset=...)")
             offset, self.offset = self.offset, self.offset + 1
         if self.seed is None:
             self.seed = int(torch.randint(1 << 62, (), device="cpu"))

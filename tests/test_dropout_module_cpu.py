@@ -1,4 +1,5 @@
 """Dropout's module without a GPU."""
+import pytest
 import torch
 
 import lazy_optimizer_step_amd as L
@@ -23,3 +24,29 @@ def test_no_seed_until_the_first_training_pass():
     x = torch.ones(3)
     assert m.eval()(x) is x and m.seed is None
     assert torch.equal(before, torch.get_rng_state())
+
+
+class _Again(torch.autograd.Function):
+    """What activation checkpointing does: the pass is run in the backward pass."""
+    @staticmethod
+    def forward(ctx, x, run):
+        ctx.run = run
+        return x.clone()
+
+    @staticmethod
+    def backward(ctx, dy):
+        ctx.run()
+        return dy, None
+
+
+def test_a_run_inside_a_backward_pass_needs_its_offset():
+    m = L.Dropout(0.5, seed=1)
+    x = torch.ones(3, requires_grad=True)
+    with pytest.raises(RuntimeError, match="offset"):
+        _Again.apply(x, lambda: m(x)).sum().backward()
+    assert m.offset == 0
+    # with one, it is the kernels' call that a CPU tensor stops
+    with pytest.raises(ValueError, match="ROCm"):
+        _Again.apply(x, lambda: m(x, offset=3)).sum().backward()
+    m.eval()
+    _Again.apply(x, lambda: m(x)).sum().backward()
