@@ -24,6 +24,16 @@ _DTYPES = {torch.float32: _lib.DTYPE_F32, torch.bfloat16: _lib.DTYPE_BF16,
            torch.float16: _lib.DTYPE_F16}
 
 
+def _as_x(t, name, x):
+    """t has x's shape and type and lies beside it."""
+    if t.shape != x.shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, x {tuple(x.shape)}")
+    if t.dtype != x.dtype:
+        raise TypeError(f"{name} must be {x.dtype}, got {t.dtype}")
+    if t.device != x.device:
+        raise ValueError(f"{name} is on {t.device}, x on {x.device}")
+
+
 def _rows(t, name, like=None):
     """(rows, cols, row stride) of a device tensor whose last axis holds adjacent values and
     whose leading axes collapse into evenly spaced rows; never a copy."""
@@ -31,12 +41,7 @@ def _rows(t, name, like=None):
         raise TypeError(f"{name} must be a torch.Tensor")
     shape = t.shape
     if like is not None:
-        if shape != like.shape:
-            raise ValueError(f"{name} has shape {tuple(shape)}, x {tuple(like.shape)}")
-        if t.dtype != like.dtype:
-            raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-        if t.device != like.device:
-            raise ValueError(f"{name} is on {t.device}, x on {like.device}")
+        _as_x(t, name, like)
     else:
         if t.dtype not in _DTYPES:
             raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
@@ -302,7 +307,7 @@ class _Dropout(torch.autograd.Function):
 
 class Dropout(torch.nn.Module):
     """Dropout of probability ``p`` in training, forward and backward in the library's kernels;
-    ``forward(x, residual)`` adds the residual stream in the same pass.
+    ``forward(x, residual)`` adds the residual stream, of x's shape and type, in the same pass.
 
     Each training pass takes the next offset under ``seed``: modules of one seed have the same
     masks.  The seed is an int, or a device int64 tensor of one value, read when the kernel
@@ -339,7 +344,10 @@ class Dropout(torch.nn.Module):
 
     def forward(self, x: torch.Tensor, residual=None, *, offset=None) -> torch.Tensor:
         if not self.training:
-            return x if residual is None else x + residual
+            if residual is None:
+                return x
+            _as_x(residual, "residual", x)
+            return x + residual
         if offset is None:
             if torch._C._current_graph_task_id() != -1:
                 raise RuntimeError("Dropout is run again inside a backward pass (activation "

@@ -50,3 +50,13 @@ def test_a_run_inside_a_backward_pass_needs_its_offset():
         _Again.apply(x, lambda: m(x, offset=3)).sum().backward()
     m.eval()
     _Again.apply(x, lambda: m(x)).sum().backward()
+
+
+def test_evaluation_takes_the_residuals_that_training_takes():
+    m = L.Dropout(0.5, seed=1).eval()
+    x = torch.ones(2, 3)
+    assert torch.equal(m(x, 2 * x), 3 * x)
+    with pytest.raises(ValueError, match="residual has shape"):
+        m(x, torch.ones(3))
+    with pytest.raises(TypeError, match="residual must be"):
+        m(x, x.double())
