@@ -178,9 +178,12 @@ class LinearCrossEntropy(torch.nn.Module):
     """The last layer and its loss: softmax cross entropy of hidden states of ``dim`` values
     against ``classes`` rows, the logits never stored.
 
-    weight: the table to use, (classes, dim) (shared, not copied), else one of its own,
-    N(0, 1 / dim).  forward(x, targets) gives the loss: x of the table's type, (..., dim);
-    targets int64 of x's leading shape.
+    weight: the table to use, (classes, dim) (shared, not copied): a parameter, or a tensor that
+    requires its gradient, which is dense; else one of its own, N(0, 1 / dim).  A table that is to
+    stay as it is comes as ``torch.nn.Parameter(weight, requires_grad=False)``: a plain tensor, such
+    as a SparseEmbedding's weight, whose step takes lookups' rows and no dense gradient, is refused.
+    forward(x, targets) gives the loss: x of the table's type, (..., dim); targets int64 of x's
+    leading shape.
 
     Before a backward pass is captured into a graph, let go of the losses of eager passes over
     the same parameters: while one lives, torch adds the parameters' gradients up on the stream
@@ -197,6 +200,10 @@ class LinearCrossEntropy(torch.nn.Module):
                                         / dim ** 0.5)
         if tuple(weight.shape) != (classes, dim):
             raise ValueError(f"weight has shape {tuple(weight.shape)}, needs ({classes}, {dim})")
+        if not (weight.requires_grad or isinstance(weight, torch.nn.Parameter)):
+            raise ValueError("weight is a plain tensor, which would get no gradient: pass a "
+                             "torch.nn.Parameter, with requires_grad=False for a table that stays "
+                             "as it is")
         self.weight = weight
         self.reduction, self.ignore_index = reduction, ignore_index
         self.label_smoothing = label_smoothing
