@@ -41,8 +41,8 @@ def batches(rows: int, classes: int, bags: int, bag: int, seed: int):
 
 
 def train(steps: int = 200, rows: int = 100_000, dim: int = 128, classes: int = 40,
-          bags: int = 512, bag: int = 16, dropout: float = 0.0, seed: int = 0,
-          log=None) -> list[float]:
+          bags: int = 512, bag: int = 16, seed: int = 0, log=None,
+          dropout: float = 0.0) -> list[float]:
     """Trains for `steps` batches; returns the losses."""
     torch.manual_seed(seed)
     table = SparseEmbedding(rows, dim, lr=1e-2, mode="lazy", init_std=0.05)
