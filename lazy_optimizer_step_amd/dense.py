@@ -26,12 +26,23 @@ _DTYPES = {torch.float32: _lib.DTYPE_F32, torch.bfloat16: _lib.DTYPE_BF16,
 
 def _as_x(t, name, x):
     """t has x's shape and type and lies beside it."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
     if t.shape != x.shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, x {tuple(x.shape)}")
     if t.dtype != x.dtype:
         raise TypeError(f"{name} must be {x.dtype}, got {t.dtype}")
     if t.device != x.device:
         raise ValueError(f"{name} is on {t.device}, x on {x.device}")
+
+
+def _apart(t, name, *others):
+    """An output t does not begin where one of others, (tensor, name), does."""
+    if t is None or t.numel() == 0:
+        return
+    for o, what in others:
+        if o is not None and o.data_ptr() == t.data_ptr() and o.numel():
+            raise ValueError(f"{name} may not be {what}")
 
 
 def _rows(t, name, like=None):
@@ -240,7 +251,7 @@ def dropout_forward(x: torch.Tensor, p: float, seed, *, offset: int = 0, residua
     it.  p counts in steps of 2^-16.  x: float32, bfloat16 or float16, its rows evenly spaced;
     residual: as x, or None.  seed: an int, or a device int64 tensor of one value that the
     kernel reads when it runs (a replayed graph then takes what it holds).  out may be x or
-    residual."""
+    residual (with the same row stride)."""
     rows, cols, xs = _rows(x, "x")
     _here(x, "x")
     rs = ys = cols
@@ -248,6 +259,12 @@ def dropout_forward(x: torch.Tensor, p: float, seed, *, offset: int = 0, residua
         _, _, rs = _rows(residual, "residual", x)
     if out is not None:
         _, _, ys = _rows(out, "out", x)
+    if out is not None and rows > 1:
+        # In place, a value has to be written where it was read.
+        if ys != xs:
+            _apart(out, "out with another row stride", (x, "x"))
+        if ys != rs:
+            _apart(out, "out with another row stride", (residual, "residual"))
     seed, d_seed = _seed(seed, x)
     if out is None:
         with _alloc_on(stream):
@@ -267,6 +284,8 @@ def dropout_backward(dy: torch.Tensor, p: float, seed, *, offset: int = 0, out=N
     os_ = cols
     if out is not None:
         _, _, os_ = _rows(out, "out", dy)
+        if os_ != ds and rows > 1:
+            _apart(out, "out with another row stride", (dy, "dy"))
     seed, d_seed = _seed(seed, dy)
     if out is None:
         with _alloc_on(stream):

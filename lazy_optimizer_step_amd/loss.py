@@ -14,7 +14,7 @@ import functools
 import torch
 
 from . import _alloc_on, _flags, _here, _lib, _need, _ptr, _stream, check
-from .dense import _DTYPES, _like, _rows, _spaced
+from .dense import _DTYPES, _apart, _like, _rows, _spaced
 
 _REDUCTIONS = {"none": _lib.REDUCE_NONE, "sum": _lib.REDUCE_SUM, "mean": _lib.REDUCE_MEAN}
 
@@ -92,7 +92,8 @@ def linear_cross_entropy_forward(x: torch.Tensor, weight: torch.Tensor, targets:
     each row's log of its sum of exponentials, as linear_cross_entropy_backward takes it.  x:
     (..., cols) of float32, bfloat16 or float16, its rows evenly spaced; weight: (classes,
     cols) of x's type; targets: int64 of x's leading shape.  Rows whose target is ignore_index
-    do not count: loss and lse are 0 there; with none that counts the loss is 0."""
+    do not count: loss and lse are 0 there; with none that counts the loss is 0.  Outputs and
+    workspace may not overlap one another or an input."""
     rows, cols, xs, classes, ws, how = _inputs(x, weight, targets, reduction)
     shape = x.shape[:-1] if reduction == "none" else ()
     if out is not None:
@@ -100,6 +101,11 @@ def linear_cross_entropy_forward(x: torch.Tensor, weight: torch.Tensor, targets:
     if lse is not None:
         _floats(lse, "lse", x, rows)
     _space(workspace, x)
+    if out is not None or lse is not None or workspace is not None:
+        read = (x, "x"), (weight, "weight"), (targets, "targets")
+        _apart(out, "out", *read, (lse, "lse"))
+        _apart(lse, "lse", *read)
+        _apart(workspace, "workspace", *read, (out, "out"), (lse, "lse"))
     with _alloc_on(stream):
         if out is None:
             out = x.new_empty(shape, dtype=torch.float32)
@@ -122,7 +128,8 @@ def linear_cross_entropy_backward(dloss: torch.Tensor, x: torch.Tensor, weight: 
                                   want_dx=True, want_dweight=True, workspace=None, stream=None,
                                   validate: bool = False):
     """The gradients of linear_cross_entropy_forward: (dx, dweight), None for what is not
-    wanted.  dloss: float32, one value, or one a row for reduction "none"."""
+    wanted.  dloss: float32, one value, or one a row for reduction "none".  Outputs and workspace
+    may not overlap one another or an input."""
     rows, cols, xs, classes, ws, how = _inputs(x, weight, targets, reduction)
     _floats(dloss, "dloss", x, rows if reduction == "none" else 1)
     _floats(lse, "lse", x, rows)
@@ -135,6 +142,11 @@ def linear_cross_entropy_backward(dloss: torch.Tensor, x: torch.Tensor, weight: 
                              f"{tuple(weight.shape)}")
         _, _, dws = _rows(dweight, "dweight")
     _space(workspace, x)
+    if out is not None or dweight is not None or workspace is not None:
+        read = (x, "x"), (weight, "weight"), (targets, "targets"), (dloss, "dloss"), (lse, "lse")
+        _apart(out, "out", *read, (dweight, "dweight"))
+        _apart(dweight, "dweight", *read)
+        _apart(workspace, "workspace", *read, (out, "out"), (dweight, "dweight"))
     with _alloc_on(stream):
         if want_dx and out is None:
             out = _like(x)
