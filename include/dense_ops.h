@@ -223,14 +223,15 @@ SPOPT_API int linear_cross_entropy_forward(const void* x, int64_t x_stride, cons
  *   dweight   classes x cols of `dtype`, with its row stride, or NULL.  Written,
  *             not added to; all zero for rows == 0.
  * None of the outputs may overlap another, an input or the workspace.
- * g is rounded to the operands' type before the products (float32: kept as it is in
- * small calls, else taken as two float16 like the operands), with a factor in front
- * that brings max |c_i| (1 - e) to 2^13; under SPOPT_REDUCE_NONE each row in float16
- * or two has a power of two more, to the same binade.  So g_ij is off by half a step
- * of its type (two float16: 2^-22 of it), and in float16 or two by 2^-38 |c_i| at
- * least: a row gives nothing to classes of less probability than that.  For dweight
- * the powers are taken back from x's rows, c_i x_i then being off by 2^-37 of the
- * largest (small calls in float16: from g, off by 2^-38 of max |c_i|).  Sums are
+ * In small calls g is float32, which the products of 16-bit types take as two values
+ * of the type; in others it is rounded to the operands' type (float32: taken as two
+ * float16, like the operands).  It has a factor in front that brings max |c_i| (1 - e)
+ * to 2^13; under SPOPT_REDUCE_NONE each row in float16 or two has a power of two more,
+ * to the same binade.  So g_ij is off by half a step of its type (two float16: 2^-22
+ * of it, two bfloat16: 2^-16), and in float16 or two by 2^-38 |c_i| at least: a row
+ * gives nothing to classes of less probability than that.  For dweight the powers are
+ * taken back from x's rows, c_i x_i then being off by 2^-37 of the largest (small calls
+ * have none there: g is off by 2^-38 of max |c_i| in two float16).  Sums are
  * float32, rounded once.  g exists for one piece of the classes at a time, of up
  * to 512 MiB (or 2048 classes).  A row whose target is
  * neither a class nor ignore_index makes its row of dx and all of dweight NaN.

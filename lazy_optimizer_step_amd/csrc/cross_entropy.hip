@@ -15,7 +15,7 @@
 //
 // Types.  16-bit operands go to the matrix cores as they are, sums are float32,
 // and g is rounded to the operands' type (cross_entropy.hpp's CeFactor says with
-// what in front).  A float32 operand a becomes two float16, hi = a 2^e rounded and
+// what in front; small calls hold it in float32).  A float32 operand a becomes two float16, hi = a 2^e rounded and
 // lo = a 2^e - hi rounded, e one for the whole operand that brings its largest
 // value to 2^14: 22 bits of each value (fewer of those below 2^-18 of the largest:
 // off by 2^-39 of it at most).  A product is hi hi + hi lo + lo hi, three matrix
@@ -454,8 +454,7 @@ __global__ __launch_bounds__(TL::kThreads)
         sums.template store<BM, TL::WGN>(tile, w, (float*)lds_raw, i0, c.m, w.first_part + part);
     } else {
         CeRowGrads<Tile> grads;
-        grads.init(tile, w, i0, c.m, c.n, e, [&](int64_t i) { return w.coef[i]; },
-                   [](int64_t) { return 1.f; });
+        grads.init(tile, w, i0, c.m, c.n, e, [&](int64_t i) { return w.coef[i]; });
         tile.run((T*)lds_raw, c, i0, t0, t1, 0, c.steps, [&](int64_t t) {
             grads.template store<T, SPLIT, BN, TL::WGN>(tile, w, i0, t * BN, c.n);
         });
@@ -786,8 +785,9 @@ __global__ __launch_bounds__(1024) void k_ce_coef(CeRows rows, int64_t rows_p, f
         scalars->ed = 0;
     }
     for (int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x; i < rows_p; i += gridDim.x * 1024) {
-        coef[i] = i < rows.rows ? f.of(rows, i) : 0.f;
-        if (rows.powers) powers[i] = i < rows.rows ? f.power(rows, i) : 0;
+        const int power = i < rows.rows ? f.power(rows, i) : 0;
+        coef[i] = i < rows.rows ? f.of(rows, i, power) : 0.f;
+        if (rows.powers) powers[i] = power;
     }
 }
 
@@ -920,7 +920,6 @@ struct CeBuffers {
     float* coef;
     int* powers;
     void* g;
-    void* g2;
     float* dx_parts;
     float* dw_parts;
 };
@@ -991,7 +990,7 @@ static CeRun ce_run(const CeShape& s, bool backward) {
     // Grids and g have to fit at once.
     const int64_t blocks = ceil_div(s.rows, 16) * ceil_div(s.classes, 64) +
                            (ceil_div(s.rows, 16) + ceil_div(s.classes, 16)) * ceil_div(s.cols, 64);
-    const bool fits = blocks < (1 << 22) && s.rows_p <= ((int64_t)1 << 29) / (d.piece * 2 * s.value);
+    const bool fits = blocks < (1 << 22) && s.rows_p <= ((int64_t)1 << 29) / (d.piece * 4);
     if (fits && us_d <= 1.1 * us_p) return d;
     for (int64_t v = 0; v < s.classes; v += p.piece) {
         const int64_t n = s.classes - v < p.piece ? s.classes - v : p.piece;
@@ -1027,12 +1026,9 @@ static size_t ce_layout(const CeRun& r, bool backward, char* base, CeBuffers* b)
     if (!r.direct) b->coef = (float*)take((size_t)s.rows_p * 4);
     if (s.dtype != SPOPT_DTYPE_BF16 && !(r.direct && s.split)) {
         b->powers = (int*)take((size_t)s.rows_p * 4);
-        if (r.direct)
-            b->g2 = take((size_t)(s.rows_p * r.piece) * 2);
-        else
-            b->x2 = take((size_t)(s.rows_p * s.cols_p * s.value) * 2);
+        if (!r.direct) b->x2 = take((size_t)(s.rows_p * s.cols_p * s.value) * 2);
     }
-    b->g = take((size_t)(s.rows_p * r.piece * s.value) * 2);
+    b->g = take((size_t)(s.rows_p * r.piece) * (r.direct ? 4 : 2 * s.value));
     b->dx_parts = (float*)take((size_t)(r.dx.splits * s.rows * s.cols_p) * 4);
     b->dw_parts = (float*)take(
         r.dw.splits > 1 ? (size_t)(r.dw.splits * r.piece * s.cols_p) * 4 : 0);
@@ -1312,8 +1308,8 @@ extern "C" int linear_cross_entropy_forward(const void* x, int64_t x_stride, con
     CeProduct c{};
     int amax = 0;
     if (r.direct) {
-        rc = ce_direct_loss(dtype, r.logits.tile, CeSide{x, x_stride, rows, cols, targets, ignore_index},
-                            CeSide{weight, weight_stride, classes, cols, nullptr, 0}, w, s);
+        rc = ce_direct_loss(dtype, r.logits.tile, CeSide{x, x_stride, rows, cols, targets, ignore_index, nullptr},
+                            CeSide{weight, weight_stride, classes, cols, nullptr, 0, nullptr}, w, s);
     } else {
         rc = ce_amax(sh, x, x_stride, targets, ignore_index, weight, weight_stride, false, b, &amax,
                      s);
@@ -1418,14 +1414,12 @@ extern "C" int linear_cross_entropy_backward(
     if (r.direct) {
         w.ldg = w.cols_p = r.piece;
         w.rows_p = rows;
-        const CeSide xs{x, x_stride, rows, cols, targets, ignore_index};
-        const CeSide ws{weight, weight_stride, classes, cols, nullptr, 0};
-        w.g2 = b.g2;
+        const CeSide xs{x, x_stride, rows, cols, targets, ignore_index, nullptr};
+        const CeSide ws{weight, weight_stride, classes, cols, nullptr, 0, nullptr};
         rc = ce_direct_grad(dtype, r.logits.tile, xs, ws, w, factors, b.scalars, b.powers, s);
         if (rc) return rc;
         CeBoth both{};
-        both.g = both.g2 = CeSide{b.g, r.piece, rows, classes, nullptr, 0};
-        if (powers != nullptr) both.g2.base = b.g2;
+        both.g = CeSide{b.g, r.piece, rows, r.piece, nullptr, 0, powers};
         both.w = ws;
         both.x = xs;
         both.rows = rows;

@@ -54,7 +54,6 @@ struct CeLogits {
     const float* lse;
     const float* coef;   // [row] c_i 2^ek / mu
     void* g;             // [row][ldg]
-    void* g2;            // the same without the rows' powers (CeRowGrads with TWO)
     int64_t ldg, rows_p, cols_p;  // g's extent, zeros beyond the matrix
 };
 
@@ -222,17 +221,15 @@ struct CeRowSums {
 // bits = c lse rounded, times a factor that takes the rounding back.  A value costs
 // a fused multiply-add, an exponential (at a quarter of the rate), a product and a
 // select.
-// TWO: g2 as well, for which down_of(i) takes a row's power back.
-template <class Tile, bool TWO = false>
+template <class Tile>
 struct CeRowGrads {
-    float coef[Tile::FM], bits[Tile::FM], factor[Tile::FM], down[TWO ? Tile::FM : 1];
+    float coef[Tile::FM], bits[Tile::FM], factor[Tile::FM];
     int target[Tile::FM];
     float to_bits;
 
-    template <class C, class D>
+    template <class C>
     __device__ __forceinline__ void init(const Tile& tile, const CeLogits& w, int64_t i0,
-                                         int64_t m, int64_t n, int exponent, C coef_of,
-                                         D down_of) {
+                                         int64_t m, int64_t n, int exponent, C coef_of) {
         to_bits = ce_logit_scale(exponent) * kLog2e;
 #pragma unroll
         for (int x = 0; x < Tile::FM; ++x) {
@@ -242,7 +239,6 @@ struct CeRowGrads {
             const float lse = row ? w.lse[i] : 0.f;
             target[x] = t >= 0 && t < n ? (int)t : -1;
             coef[x] = row ? coef_of(i) : 0.f;
-            if constexpr (TWO) down[x] = row ? down_of(i) : 0.f;
             bits[x] = lse * kLog2e;
             factor[x] = coef[x] * __builtin_amdgcn_exp2f(-__builtin_fmaf(lse, kLog2e, -bits[x]));
             // Rows that do not count may have any lse.
@@ -301,11 +297,6 @@ struct CeRowGrads {
                     store_v<T, V>(to + 32, lo);
                 } else {
                     store_v<T, V>(g + i * w.ldg + j0 + j, v);
-                    if constexpr (TWO) {
-#pragma unroll
-                        for (int e = 0; e < V; ++e) v[e] *= down[x];
-                        store_v<T, V>((T*)w.g2 + i * w.ldg + j0 + j, v);
-                    }
                 }
             }
         }
@@ -411,13 +402,15 @@ __device__ __forceinline__ CeScan ce_scan_rows(const CeRows& a, int64_t first, i
 // at the targets, the largest by far, lie at a power of two or just below, where
 // rounding takes least of them.  8192 x 4096 x 131072 bfloat16, errors of dx and dW
 // (norm of the difference over norm): 1.7e-3, which is the results' own rounding;
-// with a power of two in front 1.8e-3 to 2.5e-3, by where c's mantissa lies.
+// with a power of two in front 1.8e-3 to 2.5e-3, by where c's mantissa lies, and where
+// each row has a factor of its own 2.2e-3.  (Two bfloat16 for each of g, as in small
+// calls, would take that off and two thirds more time: 10 n V d operations in place of 6.)
 //
 // Where every row has a factor of its own and g is held in float16 (one or two), a row
 // whose factor is small beside the largest would lose what its classes of small
 // probability add up to.  So its g has a power of two more, which its row of dx is
-// brought back by; dW sums over rows, so that there x's rows have the opposite power,
-// or (direct) g is stored a second time without it.
+// brought back by; dW sums over rows, so that there x's rows have the opposite power.
+// (Direct: g is float32, and gets the power on its way into dx's product alone.)
 struct CeFactor {
     float one, inv;
     int ek, e0;  // |c| < 2^e0
@@ -473,11 +466,12 @@ struct CeFactor {
         frexpf(c, &e);
         return e0 - e;
     }
-    __device__ __forceinline__ float of(const CeRows& a, int64_t i) const {
+    // c_i 2^ek / mu.
+    __device__ __forceinline__ float of(const CeRows& a, int64_t i, int power = 0) const {
         const int64_t t = a.targets[i];
         if (t == a.ignored) return 0.f;
         if (t < 0 || t >= a.classes) return NAN;
-        return ldexpf(a.reduction == kCeNone ? a.dloss[i] : one, ek + power(a, i)) * inv;
+        return ldexpf(a.reduction == kCeNone ? a.dloss[i] : one, ek + power) * inv;
     }
 };
 
@@ -493,12 +487,12 @@ struct CeSide {
     int64_t ld, rows, cols;
     const int64_t* targets;  // or NULL
     int64_t ignored;
+    const int* powers;       // of each row, or NULL
 };
 
 // The two products of the gradients: tiles of dx come first, then those of dW.
 struct CeBoth {
     CeSide g, w, x;
-    CeSide g2;  // dW's g
     CeResult dx, dw;
     int64_t rows, cols, classes;
     int64_t dx_blocks, dw_blocks;  // of each split; 0 where not wanted

@@ -5,30 +5,39 @@
 // A launch costs the host 3.5 us, which is all that a small call takes.  These
 // take two launches forward (the logits' tiles, the join) and two backward (g;
 // both products, and a third where an inner axis is cut), where packed operands
-// take up to five and nine.  Operands go through registers into LDS, four or six
+// take up to five and nine.  Operands go through registers into LDS, three to six
 // stages on their way, in tiles of 64 x 64 or, of few rows, 16 x 64, laid out in LDS
 // as cross_entropy.hip's.  4 x 256 x 1000 float32: 18.7 us forward and 25.9 backward a
 // call, packed 28.9 and 39.1; of the 18.7 the host takes about 13.  6 x 966 x 67682
-// float16 backward 143 us, where one pass over W takes 26: rows at odd addresses
-// (960 columns 131 us), and W read twice.
+// float16 backward 155 us, where one pass over W takes 26: rows at odd addresses, and
+// W read twice.
 #include "cross_entropy.hpp"
 
 namespace spopt {
 
 typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
 
-template <class T, bool TP, bool TQ, int BM_>
+// PAIR: P is g in float32, which is taken as two of T, the rounded value and what that
+// leaves, and multiplied twice: what rounds the gradients is then their own type
+// alone.  Of few rows or classes g rounded once is off by as much again (bfloat16, 2.4e-3
+// against 1.6e-3), and what a row's classes have in common does not leave dx.  Small calls
+// have the time: 300 x 100 x 3001 bfloat16 30.5 -> 31.2 us, 2000 x 256 x 1000 44 -> 47.5,
+// 6 x 966 x 67682 float16 148 -> 155.
+template <class T, bool TP, bool TQ, int BM_, bool PAIR = false>
 struct CeDirect {
     static constexpr int BM = BM_, BN = 64, WGN = BM == 64 ? 2 : 4;  // four waves
     static constexpr int FM = BM / 16 * WGN / 4, FN = 4 / WGN;
-    static constexpr int kAhead = BM == 64 ? 4 : 6;       // stages on their way in registers
+    static constexpr int kAhead = BM == 64 ? PAIR ? 3 : 4 : 6;  // stages on their way in registers
     static constexpr int kRow = TQ || FN % 2 ? 4 : 8;     // adjacent columns of a lane
     static constexpr int E = 16 / (int)sizeof(T);         // values of a chunk
     static constexpr int kInner = 128 / (int)sizeof(T);   // values of the inner axis a stage
-    static constexpr int kSideP = BM * 128, kSideQ = BN * 128;  // bytes of a stage
+    static constexpr int kPlane = BM * 128;               // bytes of a stage
+    static constexpr int kSideP = kPlane * (PAIR ? 2 : 1), kSideQ = BN * 128;
     static constexpr int kBytes = 2 * (kSideP + kSideQ);  // of LDS
     typedef T chunk __attribute__((ext_vector_type(E)));
+    typedef float wide __attribute__((ext_vector_type(E)));
     static_assert(BM == 64 || BM == 16, "two tiles");
+    static_assert(!PAIR || sizeof(T) == 2, "float32 holds g");
 
     // Row v of a turned side has its 16 columns from 16 u on at u ^ turn(v).
     template <int B>
@@ -37,15 +46,18 @@ struct CeDirect {
     }
 
     // A side's loads: 8 B chunks a stage.
-    template <bool TURN, int B>
+    template <bool TURN, int B, bool WIDE = false>
     struct Feed {
         static constexpr int kLoads = B == 64 ? 2 : 1;
-        const T* base;
+        typedef std::conditional_t<WIDE, float, T> S;
+        typedef std::conditional_t<WIDE, wide, chunk> loaded;
+        const S* base;
+        int up[WIDE && !TURN ? kLoads : 1];  // the row's power of two
         const int64_t* targets;
         int64_t ld, rows, cols, ignored, row[kLoads], col;
         int place[kLoads];
         __device__ __forceinline__ void init(const CeSide& s, int64_t first, bool pair) {
-            base = (const T*)s.base;
+            base = (const S*)s.base;
             targets = s.targets;
             ld = s.ld;
             rows = s.rows;
@@ -65,13 +77,15 @@ struct CeDirect {
                     row[l] = first + (pair ? v - in + ((in & 12) >> 2) * 8 + (in >> 4) * 4 + (in & 3)
                                            : v);
                     if (row[l] >= rows || (targets && targets[row[l]] == ignored)) row[l] = -1;
+                    if constexpr (WIDE)
+                        up[l] = s.powers && row[l] >= 0 ? s.powers[row[l]] : 0;
                     col = c * E;
                     place[l] = (v * 8 + (c ^ (v & 7))) * 16;
                 }
             }
         }
         // Chunk l of step k, `shift` columns on (of a turned side).
-        __device__ __forceinline__ chunk load(int64_t k, int l, int64_t shift) const {
+        __device__ __forceinline__ loaded load(int64_t k, int l, int64_t shift) const {
             int64_t r = row[l], c = TURN ? col + shift : col;
             bool in;
             if constexpr (TURN) {
@@ -81,30 +95,50 @@ struct CeDirect {
                 c += k * kInner;
                 in = r >= 0;
             }
-            chunk v = {};
+            loaded v = {};
             if (!in || c >= cols) return v;
-            const T* p = base + r * ld;
-            if (cols < E) {
+            const S* p = base + r * ld;
+            if constexpr (WIDE) {
+                return *(const loaded*)(p + c);  // g's rows are padded to whole chunks
+            } else {
+                if (cols < E) {
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    if (c + e < cols) v[e] = p[c + e];
+                    for (int e = 0; e < E; ++e)
+                        if (c + e < cols) v[e] = p[c + e];
+                    return v;
+                }
+                // The chunk at a row's end is moved back to end with it, and its values
+                // forward again: loads of single values would keep the whole wave.
+                const int64_t at = c + E <= cols ? c : cols - E;
+                v = *(const typename Pack<T, E>::type*)(p + at);
+                const int skip = (int)(c - at);
+                if (skip != 0) {
+                    uint4v q = __builtin_bit_cast(uint4v, v);
+                    if (skip & E / 2) q = uint4v{q[2], q[3], 0, 0};
+                    if (skip & E / 4) q = uint4v{q[1], q[2], q[3], 0};
+                    if (E == 8 && skip & 1)
+                        q = uint4v{q[0] >> 16 | q[1] << 16, q[1] >> 16 | q[2] << 16,
+                                   q[2] >> 16 | q[3] << 16, q[3] >> 16};
+                    v = __builtin_bit_cast(chunk, q);
+                }
                 return v;
             }
-            // The chunk at a row's end is moved back to end with it, and its values
-            // forward again: loads of single values would keep the whole wave.
-            const int64_t at = c + E <= cols ? c : cols - E;
-            v = *(const typename Pack<T, E>::type*)(p + at);
-            const int skip = (int)(c - at);
-            if (skip != 0) {
-                uint4v q = __builtin_bit_cast(uint4v, v);
-                if (skip & E / 2) q = uint4v{q[2], q[3], 0, 0};
-                if (skip & E / 4) q = uint4v{q[1], q[2], q[3], 0};
-                if (E == 8 && skip & 1)
-                    q = uint4v{q[0] >> 16 | q[1] << 16, q[1] >> 16 | q[2] << 16,
-                               q[2] >> 16 | q[3] << 16, q[3] >> 16};
-                v = __builtin_bit_cast(chunk, q);
+        }
+        // Chunk l into a stage in LDS.
+        __device__ __forceinline__ void put(char* to, int l, const loaded& v) const {
+            if constexpr (WIDE) {
+                chunk hi, lo;
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const float u = TURN ? v[e] : ldexpf(v[e], up[l]);
+                    hi[e] = (T)u;
+                    lo[e] = (T)(u - (float)hi[e]);
+                }
+                *(chunk*)(to + place[l]) = hi;
+                *(chunk*)(to + kPlane + place[l]) = lo;
+            } else {
+                *(chunk*)(to + place[l]) = v;
             }
-            return v;
         }
     };
 
@@ -152,14 +186,15 @@ struct CeDirect {
     template <class F>
     __device__ __forceinline__ void run(char* lds, const CeSide& p, const CeSide& q, int64_t i0,
                                         int tiles, int64_t j0, int64_t k0, int64_t k1, F done) {
-        typedef Feed<TP, BM> FeedP;
+        typedef Feed<TP, BM, PAIR> FeedP;
         typedef Feed<TQ, BN> FeedQ;
         FeedP fp;
         FeedQ fq;
         fp.init(p, i0, false);
         fq.init(q, j0, kRow == 8);
         const bool with_p = BM == 64 || threadIdx.x < 8 * BM;
-        chunk cp[kAhead][FeedP::kLoads], cq[kAhead][FeedQ::kLoads];
+        typename FeedP::loaded cp[kAhead][FeedP::kLoads];
+        chunk cq[kAhead][FeedQ::kLoads];
         int64_t bk = k0, shift = 0, left = tiles * (k1 - k0);
         if (left <= 0) return;  // the host cuts no axis into more parts than it has steps
         auto bring = [&](int u) {
@@ -187,19 +222,23 @@ struct CeDirect {
                 char* const to = lds + buf * (kSideP + kSideQ);
 #pragma unroll
                 for (int l = 0; l < FeedP::kLoads; ++l)
-                    if (with_p) *(chunk*)(to + fp.place[l]) = cp[u][l];
+                    if (with_p) fp.put(to, l, cp[u][l]);
 #pragma unroll
-                for (int l = 0; l < FeedQ::kLoads; ++l)
-                    *(chunk*)(to + kSideP + fq.place[l]) = cq[u][l];
+                for (int l = 0; l < FeedQ::kLoads; ++l) fq.put(to + kSideP, l, cq[u][l]);
                 bring(u);
                 // One barrier a stage: whoever writes this place next has passed
                 // the other one's, after all reads of this.
                 __syncthreads();
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
-                    chunk a[FM], b[FN];
+                    chunk a[FM], b[FN], less[PAIR ? FM : 1];
 #pragma unroll
                     for (int x = 0; x < FM; ++x) a[x] = operand<TP, BM>(to, wi + x * 16, kk);
+                    if constexpr (PAIR) {
+#pragma unroll
+                        for (int x = 0; x < FM; ++x)
+                            less[x] = operand<TP, BM>(to + kPlane, wi + x * 16, kk);
+                    }
 #pragma unroll
                     for (int y = 0; y < FN; ++y) b[y] = operand<TQ, BN>(to + kSideP, wj + y * 16, kk);
 #pragma unroll
@@ -213,6 +252,8 @@ struct CeDirect {
                                         b[y][e], a[x][e], acc[x][y], 0, 0, 0);
                             } else {
                                 acc[x][y] = matrix_16x16x32(b[y], a[x], acc[x][y]);
+                                if constexpr (PAIR)
+                                    acc[x][y] = matrix_16x16x32(b[y], less[x], acc[x][y]);
                             }
                         }
                 }
@@ -260,20 +301,12 @@ __global__ __launch_bounds__(256) void k_ced_logits(CeSide x, CeSide w, CeLogits
             scalars->ek = f.ek;
             scalars->mu = f.mu;
         }
-        auto store = [&](auto& grads) {
-            grads.init(tile, l, i0, x.rows, w.rows, 0, [&](int64_t i) { return f.of(rows, i); },
-                       [&](int64_t i) { return ldexpf(1.f, -f.power(rows, i)); });
-            grads.template store<T, false, 64, Tile::WGN>(tile, l, i0, j0, w.rows);
-        };
-        if (std::is_same_v<T, _Float16> && rows.powers) {
-            const int64_t i = i0 + threadIdx.x;
-            if (tj == 0 && threadIdx.x < BM && i < x.rows) powers[i] = f.power(rows, i);
-            CeRowGrads<Tile, true> grads;
-            store(grads);
-        } else {
-            CeRowGrads<Tile> grads;
-            store(grads);
-        }
+        // Its rows' powers are the next launch's.
+        const int64_t i = i0 + threadIdx.x;
+        if (rows.powers && tj == 0 && threadIdx.x < BM && i < x.rows) powers[i] = f.power(rows, i);
+        CeRowGrads<Tile> grads;
+        grads.init(tile, l, i0, x.rows, w.rows, 0, [&](int64_t i) { return f.of(rows, i); });
+        grads.template store<float, false, 64, Tile::WGN>(tile, l, i0, j0, w.rows);
     }
 }
 
@@ -284,7 +317,7 @@ __device__ __forceinline__ void ced_product(char* lds, const CeSide& p, const Ce
                                             const CeResult& w, int64_t at, int64_t blocks,
                                             int group, int splits, int64_t m, int64_t n, int64_t k,
                                             const CeScalars* sc) {
-    CeDirect<T, TP, true, BM> tile;
+    CeDirect<T, TP, true, BM, sizeof(T) == 2> tile;
     const int64_t split = at / blocks, t = at % blocks, tn = (n + 63) / 64;
     const int64_t steps = (k + tile.kInner - 1) / tile.kInner;
     const int64_t i0 = t / tn * group * BM, j0 = t % tn * 64;
@@ -300,9 +333,10 @@ __device__ __forceinline__ void ced_product(char* lds, const CeSide& p, const Ce
              });
 }
 
+// Three blocks a CU: 6 x 966 x 67682 float16 155 us, with two 188.
 template <class T, int BM_DX, int BM_DW>
-__global__ __launch_bounds__(256) void k_ced_products(CeBoth b) {
-    __shared__ __align__(16) char lds[CeDirect<T, true, true, 64>::kBytes];
+__global__ __launch_bounds__(256, 3) void k_ced_products(CeBoth b) {
+    __shared__ __align__(16) char lds[CeDirect<T, true, true, 64, sizeof(T) == 2>::kBytes];
     // The product whose blocks take longer begins.
     const int64_t dx = b.dx_blocks * b.dx_splits, dw = b.dw_blocks * b.dw_splits;
     const bool dw_first = b.rows / b.dw_splits > b.classes / b.dx_splits;
@@ -311,7 +345,7 @@ __global__ __launch_bounds__(256) void k_ced_products(CeBoth b) {
         ced_product<T, false, BM_DX>(lds, b.g, b.w, b.dx, dw_first ? at - dw : at, b.dx_blocks,
                                      1, b.dx_splits, b.rows, b.cols, b.classes, b.scalars);
     else
-        ced_product<T, true, BM_DW>(lds, b.g2, b.x, b.dw, dw_first ? at : at - dx, b.dw_blocks,
+        ced_product<T, true, BM_DW>(lds, b.g, b.x, b.dw, dw_first ? at : at - dx, b.dw_blocks,
                                     b.dw_group, b.dw_splits, b.classes, b.cols, b.rows, b.scalars);
 }
 
