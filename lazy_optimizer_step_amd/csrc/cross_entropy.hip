@@ -25,7 +25,7 @@
 // Measured on one MI355X (cards differ by 7%): 4096 x 2048 x 131072 bfloat16 forward
 // 1.79 to 1.94 ms (1.13 to 1.23 PFLOP/s), 8192 x 4096 x 131072 backward 20.7 to 21.9
 // ms (1.20 to 1.28 PFLOP/s; a library product of these sizes 1.31 to 1.50), 8192 x 128
-// x 50021 float32 0.33 to 0.36 and 1.40 to 1.54 ms.
+// x 50021 float32 0.36 to 0.37 and 1.46 to 1.54 ms, bfloat16 0.18 to 0.19 and 0.70.
 #include "cross_entropy.hpp"
 
 namespace spopt {
@@ -427,8 +427,8 @@ using CeTileOf = std::conditional_t<TL::BM == 256, CeWide<T, TP, TQ>, CeTile<T, 
 
 // A block takes one of `parts` parts of the piece's tiles of classes, for one tile
 // of rows: their maxima and sums stay in registers from tile to tile (8192 x 128 x
-// 50021 float32: 345 us, 446 with a block and a place in the workspace for each
-// tile).  Blocks of the same part follow one another, so that an XCD's L2 sees W's
+// 50021 float32: 360 us; sums in float32 345, and then 446 with a block and a place in
+// the workspace for each tile).  Blocks of the same part follow one another, so that an XCD's L2 sees W's
 // rows once.
 template <class T, bool SPLIT, int MODE, class TL>
 __global__ __launch_bounds__(TL::kThreads)
@@ -886,9 +886,11 @@ static CeShape ce_shape(int64_t rows, int64_t cols, int64_t classes, int32_t dty
 
 // Classes at a time.  Forward: copies of W's rows of up to 256 MiB, and grids of
 // up to 2^22 tiles.  Backward: g of up to 512 MiB, or 256 where rows are short and
-// g's traffic bounds the pass, as the last-level cache then keeps much of it (8192
-// x 128 x 50021 float32 1700 against 1450 us, bfloat16 1080 against 731; 4096 x 1024 x
-// 131072 bfloat16 3225 against 4044); for at least 2048 classes.
+// g's traffic bounds the pass, as the last-level cache then keeps much of it (512
+// against 256: 8192 x 128 x 50021 float32 1735 and 1552 us, bfloat16 820 and 709; 2000 x 64
+// x 100000 bfloat16 408 and 290; 8192 x 256 x 50021 bfloat16 1130 and 1103; 384 to 640
+// columns within 6% either way; 2000 x 1024 x 100000 bfloat16 1404 and 1642, 4096 x 1024 x
+// 131072 3692 and 4363); for at least 2048 classes.
 static int64_t ce_piece(const CeShape& s, bool backward) {
     int64_t most = ((int64_t)1 << 28) / (s.cols_p * s.value * 2);
     if (backward) {
@@ -957,10 +959,11 @@ static CePlan ce_direct_plan(const CeShape& s, int64_t m, int64_t n, int64_t k, 
 // any backward pass; both operands' of float32, 12 bytes a value with the pass that
 // finds the largest; of 16 bits, 4 bytes a value of rows that have a remainder);
 // the direct kernels multiply more slowly, those of float32 far more.  Both sides
-// measured at 114 sizes, forward and backward: the estimates choose the slower one
-// at 19 of 228, by 1.03 to 1.24 times.  4 x 256 x 1000 float32: 18.7 against 28.9 us forward
-// and 25.9 against 39.1 backward; 500 x 256 x 100000 float32: 337 against 176 and
-// 934 against 446.
+// measured at 136 sizes, forward and backward: the estimates choose the slower one
+// at 30 of 272, by 1.03 to 1.3 times, and 1.5 to 1.7 backward at 200000 rows and more of 10
+// classes, where a block's time is not what its steps take.  4 x 256 x 1000 float32: 20.7
+// against 31.8 us forward and 24.4 against 43.3 backward; 500 x 256 x 100000 float32: 323
+// against 153 and 1007 against 416.
 static CeRun ce_run(const CeShape& s, bool backward) {
     CeRun d{}, p{};
     d.s = p.s = s;

@@ -90,11 +90,10 @@ __device__ __forceinline__ float ce_logit_scale(int exponent) {
 // whole table of classes, thousands of tiles: a tile's few values are added up in
 // float32, and tiles in double.  (In float32 a class of probability near 1 early in
 // the table leaves the later ones' shares no bits: with 0.999 there and 131072
-// classes in one part, the loss came out 6% low.  It costs 4% of 8192 x 128 x 50021
-// float32.)  The base is the largest logit so far or
-// less than a factor of 2 below it: so the sum is scaled anew only where it at least
-// doubles, and the factors' roundings do not add up either.  Bases are of z / scale,
-// scale a power of two.
+// classes in one part, the loss came out 6% low.  Double costs 4% of 8192 x 128 x
+// 50021 float32.)  The base is the largest logit so far or less than a factor of 2
+// below it: so the sum is scaled anew only where it at least doubles, and the factors'
+// roundings do not add up either.  Bases are of z / scale, scale a power of two.
 template <class Tile>
 struct CeRowSums {
     float top[Tile::FM];

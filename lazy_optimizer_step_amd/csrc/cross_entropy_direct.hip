@@ -7,8 +7,8 @@
 // both products, and a third where an inner axis is cut), where packed operands
 // take up to five and nine.  Operands go through registers into LDS, three to six
 // stages on their way, in tiles of 64 x 64 or, of few rows, 16 x 64, laid out in LDS
-// as cross_entropy.hip's.  4 x 256 x 1000 float32: 18.7 us forward and 25.9 backward a
-// call, packed 28.9 and 39.1; of the 18.7 the host takes about 13.  6 x 966 x 67682
+// as cross_entropy.hip's.  4 x 256 x 1000 float32: 20.7 us forward and 24.4 backward a
+// call, packed 31.8 and 43.3; of the 20.7 the host takes about 13.  6 x 966 x 67682
 // float16 backward 155 us, where one pass over W takes 26: rows at odd addresses, and
 // W read twice.
 #include "cross_entropy.hpp"

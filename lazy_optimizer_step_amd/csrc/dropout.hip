@@ -81,7 +81,9 @@ __global__ __launch_bounds__(256) void k_dropout(const T* x, const T* res, T* y,
     }
 }
 
-// Rows with gaps between them.  Eight values may run over the end of a row.
+// Rows with gaps between them.  Eight values may run over the end of a row, and are
+// then taken one by one: 16384 x 4096 bfloat16 in rows of 4160 46 us (torch's copy of them
+// 45), 4091 columns in rows of 4160 78 (46), 65536 x 125 in rows of 128 23 (9).
 template <class T, bool RES>
 __global__ __launch_bounds__(256) void k_dropout_rows(const T* x, int64_t xs, const T* res,
                                                       int64_t rs, T* y, int64_t ys, int64_t rows,
