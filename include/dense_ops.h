@@ -188,8 +188,8 @@ SPOPT_API int muon_step(void* params, int32_t pdtype, float* buf, const void* g,
 SPOPT_API int linear_cross_entropy_workspace_size(int64_t rows, int64_t cols, int64_t classes,
                                                   int32_t dtype, int32_t backward, size_t* bytes);
 
-/* Which kernels a pass takes at a size, by the sizes alone: what two calls share
- * that give the same bits, and what a measurement of the rule asks for. */
+/* Which kernels a pass takes, which goes by its sizes and type alone: for tests of each
+ * and for measurements of the rule. */
 typedef struct spopt_ce_plan {
     int32_t direct;       /* 1: operands read in place by kernels for small calls; tiles below 16 or 64 */
     int32_t tile_logits;  /* rows of a tile of the logits, */
