@@ -179,8 +179,8 @@ SPOPT_API int muon_step(void* params, int32_t pdtype, float* buf, const void* g,
  * for the pass (backward 0 or 1).  Small calls read their inputs in place.  In
  * others those with cols a multiple of 64, strides multiples of 8 and 16-byte
  * aligned bases are read in place where they are of 16 bits, and the rest (x
- * always in the backward pass, but for bfloat16 with room for two copies) are copied
- * into the workspace, the weight up to 256 MiB (or 2048 rows) at a time.
+ * always in the backward pass, float16 and float32 with room for a second copy) are
+ * copied into the workspace, the weight up to 256 MiB (or 2048 rows) at a time.
  * Errors: SPOPT_EINVAL (NULL, sizes, a stride below cols, types, reduction,
  * label_smoothing outside [0, 1]), SPOPT_EWORKSPACE; rows up to 2^27, cols to
  * 2^20, classes to 2^30, either matrix to 2^36 values.  SPOPT_VALIDATE reads
